@@ -297,6 +297,145 @@ int gdn_inproj_affine4(const gdn_shape *shape, int32_t rows, int32_t hidden, int
                        const uint16_t *biases_tiled, uint16_t *qkv, uint16_t *a, uint16_t *b, void *stream);
 
 /*
+ * Attention layers
+ * ----------------
+ * A hybrid model's other layers are gated full attention over a growing
+ * key-value cache.  The calls below run them beside the mixer's: the same
+ * packed rows, windows, trees and accepted rows, every count read on the
+ * device.  (The engine on the pages keeps its gated attention in qwen35.cu,
+ * cuts decode attention into key chunks at logical positions, and stores e4m3
+ * cache rows with an fp32 scale of amax / 448.)
+ *
+ * The cache is paged.  K and V are [n_pages][hkv][page_size][d] (bf16, or
+ * e4m3 codes with one fp32 scale a row in [n_pages][hkv][page_size]); a
+ * stream's cache row i is row i % page_size of page block_table[s][i /
+ * page_size], block_table [n][max_blocks] int32.  Slot numbers are page *
+ * page_size + row.  page_size is 16, 32, 64, 128 or 256, d is 64, 128 or 256,
+ * and n_pages * hkv * page_size < 2^31 (GDN_EUNSUPPORTED otherwise).  Query
+ * head h reads kv head h / (hq / hkv).  A step is a window of one row.
+ */
+enum gdn_kv_format {
+    GDN_KV_BF16 = 0,
+    GDN_KV_E4M3 = 1   /* OCP e4m3, value = code * scale of its row */
+};
+
+typedef struct gdn_kv_cache {
+    void *k, *v;                /* [n_pages][hkv][page_size][d], 16-byte aligned  */
+    float *k_scale, *v_scale;   /* [n_pages][hkv][page_size], GDN_KV_E4M3 only    */
+    int32_t n_pages, page_size;
+    int32_t hkv, d;
+    int32_t format;             /* enum gdn_kv_format */
+} gdn_kv_cache;
+
+/*
+ * Block tables and slot maps from the streams' lengths.  Stream s is to hold
+ * kv_len[s] cache rows and its row_start[s+1] - row_start[s] packed rows of
+ * this pass, in ceil of their sum / page_size pages; a stream with kv_len[s] <
+ * 0 has finished and holds none.
+ *   row_start  [n+1] int32; parent [total_rows] int32 or NULL (chains of any
+ *              length; with parents a window has at most 16 rows)
+ *   kv_len, page_count [n] int32: cached rows, and pages held so far
+ *   free_count [1], free_pages [n_pages] int32: a stack of unused pages
+ *   block_table [n][max_blocks] int32, in/out
+ *   slots, positions [total_rows] int32 out: the slot of each packed row, cache
+ *              row kv_len + (its place in the window), and its position,
+ *              kv_len + (its number of ancestors in the window)
+ *   page_count_out [n], free_count_out [1]: may be page_count and free_count
+ * Pages that streams no longer need go onto the stack in stream order; then
+ * the streams that grow take theirs from its top, in stream order, and the
+ * first one whose pages are not all there, with every later one that grows,
+ * takes none.  Rows of a stream that got none, has finished, would need more
+ * than max_blocks pages, or breaks the layout rules, and rows of no stream, get
+ * slot and position -1.  Entries of block_table past a stream's pages and
+ * entries of free_pages past those pushed are left as they were.
+ * n <= 4096.
+ */
+int gdn_kv_tables(int32_t n_streams, int32_t total_rows, int32_t page_size, int32_t n_pages,
+                  int32_t max_blocks, const int32_t *row_start, const int32_t *parent,
+                  const int32_t *kv_len, const int32_t *page_count, const int32_t *free_count,
+                  int32_t *free_pages, int32_t *block_table, int32_t *slots, int32_t *positions,
+                  int32_t *page_count_out, int32_t *free_count_out, void *stream);
+
+/*
+ * What lies between the projections and attention, for any number of packed
+ * rows: RMS norm of every query and key head, rotation of its first rot_dim
+ * channels by the row's position, queries to q_out, keys and values to the
+ * row's slot of the cache.
+ *     y = x / sqrt(mean(x^2) + eps) * norm,
+ *     (a, b) -> rot_scale (a cos t - b sin t, b cos t + a sin t),
+ *     t = positions[r] * inv_freq[i],  i < rot_dim / 2,
+ * with (a, b) channels (i, i + rot_dim/2), or (2i, 2i+1) if interleaved.  A
+ * scaling for long contexts is in the caller's inv_freq and rot_scale.  Values
+ * are stored as they are.
+ *   q [rows] x [hq][d], k, v [rows] x [hkv][d] bf16 with row and head strides
+ *     in elements (multiples of 8; 16-byte aligned), so that they may lie in
+ *     one projection's rows
+ *   q_norm, k_norm [d] fp32, or NULL for no norm;  inv_freq [rot_dim/2] fp32
+ *   positions, slots [rows] int32 (gdn_kv_tables); a row whose slot is outside
+ *     the cache stores no key and value
+ *   q_out [rows][hq][d] bf16
+ * GDN_KV_E4M3 rows get scale = max(max|y|, 2^-100) / 448 and codes y / scale
+ * rounded to nearest.  No two rows may have the same slot.
+ */
+typedef struct gdn_rope {
+    const float *inv_freq;   /* [rot_dim / 2], device */
+    int32_t rot_dim;         /* even, 0 .. d          */
+    int32_t interleaved;
+    float rot_scale;
+} gdn_rope;
+
+int gdn_attn_prep(const gdn_kv_cache *cache, int32_t rows, int32_t hq, const uint16_t *q,
+                  int64_t q_row_stride, int64_t q_head_stride, const uint16_t *k,
+                  int64_t k_row_stride, int64_t k_head_stride, const uint16_t *v,
+                  int64_t v_row_stride, int64_t v_head_stride, const float *q_norm,
+                  const float *k_norm, float eps, const gdn_rope *rope, const int32_t *positions,
+                  const int32_t *slots, uint16_t *q_out, void *stream);
+
+/*
+ * Attention of one-row steps, verify windows and draft trees over the cache,
+ * whose rows of this pass are already stored (gdn_attn_prep).  Row t of stream
+ * s sees the stream's kv_len[s] cached rows, itself, and the rows before it in
+ * the window, or, with parents, its ancestors:
+ *     out = sigmoid(gate) * softmax(scale q K^T) V.
+ *   q, out [total_rows][hq][d] bf16;  gate bf16 with row and head strides in
+ *     elements (multiples of 4; 8-byte aligned), or NULL
+ *   max_rows 1..16 and max_kv (at most 2^24): bounds on every window's rows and
+ *     on kv_len[s] + its rows
+ *   workspace: gdn_attn_workspace_bytes() of device memory, 16-byte aligned
+ *     (NULL where that is 0); its contents need not be kept between calls, and
+ *     calls that may overlap need their own
+ * A stream that breaks a rule (window, parents, lengths over max_kv or
+ * max_blocks, a page outside the cache) is skipped: its rows of out are left as
+ * they were, and so are rows of no stream.  A stream's results depend on
+ * neither the other streams of the call nor its place in it, bit for bit, for
+ * the same max_rows.  A row takes nothing from rows that it does not see,
+ * whatever they hold.
+ */
+size_t gdn_attn_workspace_bytes(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,
+                                int32_t max_rows, int32_t max_kv, int32_t hq);
+
+int gdn_attn_window(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,
+                    int32_t max_rows, int32_t max_kv, int32_t max_blocks, int32_t hq,
+                    const int32_t *row_start, const int32_t *parent, const int32_t *kv_len,
+                    const int32_t *block_table, const uint16_t *q, const uint16_t *gate,
+                    int64_t gate_row_stride, int64_t gate_head_stride, float scale, uint16_t *out,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Commit of the accepted rows in the cache, beside gdn_commit or
+ * gdn_commit_replay: the rows of the path that ends at accept_row[s] (a packed
+ * row of the stream's window, or -1 to keep none), root first, move to cache
+ * rows kv_len[s], kv_len[s] + 1, ..., and kv_len_out[s] = kv_len[s] + their
+ * number.  parent NULL: chains (nothing moves).  kv_len_out may be kv_len.  A
+ * stream whose accepted row or layout breaks the rules keeps its length, and
+ * none of its rows move.
+ */
+int gdn_attn_commit(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,
+                    int32_t max_rows, int32_t max_blocks, const int32_t *row_start,
+                    const int32_t *parent, const int32_t *accept_row, const int32_t *kv_len,
+                    const int32_t *block_table, int32_t *kv_len_out, void *stream);
+
+/*
  * Host-side check of a window or tree layout (HOST copies of row_start and,
  * for trees, parent; parent may be NULL for chains).  Returns GDN_OK or
  * GDN_EINVAL with gdn_last_error() naming the first broken rule.

@@ -2,12 +2,14 @@
 // launches on the caller's stream.  Declarations and contracts are in
 // include/libgdn.h.  Nothing here allocates device memory or keeps state
 // between calls.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
 #include <mutex>
 
 #include "../../include/libgdn.h"
+#include "gdn_attn.h"
 #include "gdn_internal.h"
 #include "gdn_inproj.h"
 #include "gdn_prefill.h"
@@ -584,6 +586,290 @@ int gdn_inproj_pack_affine4(const gdn_shape *shape, int32_t hidden, int32_t grou
     P.scales_tiled = scales_tiled;
     P.biases_tiled = biases_tiled;
     return launched(gdn::launch_inproj_pack(P, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// log2 of a page size, or -1 if it is not supported
+int page_shift(int32_t page_size)
+{
+    for (int sh = 4; sh <= 8; ++sh)
+        if (page_size == 1 << sh) return sh;
+    return -1;
+}
+
+// Sizes of a cache (no pointers); fills K's.
+int check_cache_sizes(const gdn_kv_cache *c, gdn::KvArgs &K)
+{
+    K = gdn::KvArgs{};
+    if (!c) return fail(GDN_EINVAL, "cache is NULL");
+    if (c->n_pages <= 0 || c->hkv <= 0 || c->d <= 0 || c->page_size <= 0)
+        return fail(GDN_EINVAL, "cache sizes must be positive (n_pages=%d hkv=%d page_size=%d d=%d)", c->n_pages,
+                    c->hkv, c->page_size, c->d);
+    if (c->format != GDN_KV_BF16 && c->format != GDN_KV_E4M3) return fail(GDN_EINVAL, "unknown cache format %d", c->format);
+    if (c->d != 64 && c->d != 128 && c->d != 256)
+        return fail(GDN_EUNSUPPORTED, "d %d: only 64, 128 and 256 are supported", c->d);
+    K.page_shift = page_shift(c->page_size);
+    if (K.page_shift < 0)
+        return fail(GDN_EUNSUPPORTED, "page_size %d: only 16, 32, 64, 128 and 256 are supported", c->page_size);
+    // the kernels number a cache's rows in 31 bits
+    if ((long long)c->n_pages * c->page_size > 0x7fffffffLL / c->hkv)
+        return fail(GDN_EUNSUPPORTED, "cache has 2^31 rows or more");
+    K.n_pages = c->n_pages;
+    K.hkv = c->hkv;
+    K.d = c->d;
+    return GDN_OK;
+}
+
+int check_cache_pointers(const gdn_kv_cache *c, gdn::KvArgs &K)
+{
+    const void *k = c->k, *v = c->v, *k_scale = c->k_scale, *v_scale = c->v_scale;
+    REQUIRE_PTR(k);
+    REQUIRE_PTR(v);
+    K.k = static_cast<uint8_t *>(c->k);
+    K.v = static_cast<uint8_t *>(c->v);
+    if (c->format == GDN_KV_E4M3) {
+        REQUIRE_PTR(k_scale);
+        REQUIRE_PTR(v_scale);
+        K.k_scale = c->k_scale;
+        K.v_scale = c->v_scale;
+    }
+    return GDN_OK;
+}
+
+int check_counts(int32_t n_streams, int32_t total_rows, int32_t max_rows, int32_t max_blocks, int32_t page_size)
+{
+    if (n_streams < 0) return fail(GDN_EINVAL, "n_streams %d is negative", n_streams);
+    if (total_rows < 0) return fail(GDN_EINVAL, "total_rows %d is negative", total_rows);
+    if (max_rows < 1 || max_rows > GDN_MAX_WINDOW_ROWS)
+        return fail(GDN_EINVAL, "max_rows %d is outside 1..%d", max_rows, GDN_MAX_WINDOW_ROWS);
+    if (max_blocks < 1) return fail(GDN_EINVAL, "max_blocks %d must be positive", max_blocks);
+    if ((long long)max_blocks * page_size > 0x7fffffffLL)
+        return fail(GDN_EUNSUPPORTED, "max_blocks %d: a stream would hold 2^31 rows or more", max_blocks);
+    return GDN_OK;
+}
+
+// A query-head count over the cache's kv heads, and the longest stream.
+int check_heads(const gdn_kv_cache *c, int32_t hq, int32_t max_kv)
+{
+    if (hq <= 0 || hq % c->hkv != 0) return fail(GDN_EINVAL, "hq (%d) must be a positive multiple of hkv (%d)", hq, c->hkv);
+    if (hq > 1024) return fail(GDN_EUNSUPPORTED, "hq %d: at most 1024", hq);
+    if (max_kv < 1) return fail(GDN_EINVAL, "max_kv %d must be positive", max_kv);
+    if (max_kv > 1 << 24) return fail(GDN_EUNSUPPORTED, "max_kv %d: at most 2^24", max_kv);
+    return GDN_OK;
+}
+
+int check_strides(const char *name, int64_t row, int64_t head, int multiple)
+{
+    if (row % multiple != 0 || head % multiple != 0 || row < 0 || head < 0)
+        return fail(GDN_EINVAL, "%s strides (%lld, %lld) must be non-negative multiples of %d", name, (long long)row,
+                    (long long)head, multiple);
+    return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdn_kv_tables(int32_t n_streams, int32_t total_rows, int32_t page_size, int32_t n_pages,
+                  int32_t max_blocks, const int32_t *row_start, const int32_t *parent,
+                  const int32_t *kv_len, const int32_t *page_count, const int32_t *free_count,
+                  int32_t *free_pages, int32_t *block_table, int32_t *slots, int32_t *positions,
+                  int32_t *page_count_out, int32_t *free_count_out, void *stream)
+{
+    const int shift = page_shift(page_size);
+    if (shift < 0)
+        return fail(GDN_EUNSUPPORTED, "page_size %d: only 16, 32, 64, 128 and 256 are supported", page_size);
+    const int rc = check_counts(n_streams, total_rows, 1, max_blocks, page_size);
+    if (rc) return rc;
+    if (n_pages < 1) return fail(GDN_EINVAL, "n_pages %d must be positive", n_pages);
+    if (n_streams > gdn::kMaxTableStreams) return fail(GDN_EUNSUPPORTED, "at most %d streams a call", gdn::kMaxTableStreams);
+    if ((long long)n_pages * page_size > 0x7fffffffLL || (long long)n_streams * max_blocks > 0x7fffffffLL)
+        return fail(GDN_EUNSUPPORTED, "the pool or the block table is too large");
+    if (!row_start) return fail(GDN_EINVAL, "row_start is NULL");
+    if (!free_count || !free_count_out) return fail(GDN_EINVAL, "free_count or free_count_out is NULL");
+    if (!free_pages) return fail(GDN_EINVAL, "free_pages is NULL");
+    if (n_streams > 0) {
+        if (!kv_len) return fail(GDN_EINVAL, "kv_len is NULL");
+        if (!page_count || !page_count_out) return fail(GDN_EINVAL, "page_count or page_count_out is NULL");
+        if (!block_table) return fail(GDN_EINVAL, "block_table is NULL");
+    }
+    if (total_rows > 0 && (!slots || !positions)) return fail(GDN_EINVAL, "slots or positions is NULL");
+    gdn::TablesArgs A = {};
+    A.n_streams = n_streams;
+    A.total_rows = total_rows;
+    A.page_shift = shift;
+    A.max_blocks = max_blocks;
+    A.n_pages = n_pages;
+    A.row_start = row_start;
+    A.parent = parent;
+    A.kv_len = kv_len;
+    A.page_count = page_count;
+    A.free_count = free_count;
+    A.free_pages = free_pages;
+    A.table = block_table;
+    A.slots = slots;
+    A.positions = positions;
+    A.page_count_out = page_count_out;
+    A.free_count_out = free_count_out;
+    return launched(gdn::launch_tables(A, static_cast<hipStream_t>(stream)));
+}
+
+int gdn_attn_prep(const gdn_kv_cache *cache, int32_t rows, int32_t hq, const uint16_t *q,
+                  int64_t q_row_stride, int64_t q_head_stride, const uint16_t *k,
+                  int64_t k_row_stride, int64_t k_head_stride, const uint16_t *v,
+                  int64_t v_row_stride, int64_t v_head_stride, const float *q_norm,
+                  const float *k_norm, float eps, const gdn_rope *rope, const int32_t *positions,
+                  const int32_t *slots, uint16_t *q_out, void *stream)
+{
+    gdn::PrepArgs A = {};
+    int rc = check_cache_sizes(cache, A.kv);
+    if (!rc) rc = check_heads(cache, hq, 1);
+    if (!rc) rc = check_strides("q", q_row_stride, q_head_stride, 8);
+    if (!rc) rc = check_strides("k", k_row_stride, k_head_stride, 8);
+    if (!rc) rc = check_strides("v", v_row_stride, v_head_stride, 8);
+    if (rc) return rc;
+    if (rows < 0) return fail(GDN_EINVAL, "rows %d is negative", rows);
+    if (!rope) return fail(GDN_EINVAL, "rope is NULL");
+    if (rope->rot_dim < 0 || rope->rot_dim > cache->d || rope->rot_dim % 2 != 0)
+        return fail(GDN_EINVAL, "rot_dim %d must be even and in 0..%d", rope->rot_dim, cache->d);
+    if (!(eps > 0.0f) || !isfinite(eps)) return fail(GDN_EINVAL, "eps must be positive");
+    if (!isfinite(rope->rot_scale)) return fail(GDN_EINVAL, "rot_scale must be finite");
+    if (rows == 0) {
+        g_err[0] = '\0';
+        return GDN_OK;
+    }
+    rc = check_cache_pointers(cache, A.kv);
+    if (rc) return rc;
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(k);
+    REQUIRE_PTR(v);
+    REQUIRE_PTR(q_out);
+    if (q_norm && !aligned16(q_norm)) return fail(GDN_EINVAL, "q_norm must be 16-byte aligned");
+    if (k_norm && !aligned16(k_norm)) return fail(GDN_EINVAL, "k_norm must be 16-byte aligned");
+    if (rope->rot_dim && !rope->inv_freq) return fail(GDN_EINVAL, "inv_freq is NULL");
+    if (!positions || !slots) return fail(GDN_EINVAL, "positions or slots is NULL");
+    A.rows = rows;
+    A.hq = hq;
+    A.rot = rope->rot_dim;
+    A.interleaved = rope->interleaved != 0;
+    A.q = q;
+    A.k = k;
+    A.v = v;
+    A.q_row = q_row_stride;
+    A.q_head = q_head_stride;
+    A.k_row = k_row_stride;
+    A.k_head = k_head_stride;
+    A.v_row = v_row_stride;
+    A.v_head = v_head_stride;
+    A.q_norm = q_norm;
+    A.k_norm = k_norm;
+    A.inv_freq = rope->inv_freq;
+    A.eps = eps;
+    A.rot_scale = rope->rot_scale;
+    A.positions = positions;
+    A.slots = slots;
+    A.q_out = q_out;
+    return launched(gdn::launch_prep(A, static_cast<hipStream_t>(stream)));
+}
+
+size_t gdn_attn_workspace_bytes(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,
+                                int32_t max_rows, int32_t max_kv, int32_t hq)
+{
+    gdn::KvArgs K;
+    if (check_cache_sizes(cache, K) != GDN_OK || check_heads(cache, hq, max_kv) != GDN_OK
+        || check_counts(n_streams, total_rows, max_rows, 1, cache->page_size) != GDN_OK)
+        return 0;
+    return gdn::attn_workspace_bytes(hq, cache->hkv, cache->d, total_rows, max_rows, max_kv);
+}
+
+int gdn_attn_window(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,
+                    int32_t max_rows, int32_t max_kv, int32_t max_blocks, int32_t hq,
+                    const int32_t *row_start, const int32_t *parent, const int32_t *kv_len,
+                    const int32_t *block_table, const uint16_t *q, const uint16_t *gate,
+                    int64_t gate_row_stride, int64_t gate_head_stride, float scale, uint16_t *out,
+                    void *workspace, size_t workspace_bytes, void *stream)
+{
+    gdn::AttnArgs A = {};
+    int rc = check_cache_sizes(cache, A.kv);
+    if (!rc) rc = check_heads(cache, hq, max_kv);
+    if (!rc) rc = check_counts(n_streams, total_rows, max_rows, max_blocks, cache->page_size);
+    if (!rc && gate) rc = check_strides("gate", gate_row_stride, gate_head_stride, 4);
+    if (rc) return rc;
+    if ((long long)total_rows > (long long)n_streams * max_rows)
+        return fail(GDN_EINVAL, "total_rows %d exceeds n_streams * max_rows", total_rows);
+    if (!isfinite(scale)) return fail(GDN_EINVAL, "scale must be finite");
+    if (n_streams == 0 || total_rows == 0) {
+        g_err[0] = '\0';
+        return GDN_OK;
+    }
+    rc = check_cache_pointers(cache, A.kv);
+    if (rc) return rc;
+    if (!row_start) return fail(GDN_EINVAL, "row_start is NULL");
+    if (!kv_len) return fail(GDN_EINVAL, "kv_len is NULL");
+    if (!block_table) return fail(GDN_EINVAL, "block_table is NULL");
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(out);
+    if (reinterpret_cast<uintptr_t>(gate) & 7u) return fail(GDN_EINVAL, "gate must be 8-byte aligned");
+    const size_t need = gdn::attn_workspace_bytes(hq, cache->hkv, cache->d, total_rows, max_rows, max_kv);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return fail(GDN_EWORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+        if (!aligned16(workspace)) return fail(GDN_EINVAL, "workspace must be 16-byte aligned");
+    }
+    A.n_streams = n_streams;
+    A.total_rows = total_rows;
+    A.max_rows = max_rows;
+    A.max_kv = max_kv;
+    A.max_blocks = max_blocks;
+    A.hq = hq;
+    A.group = hq / cache->hkv;
+    A.row_start = row_start;
+    A.parent = parent;
+    A.kv_len = kv_len;
+    A.table = block_table;
+    A.q = q;
+    A.gate = gate;
+    A.gate_row = gate_row_stride;
+    A.gate_head = gate_head_stride;
+    A.scale = scale * 1.44269504088896340736f;
+    A.out = out;
+    if (!gdn::attn_fits(A)) return fail(GDN_EUNSUPPORTED, "too many streams and chunks for one launch");
+    return launched(gdn::launch_attn(A, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int gdn_attn_commit(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,
+                    int32_t max_rows, int32_t max_blocks, const int32_t *row_start,
+                    const int32_t *parent, const int32_t *accept_row, const int32_t *kv_len,
+                    const int32_t *block_table, int32_t *kv_len_out, void *stream)
+{
+    gdn::AttnCommitArgs A = {};
+    int rc = check_cache_sizes(cache, A.kv);
+    if (!rc) rc = check_counts(n_streams, total_rows, max_rows, max_blocks, cache->page_size);
+    if (rc) return rc;
+    if (n_streams == 0) {
+        g_err[0] = '\0';
+        return GDN_OK;
+    }
+    rc = check_cache_pointers(cache, A.kv);
+    if (rc) return rc;
+    if (!row_start) return fail(GDN_EINVAL, "row_start is NULL");
+    if (!accept_row) return fail(GDN_EINVAL, "accept_row is NULL");
+    if (!kv_len || !kv_len_out) return fail(GDN_EINVAL, "kv_len or kv_len_out is NULL");
+    if (!block_table) return fail(GDN_EINVAL, "block_table is NULL");
+    A.n_streams = n_streams;
+    A.total_rows = total_rows;
+    A.max_rows = max_rows;
+    A.max_blocks = max_blocks;
+    A.row_start = row_start;
+    A.parent = parent;
+    A.accept = accept_row;
+    A.kv_len = kv_len;
+    A.table = block_table;
+    A.kv_len_out = kv_len_out;
+    return launched(gdn::launch_attn_commit(A, static_cast<hipStream_t>(stream)));
 }
 
 int gdn_check_layout(int32_t n_streams, int32_t total_rows, int32_t max_rows,

@@ -29,6 +29,7 @@ EXPORTED = (
     "gdn_prefill_workspace_bytes", "gdn_prefill_chunked", "gdn_prefill_chunked_noalloc",
     "gdn_check_layout",
     "gdn_inproj_affine4", "gdn_inproj_pack_affine4", "gdn_inproj_padded_features",
+    "gdn_kv_tables", "gdn_attn_prep", "gdn_attn_workspace_bytes", "gdn_attn_window", "gdn_attn_commit",
 )
 
 
@@ -45,6 +46,16 @@ class _Shape(C.Structure):
 
 class _Params(C.Structure):
     _fields_ = [("conv_w", C.c_void_p), ("a_log", C.c_void_p), ("dt_bias", C.c_void_p)]
+
+
+class _KvCache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("n_pages", C.c_int32), ("page_size", C.c_int32), ("hkv", C.c_int32), ("d", C.c_int32),
+                ("format", C.c_int32)]
+
+
+class _Rope(C.Structure):
+    _fields_ = [("inv_freq", C.c_void_p), ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("rot_scale", C.c_float)]
 
 
 _lock = threading.Lock()
@@ -81,10 +92,18 @@ def lib():
             L.gdn_inproj_pack_affine4.argtypes = [P, i32, i32, P, P, P, P, P, P, P]
             L.gdn_inproj_padded_features.restype = i32
             L.gdn_inproj_padded_features.argtypes = [P]
+            i64, f32 = C.c_int64, C.c_float
+            L.gdn_kv_tables.argtypes = [i32] * 5 + [P] * 12
+            L.gdn_attn_prep.argtypes = [P, i32, i32, P, i64, i64, P, i64, i64, P, i64, i64, P, P, f32, P, P, P, P, P]
+            L.gdn_attn_workspace_bytes.restype = C.c_size_t
+            L.gdn_attn_workspace_bytes.argtypes = [P, i32, i32, i32, i32, i32]
+            L.gdn_attn_window.argtypes = [P] + [i32] * 6 + [P] * 6 + [i64, i64, f32, P, P, C.c_size_t, P]
+            L.gdn_attn_commit.argtypes = [P] + [i32] * 4 + [P] * 7
             for name in ("gdn_conv_step", "gdn_recur_window", "gdn_recur_tree", "gdn_commit",
                          "gdn_recur_log", "gdn_commit_replay", "gdn_prefill_chunked",
                          "gdn_prefill_chunked_noalloc",
-                         "gdn_check_layout", "gdn_inproj_affine4", "gdn_inproj_pack_affine4"):
+                         "gdn_check_layout", "gdn_inproj_affine4", "gdn_inproj_pack_affine4", "gdn_kv_tables",
+                         "gdn_attn_prep", "gdn_attn_window", "gdn_attn_commit"):
                 getattr(L, name).restype = C.c_int
             _lib = L
     return _lib
@@ -308,6 +327,171 @@ def inproj_affine4(shape, x, wq, scales, biases, qkv, a, b, group: int):
     _check(lib().gdn_inproj_affine4(C.byref(sh), x.shape[0], x.shape[1], int(group), _ptr(x), _ptr(wq),
                                     _ptr(scales), _ptr(biases), _ptr(qkv), _ptr(a), _ptr(b), _stream(x)),
            "gdn_inproj_affine4")
+
+
+# ---- attention layers -------------------------------------------------------
+
+def _same(dev, dtype, name, t, shape=None):
+    """One argument of an attention-layer call: a contiguous tensor of this type
+    (and shape) on the call's device; its address."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise TypeError(f"{name} must be on {dev}, got {t.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _on(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    return t.device
+
+
+def _launch(dev, fn, *args):
+    """A call on torch's current stream of ``dev``, with ``dev`` current."""
+    f = getattr(_lib or lib(), fn)
+    if torch.cuda.current_device() == dev.index:
+        status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != GDN_OK:
+        _check(status, fn)
+
+
+def _cache(dev, k, v, k_scale, v_scale) -> _KvCache:
+    if k.dim() != 4:
+        raise ValueError(f"k_cache must be [pages][kv heads][page size][d], got {tuple(k.shape)}")
+    pages, hkv, page, d = k.shape
+    if k.dtype is torch.bfloat16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+        return _KvCache(_same(dev, torch.bfloat16, "k_cache", k), _same(dev, torch.bfloat16, "v_cache", v, k.shape), None,
+                        None, pages, page, hkv, d, 0)
+    if k.dtype is not torch.float8_e4m3fn:
+        raise TypeError(f"k_cache must be torch.bfloat16 or torch.float8_e4m3fn, got {k.dtype}")
+    if k_scale is None or v_scale is None:
+        raise ValueError("a float8_e4m3fn cache needs k_scale and v_scale")
+    rows = k.shape[:3]
+    return _KvCache(_same(dev, k.dtype, "k_cache", k), _same(dev, k.dtype, "v_cache", v, k.shape),
+                    _same(dev, torch.float32, "k_scale", k_scale, rows), _same(dev, torch.float32, "v_scale", v_scale, rows),
+                    pages, page, hkv, d, 1)
+
+
+def kv_tables(row_start, kv_len, page_count, free_count, free_pages, block_table, slots, positions, page_size: int,
+              parent=None, page_count_out=None, free_count_out=None):
+    """Block tables [n][max_blocks] (in place), slots and positions (written) of
+    one pass's packed rows, from the streams' lengths and the stack of unused
+    pages; the counts are updated in place unless outputs are given."""
+    dev = _on(row_start, "row_start")
+    i32 = torch.int32
+    n, total = row_start.shape[0] - 1, slots.shape[0]
+    if block_table.dim() != 2 or row_start.dim() != 1 or slots.dim() != 1 or free_pages.dim() != 1:
+        raise ValueError("block_table must be [streams][blocks]; row_start, slots and free_pages one-dimensional")
+    count_out = page_count if page_count_out is None else page_count_out
+    free_out = free_count if free_count_out is None else free_count_out
+    _launch(dev, "gdn_kv_tables", n, total, page_size, free_pages.shape[0], block_table.shape[1],
+            _same(dev, i32, "row_start", row_start), None if parent is None else _same(dev, i32, "parent", parent, (total,)),
+            _same(dev, i32, "kv_len", kv_len, (n,)), _same(dev, i32, "page_count", page_count, (n,)),
+            _same(dev, i32, "free_count", free_count, (1,)), _same(dev, i32, "free_pages", free_pages),
+            _same(dev, i32, "block_table", block_table, (n, block_table.shape[1])), _same(dev, i32, "slots", slots),
+            _same(dev, i32, "positions", positions, (total,)), _same(dev, i32, "page_count_out", count_out, (n,)),
+            _same(dev, i32, "free_count_out", free_out, (1,)))
+
+
+def _heads(dev, name, t, rows, heads, d):
+    """A bf16 [rows][heads][d] view with contiguous channels: address and strides."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != dev:
+        raise TypeError(f"{name} must be on {dev}, got {t.device}")
+    if t.shape != (rows, heads, d):
+        raise ValueError(f"{name} must be {(rows, heads, d)}, got {tuple(t.shape)}")
+    row, head, one = t.stride()
+    if one != 1 and rows:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    return t.data_ptr(), row, head
+
+
+def attn_prep(q, k, v, q_norm, k_norm, inv_freq, positions, slots, q_out, k_cache, v_cache, k_scale=None, v_scale=None,
+              eps: float = 1e-6, interleaved: bool = False, rot_scale: float = 1.0):
+    """RMS norms of the query and key heads (weights fp32 [d], None: no norm) and
+    rotation of their first ``2 * len(inv_freq)`` channels; queries to q_out,
+    keys and values to the cache.  q [R][hq][d], k and v [R][hkv][d] may be
+    views into one projection's rows."""
+    dev = _on(q, "q")
+    cache = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [rows][heads][d], got {tuple(q.shape)}")
+    rows, hq, d = q.shape
+    if d != cache.d:
+        raise ValueError(f"q has {d} channels a head, the cache {cache.d}")
+    qp, qr, qh = _heads(dev, "q", q, rows, hq, d)
+    kp, kr, kh = _heads(dev, "k", k, rows, cache.hkv, d)
+    vp, vr, vh = _heads(dev, "v", v, rows, cache.hkv, d)
+    f32, i32 = torch.float32, torch.int32
+    rope = _Rope(_same(dev, f32, "inv_freq", inv_freq, (inv_freq.numel(),)), 2 * inv_freq.numel(), 1 if interleaved else 0,
+                 rot_scale)
+    _launch(dev, "gdn_attn_prep", C.byref(cache), rows, hq, qp, qr, qh, kp, kr, kh, vp, vr, vh,
+            None if q_norm is None else _same(dev, f32, "q_norm", q_norm, (d,)),
+            None if k_norm is None else _same(dev, f32, "k_norm", k_norm, (d,)), eps, C.byref(rope),
+            _same(dev, i32, "positions", positions, (rows,)), _same(dev, i32, "slots", slots, (rows,)),
+            _same(dev, torch.bfloat16, "q_out", q_out, (rows, hq, d)))
+
+
+def attn_workspace_bytes(hq: int, hkv: int, d: int, n_streams: int, total_rows: int, max_rows: int, max_kv: int) -> int:
+    """Bytes of workspace ``attn_window`` needs for passes up to these sizes."""
+    cache = _KvCache(None, None, None, None, 1, 16, hkv, d, 0)
+    return int(lib().gdn_attn_workspace_bytes(C.byref(cache), int(n_streams), int(total_rows), int(max_rows), int(max_kv),
+                                              int(hq)))
+
+
+def attn_window(row_start, kv_len, block_table, q, k_cache, v_cache, out, workspace, max_kv: int,
+                max_rows: int = MAX_WINDOW_ROWS, parent=None, gate=None, k_scale=None, v_scale=None, scale=None):
+    """Attention of steps, windows (parent None) and trees over the cache, which
+    holds this pass's rows already; ``scale`` of the scores d ** -0.5 unless
+    given, ``gate`` (bf16 [R][hq][d], may be a view) applied as sigmoid(gate)."""
+    dev = _on(q, "q")
+    cache = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    if q.dim() != 3 or row_start.dim() != 1 or block_table.dim() != 2:
+        raise ValueError("q must be [rows][heads][d], row_start one-dimensional, block_table [streams][blocks]")
+    total, hq, d = q.shape
+    if d != cache.d:
+        raise ValueError(f"q has {d} channels a head, the cache {cache.d}")
+    n, blocks = block_table.shape
+    i32, bf16 = torch.int32, torch.bfloat16
+    gp, gr, gh = (None, 0, 0) if gate is None else _heads(dev, "gate", gate, total, hq, d)
+    ws, wsb = (None, 0) if workspace is None else (_same(dev, torch.uint8, "workspace", workspace), workspace.numel())
+    _launch(dev, "gdn_attn_window", C.byref(cache), n, total, max_rows, max_kv, blocks, hq,
+            _same(dev, i32, "row_start", row_start, (n + 1,)),
+            None if parent is None else _same(dev, i32, "parent", parent, (total,)),
+            _same(dev, i32, "kv_len", kv_len, (n,)), _same(dev, i32, "block_table", block_table),
+            _same(dev, bf16, "q", q), gp, gr, gh, d ** -0.5 if scale is None else scale,
+            _same(dev, bf16, "out", out, q.shape), ws, wsb)
+
+
+def attn_commit(row_start, accept_row, kv_len, block_table, k_cache, v_cache, k_scale=None, v_scale=None, parent=None,
+                kv_len_out=None, max_rows: int = MAX_WINDOW_ROWS):
+    """Each stream's accepted path (the packed row ``accept_row``, -1 = keep none)
+    moves to the end of its cached rows; the lengths are updated in place unless
+    ``kv_len_out`` is given."""
+    dev = _on(row_start, "row_start")
+    cache = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [streams][blocks]")
+    n, blocks = block_table.shape
+    i32 = torch.int32
+    # without parents nothing tells the pass's rows: the windows are checked by row_start alone
+    total = (1 << 31) - 1 if parent is None else parent.numel()
+    _launch(dev, "gdn_attn_commit", C.byref(cache), n, total, max_rows, blocks, _same(dev, i32, "row_start", row_start, (n + 1,)),
+            None if parent is None else _same(dev, i32, "parent", parent, (total,)),
+            _same(dev, i32, "accept_row", accept_row, (n,)), _same(dev, i32, "kv_len", kv_len, (n,)),
+            _same(dev, i32, "block_table", block_table),
+            _same(dev, i32, "kv_len_out", kv_len if kv_len_out is None else kv_len_out, (n,)))
 
 
 def check_layout(row_start, max_rows: int, total_rows: int, parent=None):
