@@ -120,11 +120,11 @@ struct VRow {
     static constexpr int W = BYTES / NL / 64;           // dwords of a load: 1, 2 or 4
     static constexpr int EPL = W * (F8 ? 4 : 2);
     uint32_t w[NL][W];
-    __device__ __forceinline__ void load(const uint8_t *row, int n)
+    __device__ __forceinline__ void load(const uint8_t *base, uint32_t off)
     {
 #pragma unroll
         for (int h = 0; h < NL; ++h) {
-            const uint8_t *p = row + h * 16 * W * 4 + n * W * 4;
+            const uint8_t *p = base + (off + h * 16 * W * 4);
             if constexpr (W == 4) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(p);
                 w[h][0] = x.x, w[h][1] = x.y, w[h][2] = x.z, w[h][3] = x.w;
@@ -194,17 +194,6 @@ __device__ __forceinline__ bf8v v_operand(const VRow<D, F8> (&v)[8], int h, int 
     return __builtin_bit_cast(bf8v, x);
 }
 
-// 1.0 where a bf16 of the operand is of the class (0: NaN, 1: inf, 2: -inf), else 0
-__device__ __forceinline__ bf8v operand_class(bf8v v, int cls)
-{
-    uint4 x = __builtin_bit_cast(uint4, v);
-    uint32_t *w = &x.x;
-    auto is = [&](uint32_t b) { return cls == 0 ? (b & 0x7fffu) > 0x7f80u : b == (cls == 1 ? 0x7f80u : 0xff80u); };
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = (is(w[i] & 0xffffu) ? 0x3f80u : 0u) | (is(w[i] >> 16) ? 0x3f800000u : 0u);
-    return __builtin_bit_cast(bf8v, x);
-}
-
 __device__ __forceinline__ f4v mfma(bf8v a, bf8v b, f4v c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 
 __device__ __forceinline__ float max_rows4(float x)     // over lanes l, l ^ 16, l ^ 32, l ^ 48
@@ -231,6 +220,30 @@ __device__ __forceinline__ uint2 finish4(const AttnArgs &A, float4 o, float inv,
     return make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
 }
 
+// Adds the infinite and NaN values of the window's rows in [key0, key1) that a
+// column sees (bits of seen) to its channels d .. d + 3.
+template <int D, bool F8>
+__device__ void add_bad(const AttnArgs &A, float4 &a, const int *rows16, uint32_t seen, int key0, int key1, int kv, int k0, int d)
+{
+    for (int key = key0; key < key1; ++key) {
+        if (!(seen >> (key - kv) & 1)) continue;
+        const size_t row = (size_t)rows16[(key - k0) >> 4] + (key & 15);
+        float v[4];
+        if constexpr (F8) {
+            const uint32_t x = *reinterpret_cast<const uint32_t *>(A.kv.v + row * D + d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = (x >> (8 * i) & 0x7fu) == 0x7fu ? NAN : 0.0f;
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(A.kv.v + (row * D + d) * 2);
+            const float w[4] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                                __uint_as_float(x.y & 0xffff0000u)};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = (__float_as_uint(w[i]) & 0x7f800000u) == 0x7f800000u ? w[i] : 0.0f;
+        }
+        a.x += v[0], a.y += v[1], a.z += v[2], a.w += v[3];
+    }
+}
+
 // What a stream's skipped chunk leaves in the workspace for join_kernel: sums
 // are never negative.
 constexpr float kSkipped = -1.0f;
@@ -246,7 +259,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
     float *o_lds = reinterpret_cast<float *>(smem);                    // [waves][kCols][OP]
     float *m_lds = o_lds + kAttnWaves * kCols * OP;                    // [waves][kCols]
     float *l_lds = m_lds + kAttnWaves * kCols;                         // [waves][kCols]
-    int *rows16 = reinterpret_cast<int *>(l_lds + kAttnWaves * kCols); // cache row of each 16 keys of the chunk
+    uint4 *q_lds = reinterpret_cast<uint4 *>(l_lds + kAttnWaves * kCols);   // [KS][2][64]
+    int *bad_lds = reinterpret_cast<int *>(q_lds + KS * 2 * 64);       // whether a window row's value is not finite
+    uint32_t *seen_lds = reinterpret_cast<uint32_t *>(bad_lds + 4);    // [kCols]: bits of the window's rows a column sees
+    int *rows16 = bad_lds + 4 + kCols;                                         // cache row of each 16 keys of the chunk
 
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, g = lane >> 4;
     int x = blockIdx.x;
@@ -263,7 +279,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
     if (k0 >= len || rt * kCols >= cols) return;
     const int k1 = min(k0 + C, len), nch = chunk_count(len);
     const int col = rt * kCols + n, ncol = min(cols - rt * kCols, kCols);
-    const int t = min(col / A.group, m - 1), head = h * A.group + min(col, cols - 1) % A.group;
+    const int t = min(col / A.group, m - 1);
 
     static_assert(kAttnWaves == 4, "");
     // cache rows of the chunk's keys, 16 at a time (pages hold multiples of 16)
@@ -276,8 +292,21 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
         rows16[i] = good ? ((id * A.kv.hkv + h) << A.kv.page_shift) + (key & ((1 << A.kv.page_shift) - 1)) : 0;
     }
     const uint32_t seen = seen_rows(A, r0, m, t, ok);
+    // the queries, in the order of the lanes' operands: [k-step][half][lane] of
+    // 16 bytes (column n, channels 64 k + 16 g + 8 half; zero past the last column)
+    for (int i = tid; i < KS * 2 * 64; i += kAttnThreads) {
+        const int qn = i & 15, qg = i >> 4 & 3, hh = i >> 6 & 1, k = i >> 7;
+        const int qc = min(rt * kCols + qn, cols - 1);
+        uint4 x = {0, 0, 0, 0};
+        if (qn < ncol)
+            x = *reinterpret_cast<const uint4 *>(A.q + ((size_t)(r0 + qc / A.group) * A.hq + h * A.group + qc % A.group) * D + 64 * k
+                                                 + 16 * qg + 8 * hh);
+        q_lds[i] = x;
+    }
     const bool wave_ok = !__ballot(!ok);
     if (lane == 0) l_lds[wave] = wave_ok ? 1.0f : 0.0f;     // free until the waves join
+    if (tid == 0) *bad_lds = 0;
+    if (tid < kCols) seen_lds[tid] = seen;
     __syncthreads();
     ok = l_lds[0] + l_lds[1] + l_lds[2] + l_lds[3] == 4.0f;
     if (!ok) {
@@ -287,17 +316,6 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
         return;
     }
 
-    // the lane's query column: 8 channels of every k-step (zero past the last column)
-    bf8v q[KS][2];
-    {
-        const uint16_t *p = A.q + ((size_t)(r0 + t) * A.hq + head) * D + 16 * g;
-        const uint4 zero = {0, 0, 0, 0};
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-                q[k][hh] = __builtin_bit_cast(bf8v, n < ncol ? *reinterpret_cast<const uint4 *>(p + 64 * k + 8 * hh) : zero);
-    }
 
     f4v o[NT];
 #pragma unroll
@@ -306,22 +324,21 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
 
     Run16<F8> kk[2][KS];
     V vv[8];
+    const uint32_t k_off = n * ROW + 16 * g * ESZ, v_off = 4 * g * ROW + n * V::W * 4;
     auto load_k = [&](int tile) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const size_t row = __builtin_amdgcn_readfirstlane(rows16[2 * tile + u]);
-            const uint8_t *p = A.kv.k + row * ROW + n * ROW + 16 * g * ESZ;
+            const uint8_t *p = A.kv.k + (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]) * ROW;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) kk[u][k].load(p + 64 * k * ESZ);
+            for (int k = 0; k < KS; ++k) kk[u][k].load(p + (k_off + 64 * k * ESZ));
         }
     };
     auto load_v = [&](int tile) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const size_t row = __builtin_amdgcn_readfirstlane(rows16[2 * tile + u]);
-            const uint8_t *p = A.kv.v + row * ROW + 4 * g * ROW;
+            const uint8_t *p = A.kv.v + (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]) * ROW;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) vv[4 * u + j].load(p + j * ROW, n);
+            for (int j = 0; j < 4; ++j) vv[4 * u + j].load(p, v_off + j * ROW);
         }
     };
     const int tiles = (k1 - k0 + kTile - 1) / kTile;
@@ -333,22 +350,26 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
         const bool more = tile + kAttnWaves < tiles;
         const int key0 = k0 + tile * kTile + 4 * g;      // the lane's keys: key0 + 16 u + i
         float p[8];
+        f4v acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const bf8v q = __builtin_bit_cast(bf8v, q_lds[(2 * k + hh) * 64 + lane]);
+                acc[0] = mfma(kk[0][k].get(hh), q, acc[0]);
+                acc[1] = mfma(kk[1][k].get(hh), q, acc[1]);
+            }
+        if (more) load_k(tile + kAttnWaves);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            f4v acc = {0, 0, 0, 0};
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) acc = mfma(kk[u][k].get(hh), q[k][hh], acc);
             float4 ks = {1, 1, 1, 1};
             if constexpr (F8)
                 ks = *reinterpret_cast<const float4 *>(A.kv.k_scale + __builtin_amdgcn_readfirstlane(rows16[2 * tile + u]) + 4 * g);
-            p[4 * u] = acc[0] * A.scale * ks.x;
-            p[4 * u + 1] = acc[1] * A.scale * ks.y;
-            p[4 * u + 2] = acc[2] * A.scale * ks.z;
-            p[4 * u + 3] = acc[3] * A.scale * ks.w;
+            p[4 * u] = acc[u][0] * A.scale * ks.x;
+            p[4 * u + 1] = acc[u][1] * A.scale * ks.y;
+            p[4 * u + 2] = acc[u][2] * A.scale * ks.z;
+            p[4 * u + 3] = acc[u][3] * A.scale * ks.w;
         }
-        if (more) load_k(tile + kAttnWaves);
         const bool tail = k0 + tile * kTile + kTile > kv;   // holds keys of the window or past the end
         uint32_t vis = 0xff;
         if (tail) {
@@ -407,29 +428,13 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
                 if (key0 + 16 * (i / 4) + (i & 3) >= len) vv[i].zero();
             // 0 * inf is NaN: an infinite or NaN value of a window row must not
             // reach the rows that do not see it.  Such values are left out of the
-            // product; three products of their indicators with the visibility
-            // tell which results they belong to.
+            // product, and added at the end to the results that they belong to.
             if (m > 1) {
                 bool fin = true;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) fin = fin && vv[i].finite();
                 if (__ballot(!fin)) {
-                    uint4 vw;
-                    uint32_t *w = &vw.x;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = (vis >> (2 * i) & 1 ? 0x3f80u : 0u) | (vis >> (2 * i + 1) & 1 ? 0x3f800000u : 0u);
-                    const bf8v vb = __builtin_bit_cast(bf8v, vw);
-#pragma unroll 1
-                    for (int cls = 0; cls < 3; ++cls) {
-                        const float value = cls == 0 ? NAN : cls == 1 ? INFINITY : -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < NT; ++i) {
-                            const f4v hit = mfma(operand_class(v_operand<D, F8>(vv, i / V::EPL, i % V::EPL), cls), vb, f4v{0, 0, 0, 0});
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (hit[e] > 0.0f) o[i][e] += value;
-                        }
-                    }
+                    if (lane == 0) *bad_lds = 1;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) vv[i].drop_bad();
                 }
@@ -475,6 +480,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
             mm = fmaxf(mm, m_lds[w * kCols + cc]);
         }
         const int cg = rt * kCols + cc, r = r0 + cg / A.group, hd = h * A.group + cg % A.group;
+        if (*bad_lds) add_bad<D, F8>(A, a, rows16, seen_lds[cc], max(kv, k0), k1, kv, k0, d);
         if (nch == 1) {
             *reinterpret_cast<uint2 *>(A.out + ((size_t)r * A.hq + hd) * D + d) = finish4(A, a, 1.0f / l, r, hd, d);
         } else {
@@ -543,7 +549,8 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs A)
 template <int D, bool F8>
 hipError_t launch_d(const AttnArgs &A, hipStream_t stream)
 {
-    const size_t lds = sizeof(float) * kAttnWaves * kCols * (D + 4 + 2) + sizeof(int) * (chunk_keys(A.max_kv) / 16);
+    const size_t lds = sizeof(float) * kAttnWaves * kCols * (D + 4 + 2) + D * 2 * kCols
+                       + sizeof(int) * (4 + kCols + chunk_keys(A.max_kv) / 16);
     static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(attn_kernel<D, F8>),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)kRowsMaxLds);
     if (e != hipSuccess) return e;
