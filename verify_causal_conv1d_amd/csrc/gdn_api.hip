@@ -657,7 +657,7 @@ int check_heads(const gdn_kv_cache *c, int32_t hq, int32_t max_kv)
     if (hq <= 0 || hq % c->hkv != 0) return fail(GDN_EINVAL, "hq (%d) must be a positive multiple of hkv (%d)", hq, c->hkv);
     if (hq > 1024) return fail(GDN_EUNSUPPORTED, "hq %d: at most 1024", hq);
     if (max_kv < 1) return fail(GDN_EINVAL, "max_kv %d must be positive", max_kv);
-    if (max_kv > 1 << 24) return fail(GDN_EUNSUPPORTED, "max_kv %d: at most 2^24", max_kv);
+    if (max_kv > gdn::kMaxAttnKeys) return fail(GDN_EUNSUPPORTED, "max_kv %d: at most %d", max_kv, gdn::kMaxAttnKeys);
     return GDN_OK;
 }
 

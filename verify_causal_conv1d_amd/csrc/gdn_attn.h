@@ -55,6 +55,7 @@ struct AttnCommitArgs {
     int32_t *kv_len_out;
 };
 
+constexpr int kMaxAttnKeys = 1 << 22;    // of one stream: a workgroup lists its chunk's pages in LDS
 constexpr int kMaxTableStreams = 4096;   // a workgroup keeps six ints of each in LDS
 
 size_t attn_workspace_bytes(int hq, int hkv, int d, int total_rows, int max_rows, int max_kv);

@@ -6,16 +6,23 @@
 // ancestors in the window):
 //     s_j = scale q . k_j,   o = sum_j e^{s_j} v_j / sum_j e^{s_j},   out = o sigmoid(gate).
 // Keys and values are read once for all rows and query heads of a kv head: the
-// (row, head) pairs of a stream and kv head are the 16 columns of the matrix
-// products S^T = K Q^T and O^T = V^T P^T.  One pass over the keys keeps the
-// running maximum m and sum l of each column (base-2 exponentials).
+// (row, head) pairs of a stream and kv head are the columns, 16 to a tile, of
+// the matrix products S^T = K Q^T and O^T = V^T P^T.  One pass over the keys
+// keeps the running maximum and sum of each column (base-2 exponentials).
 //
-// A stream's keys are cut into chunks at logical positions (a rule on its own
-// length alone, so its results do not depend on the other streams of the
-// call).  A chunk is one workgroup: its waves take tiles of 32 keys in turn and
-// join through LDS.  A stream of one chunk ends there; otherwise m, l and O of
-// every chunk go to the workspace and join_kernel merges them in chunk order:
+// A stream's keys are cut into chunks at logical positions, by a rule on its
+// own length alone, so that its results do not depend on the other streams of
+// the call.  A chunk (of one kv head and up to 16 or 128 columns) is one
+// workgroup.  A stream of one chunk ends there; otherwise m, l and O of every
+// chunk go to the workspace and join_kernel merges them in chunk order:
 //     m = max m_c,   l = sum l_c 2^{m_c - m},   o = sum O_c 2^{m_c - m} / l.
+//
+// Two kernels, by the columns that a window can have (max_rows * G):
+//  - up to 16, attn_kernel: its four waves take tiles of 32 keys in turn, each
+//    straight from memory into the registers that feed the matrix
+//    instructions, and join through LDS;
+//  - more, attn_wide_kernel: each wave has a column tile of its own, and K and
+//    V pass through LDS once for all of them.
 #include "gdn_attn.h"
 #include "gdn_device.h"
 #include "gdn_internal.h"
@@ -23,31 +30,39 @@
 namespace gdn {
 namespace {
 
-constexpr int kAttnThreads = 256, kAttnWaves = 4;
 constexpr int kTile = 32;                  // keys of a wave's step
-constexpr int kCols = 16;                  // (row, head) pairs of a workgroup
-constexpr int kChunkUnit = kTile * kAttnWaves;
-constexpr int kMaxChunks = 128;            // of one stream
+constexpr int kCols = 16;                  // (row, head) pairs of a column tile
+constexpr int kChunkUnit = 128;            // chunks are whole multiples of it
+constexpr int kMaxChunks = 64;             // of one stream
 
-// Keys of a chunk of a stream with len keys: at most kMaxChunks chunks, whole
-// steps of the workgroup.
-__host__ __device__ inline int chunk_keys(int len)
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ inline int at_least(int a, int b) { return a > b ? a : b; }
+__host__ __device__ inline int at_most(int a, int b) { return a < b ? a : b; }
+
+// Keys of a chunk of a stream with len keys: short chunks (lo) up to kMidChunks
+// of them, then longer ones up to mid, then up to kMaxChunks of mid, then longer.
+constexpr int kMidChunks = 32;
+__host__ __device__ inline int chunk_lo(bool wide) { return wide ? 512 : 256; }
+__host__ __device__ inline int chunk_mid(bool wide) { return wide ? 1024 : 512; }
+
+__host__ __device__ inline int chunk_keys(int len, bool wide)
 {
-    const int unit = kChunkUnit * kMaxChunks;
-    return kChunkUnit * ((len + unit - 1) / unit);
+    const int c = at_least(at_least(chunk_lo(wide), at_most(chunk_mid(wide), ceil_div(len, kMidChunks))), ceil_div(len, kMaxChunks));
+    return kChunkUnit * ceil_div(c, kChunkUnit);
 }
 
-__host__ __device__ inline int chunk_count(int len)
+__host__ __device__ inline int chunk_count(int len, bool wide)
 {
-    return len <= 0 ? 0 : (len + chunk_keys(len) - 1) / chunk_keys(len);
+    return len <= 0 ? 0 : ceil_div(len, chunk_keys(len, wide));
 }
 
-// Chunks of the longest stream: the count falls where the chunk grows by a
-// step, so the bound is that of the last full step.
-inline int chunk_bound(int max_kv)
+// The most chunks that a stream of up to max_kv keys can have.
+inline int chunk_bound(int max_kv, bool wide)
 {
-    return max_kv >= kChunkUnit * kMaxChunks ? kMaxChunks : chunk_count(max_kv);
+    return at_most(kMaxChunks, at_least(ceil_div(max_kv, chunk_mid(wide)), at_most(kMidChunks, ceil_div(max_kv, chunk_lo(wide)))));
 }
+
+inline bool is_wide(int max_rows, int group) { return max_rows * group > kCols; }
 
 // A stream's window by the layout rules that need no parents: false skips it.
 __device__ __forceinline__ bool stream_window(const AttnArgs &A, int s, int &r0, int &m, int &kv)
@@ -114,26 +129,27 @@ struct Run16<true> {
 // A lane's share of one value row: NL loads of W dwords each.  Column i of
 // load h is channel h * 16 * EPL + (lane % 16) * EPL + i.
 template <int D, bool F8>
-struct VRow {
+struct VLayout {
     static constexpr int BYTES = D * (F8 ? 1 : 2);
     static constexpr int NL = BYTES > 256 ? 2 : 1;
     static constexpr int W = BYTES / NL / 64;           // dwords of a load: 1, 2 or 4
     static constexpr int EPL = W * (F8 ? 4 : 2);
-    uint32_t w[NL][W];
-    __device__ __forceinline__ void load(const uint8_t *base, uint32_t off)
+    static constexpr int NT = NL * EPL;                 // tiles of 16 channels of O^T
+};
+
+template <bool F8, int W>
+struct VPart {
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const uint8_t *p)
     {
-#pragma unroll
-        for (int h = 0; h < NL; ++h) {
-            const uint8_t *p = base + (off + h * 16 * W * 4);
-            if constexpr (W == 4) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(p);
-                w[h][0] = x.x, w[h][1] = x.y, w[h][2] = x.z, w[h][3] = x.w;
-            } else if constexpr (W == 2) {
-                const uint2 x = *reinterpret_cast<const uint2 *>(p);
-                w[h][0] = x.x, w[h][1] = x.y;
-            } else {
-                w[h][0] = *reinterpret_cast<const uint32_t *>(p);
-            }
+        if constexpr (W == 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(p);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        } else if constexpr (W == 2) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(p);
+            w[0] = x.x, w[1] = x.y;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
         }
     }
     // a dword's elements that are infinite or NaN, as a mask of their bits
@@ -154,40 +170,33 @@ struct VRow {
     {
         uint32_t m = 0;
 #pragma unroll
-        for (int h = 0; h < NL; ++h)
-#pragma unroll
-            for (int i = 0; i < W; ++i) m |= bad(w[h][i]);
+        for (int i = 0; i < W; ++i) m |= bad(w[i]);
         return m == 0;
     }
     __device__ __forceinline__ void drop_bad()
     {
 #pragma unroll
-        for (int h = 0; h < NL; ++h)
-#pragma unroll
-            for (int i = 0; i < W; ++i) w[h][i] &= ~bad(w[h][i]);
+        for (int i = 0; i < W; ++i) w[i] &= ~bad(w[i]);
     }
     __device__ __forceinline__ void zero()
     {
 #pragma unroll
-        for (int h = 0; h < NL; ++h)
-#pragma unroll
-            for (int i = 0; i < W; ++i) w[h][i] = 0;
+        for (int i = 0; i < W; ++i) w[i] = 0;
     }
 };
 
-// The MFMA operand of column i of load h: that channel of the lane's 8 keys.
-template <int D, bool F8>
-__device__ __forceinline__ bf8v v_operand(const VRow<D, F8> (&v)[8], int h, int i)
+// The MFMA operand of column i of a load: that channel of the lane's 8 keys.
+template <bool F8, int W>
+__device__ __forceinline__ bf8v v_operand(const VPart<F8, W> (&v)[8], int i)
 {
     uint32_t o[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         if constexpr (F8) {
-            const uint32_t both = __builtin_amdgcn_perm(v[2 * q + 1].w[h][i / 4], v[2 * q].w[h][i / 4],
-                                                        i & 2 ? 0x07030602u : 0x05010400u);
+            const uint32_t both = __builtin_amdgcn_perm(v[2 * q + 1].w[i / 4], v[2 * q].w[i / 4], i & 2 ? 0x07030602u : 0x05010400u);
             o[q] = cvt2(both, i & 1);
         } else {
-            o[q] = __builtin_amdgcn_perm(v[2 * q + 1].w[h][i / 2], v[2 * q].w[h][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
+            o[q] = __builtin_amdgcn_perm(v[2 * q + 1].w[i / 2], v[2 * q].w[i / 2], i & 1 ? 0x07060302u : 0x05040100u);
         }
     }
     const uint4 x = {o[0], o[1], o[2], o[3]};
@@ -248,141 +257,46 @@ __device__ void add_bad(const AttnArgs &A, float4 &a, const int *rows16, uint32_
 // are never negative.
 constexpr float kSkipped = -1.0f;
 
+// The running state of a wave's column tile.  Lane (n, g) = (lane % 16, lane /
+// 16) holds column n: of S^T the keys 16 u + 4 g + i of a tile of 32 (u < 2, i <
+// 4), which are also the 8 keys it feeds into O^T's product, and of O^T the
+// channels given by VLayout with row 4 g + e for lane % 16.
 template <int D, bool F8>
-__global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
-{
-    constexpr int ESZ = F8 ? 1 : 2, ROW = D * ESZ, KS = D / 64;
-    using V = VRow<D, F8>;
-    constexpr int NT = V::NL * V::EPL;             // column tiles of O^T (16 channels each)
-    constexpr int OP = D + 4;                      // padded LDS row of a column's channels
-    extern __shared__ __align__(16) uint8_t smem[];
-    float *o_lds = reinterpret_cast<float *>(smem);                    // [waves][kCols][OP]
-    float *m_lds = o_lds + kAttnWaves * kCols * OP;                    // [waves][kCols]
-    float *l_lds = m_lds + kAttnWaves * kCols;                         // [waves][kCols]
-    uint4 *q_lds = reinterpret_cast<uint4 *>(l_lds + kAttnWaves * kCols);   // [KS][2][64]
-    int *bad_lds = reinterpret_cast<int *>(q_lds + KS * 2 * 64);       // whether a window row's value is not finite
-    uint32_t *seen_lds = reinterpret_cast<uint32_t *>(bad_lds + 4);    // [kCols]: bits of the window's rows a column sees
-    int *rows16 = bad_lds + 4 + kCols;                                         // cache row of each 16 keys of the chunk
+struct Column {
+    using V = VLayout<D, F8>;
+    f4v o[V::NT];
+    float mx, sum;
 
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, g = lane >> 4;
-    int x = blockIdx.x;
-    const int c = x % A.chunks;
-    x /= A.chunks;
-    const int h = x % A.kv.hkv;
-    x /= A.kv.hkv;
-    const int rt = x % A.row_tiles, s = x / A.row_tiles;
-
-    int r0, m, kv;
-    if (!stream_window(A, s, r0, m, kv)) return;
-    const int len = kv + m, C = chunk_keys(len), k0 = c * C;
-    const int cols = m * A.group;                                      // (row, head) pairs of this kv head
-    if (k0 >= len || rt * kCols >= cols) return;
-    const int k1 = min(k0 + C, len), nch = chunk_count(len);
-    const int col = rt * kCols + n, ncol = min(cols - rt * kCols, kCols);
-    const int t = min(col / A.group, m - 1);
-
-    static_assert(kAttnWaves == 4, "");
-    // cache rows of the chunk's keys, 16 at a time (pages hold multiples of 16)
-    bool ok = true;
-    for (int i = tid; i < C / 16; i += kAttnThreads) {
-        const int key = min(k0 + 16 * i, (len - 1) & ~15);
-        const int id = A.table[(size_t)s * A.max_blocks + (key >> A.kv.page_shift)];
-        const bool good = id >= 0 && id < A.kv.n_pages;
-        ok = ok && good;
-        rows16[i] = good ? ((id * A.kv.hkv + h) << A.kv.page_shift) + (key & ((1 << A.kv.page_shift) - 1)) : 0;
-    }
-    const uint32_t seen = seen_rows(A, r0, m, t, ok);
-    // the queries, in the order of the lanes' operands: [k-step][half][lane] of
-    // 16 bytes (column n, channels 64 k + 16 g + 8 half; zero past the last column)
-    for (int i = tid; i < KS * 2 * 64; i += kAttnThreads) {
-        const int qn = i & 15, qg = i >> 4 & 3, hh = i >> 6 & 1, k = i >> 7;
-        const int qc = min(rt * kCols + qn, cols - 1);
-        uint4 x = {0, 0, 0, 0};
-        if (qn < ncol)
-            x = *reinterpret_cast<const uint4 *>(A.q + ((size_t)(r0 + qc / A.group) * A.hq + h * A.group + qc % A.group) * D + 64 * k
-                                                 + 16 * qg + 8 * hh);
-        q_lds[i] = x;
-    }
-    const bool wave_ok = !__ballot(!ok);
-    if (lane == 0) l_lds[wave] = wave_ok ? 1.0f : 0.0f;     // free until the waves join
-    if (tid == 0) *bad_lds = 0;
-    if (tid < kCols) seen_lds[tid] = seen;
-    __syncthreads();
-    ok = l_lds[0] + l_lds[1] + l_lds[2] + l_lds[3] == 4.0f;
-    if (!ok) {
-        if (nch > 1 && tid < ncol)
-            A.stat[((size_t)(r0 + (rt * kCols + tid) / A.group) * A.hq + h * A.group + (rt * kCols + tid) % A.group) * A.chunks + c] =
-                make_float2(0.0f, kSkipped);
-        return;
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < V::NT; ++i) o[i] = f4v{0, 0, 0, 0};
+        mx = -INFINITY;
+        sum = 0.0f;
     }
 
-
-    f4v o[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) o[i] = f4v{0, 0, 0, 0};
-    float mx = -INFINITY, sum = 0.0f;
-
-    Run16<F8> kk[2][KS];
-    V vv[8];
-    const uint32_t k_off = n * ROW + 16 * g * ESZ, v_off = 4 * g * ROW + n * V::W * 4;
-    auto load_k = [&](int tile) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint8_t *p = A.kv.k + (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]) * ROW;
-#pragma unroll
-            for (int k = 0; k < KS; ++k) kk[u][k].load(p + (k_off + 64 * k * ESZ));
-        }
-    };
-    auto load_v = [&](int tile) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint8_t *p = A.kv.v + (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]) * ROW;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) vv[4 * u + j].load(p, v_off + j * ROW);
-        }
-    };
-    const int tiles = (k1 - k0 + kTile - 1) / kTile;
-    if (wave < tiles) {
-        load_k(wave);
-        load_v(wave);
-    }
-    for (int tile = wave; tile < tiles; tile += kAttnWaves) {
-        const bool more = tile + kAttnWaves < tiles;
-        const int key0 = k0 + tile * kTile + 4 * g;      // the lane's keys: key0 + 16 u + i
+    // Weights of a tile's keys from its scores (before scale and k_scale): the
+    // maximum, the sum and O brought up to date, P times v_scale in bf16.  key0: the lane's first key; seen: the window's rows that the column sees.
+    // TAIL: the tile holds keys of the window or past the end.
+    template <bool TAIL>
+    __device__ __forceinline__ bf8v weights(const f4v (&acc)[2], float scale, const float4 (&ks)[2], const float4 (&vs)[2], int key0,
+                                            int kv, uint32_t seen)
+    {
         float p[8];
-        f4v acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const bf8v q = __builtin_bit_cast(bf8v, q_lds[(2 * k + hh) * 64 + lane]);
-                acc[0] = mfma(kk[0][k].get(hh), q, acc[0]);
-                acc[1] = mfma(kk[1][k].get(hh), q, acc[1]);
-            }
-        if (more) load_k(tile + kAttnWaves);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            float4 ks = {1, 1, 1, 1};
-            if constexpr (F8)
-                ks = *reinterpret_cast<const float4 *>(A.kv.k_scale + __builtin_amdgcn_readfirstlane(rows16[2 * tile + u]) + 4 * g);
-            p[4 * u] = acc[u][0] * A.scale * ks.x;
-            p[4 * u + 1] = acc[u][1] * A.scale * ks.y;
-            p[4 * u + 2] = acc[u][2] * A.scale * ks.z;
-            p[4 * u + 3] = acc[u][3] * A.scale * ks.w;
+            const float k4[4] = {ks[u].x, ks[u].y, ks[u].z, ks[u].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[4 * u + i] = F8 ? acc[u][i] * (scale * k4[i]) : acc[u][i] * scale;
         }
-        const bool tail = k0 + tile * kTile + kTile > kv;   // holds keys of the window or past the end
-        uint32_t vis = 0xff;
-        if (tail) {
-            vis = 0;
+        bool vis[8];
+        if constexpr (TAIL)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int j = key0 + 16 * (i / 4) + (i & 3) - kv;   // place in the window
-                if (j < 0 || (j < kMaxWindowRows && (seen >> j & 1))) vis |= 1u << i;
+                vis[i] = (j < 0) | ((j < kMaxWindowRows) & (seen >> (j & 31)));
+                p[i] = vis[i] ? p[i] : -INFINITY;
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (!(vis >> i & 1)) p[i] = -INFINITY;
-        }
         float tm = p[0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) tm = fmaxf(tm, p[i]);
@@ -399,60 +313,240 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
         sum = fmaf(sum, back, ps);
         if (__ballot(back != 1.0f)) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < V::NT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][e] *= back;
         }
         if constexpr (F8) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const float4 vs = *reinterpret_cast<const float4 *>(A.kv.v_scale + __builtin_amdgcn_readfirstlane(rows16[2 * tile + u]) + 4 * g);
-                p[4 * u] *= vs.x;
-                p[4 * u + 1] *= vs.y;
-                p[4 * u + 2] *= vs.z;
-                p[4 * u + 3] *= vs.w;
+                p[4 * u] *= vs[u].x;
+                p[4 * u + 1] *= vs[u].y;
+                p[4 * u + 2] *= vs[u].z;
+                p[4 * u + 3] *= vs[u].w;
             }
-            if (tail)        // a masked row's scale may be anything
+            if constexpr (TAIL)        // a masked row's scale may be anything
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (!(vis >> i & 1)) p[i] = 0.0f;
+                for (int i = 0; i < 8; ++i) p[i] = vis[i] ? p[i] : 0.0f;
         }
-        // P in bf16, rounded to nearest: its error is at most 2^-9 of each term,
+        // P in bf16, rounded to nearest: its error is at most 2^-8 of each term,
         // that of the bf16 result's own rounding; the sum keeps the fp32 values
         const uint4 pw = {pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
-        const bf8v pb = __builtin_bit_cast(bf8v, pw);
-        if (tail) {
-            // rows past the end hold anything: zero them
+        return __builtin_bit_cast(bf8v, pw);
+    }
+
+    // O^T += V^T P^T for the channels of load h
+    __device__ __forceinline__ void values(int h, const VPart<F8, V::W> (&v)[8], bf8v pb)
+    {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (key0 + 16 * (i / 4) + (i & 3) >= len) vv[i].zero();
-            // 0 * inf is NaN: an infinite or NaN value of a window row must not
-            // reach the rows that do not see it.  Such values are left out of the
-            // product, and added at the end to the results that they belong to.
-            if (m > 1) {
-                bool fin = true;
+        for (int i = 0; i < V::EPL; ++i) o[h * V::EPL + i] = mfma(v_operand(v, i), pb, o[h * V::EPL + i]);
+    }
+};
+
+// Values of a tile that holds keys of the window or past the end.  Rows past
+// the end hold anything: zeros instead.  And 0 * inf is NaN: an infinite or NaN
+// value of a window row must not reach the rows that do not see it, so such
+// values are left out of the product (true is returned), to be added at the
+// end to the results that they belong to (add_bad).
+template <bool F8, int W>
+__device__ __forceinline__ bool clean_values(VPart<F8, W> (&v)[8], int key0, int len, int m)
+{
+    bool fin = true;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) fin = fin && vv[i].finite();
-                if (__ballot(!fin)) {
-                    if (lane == 0) *bad_lds = 1;
+    for (int i = 0; i < 8; ++i) {
+        if (key0 + 16 * (i / 4) + (i & 3) >= len) v[i].zero();
+        fin = fin && v[i].finite();
+    }
+    if (m == 1 || !__ballot(!fin)) return false;      // every column of a one-row window sees all its keys
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) vv[i].drop_bad();
-                }
+    for (int i = 0; i < 8; ++i) v[i].drop_bad();
+    return true;
+}
+
+// The chunk of a workgroup.
+struct Chunk {
+    int s, h, rt, c;          // stream, kv head, tile of columns, chunk
+    int r0, m, kv, len;       // the stream's window, cached rows, keys in all
+    int k0, k1, nch;          // the chunk's keys, and chunks of the stream
+    int size;                 // keys of a full chunk
+    int cols;                 // (row, head) pairs of the stream
+};
+
+// The chunk of this workgroup, tile_cols columns wide; false if there is none.
+__device__ __forceinline__ bool find_chunk(const AttnArgs &A, bool wide, int tile_cols, Chunk &K)
+{
+    int x = blockIdx.x;
+    K.c = x % A.chunks;
+    x /= A.chunks;
+    K.h = x % A.kv.hkv;
+    x /= A.kv.hkv;
+    K.rt = x % A.row_tiles;
+    K.s = x / A.row_tiles;
+    if (!stream_window(A, K.s, K.r0, K.m, K.kv)) return false;
+    K.len = K.kv + K.m;
+    K.size = chunk_keys(K.len, wide);
+    K.k0 = K.c * K.size;
+    K.k1 = min(K.k0 + K.size, K.len);
+    K.nch = chunk_count(K.len, wide);
+    K.cols = K.m * A.group;
+    return K.k0 < K.len && K.rt * tile_cols < K.cols;
+}
+
+// Cache rows of the chunk's keys, 16 at a time (pages hold multiples of 16) up
+// to the chunk's full size: past the stream's end those of its last keys, so
+// that every load stays in its pages.  false if a page is not in the cache.
+__device__ __forceinline__ bool chunk_rows(const AttnArgs &A, const Chunk &K, int *rows16, int threads)
+{
+    bool ok = true;
+    for (int i = threadIdx.x; i < K.size / 16; i += threads) {
+        const int key = min(K.k0 + 16 * i, (K.len - 1) & ~15);
+        const int id = A.table[(size_t)K.s * A.max_blocks + (key >> A.kv.page_shift)];
+        const bool good = id >= 0 && id < A.kv.n_pages;
+        ok = ok && good;
+        rows16[i] = good ? ((id * A.kv.hkv + K.h) << A.kv.page_shift) + (key & ((1 << A.kv.page_shift) - 1)) : 0;
+    }
+    return ok;
+}
+
+// Packed row and query head of a stream's column.
+__device__ __forceinline__ int col_row(const AttnArgs &A, const Chunk &K, int col) { return K.r0 + col / A.group; }
+__device__ __forceinline__ int col_head(const AttnArgs &A, const Chunk &K, int col) { return K.h * A.group + col % A.group; }
+// and its place in the workspace
+__device__ __forceinline__ size_t col_part(const AttnArgs &A, const Chunk &K, int col)
+{
+    return ((size_t)col_row(A, K, col) * A.hq + col_head(A, K, col)) * A.chunks + K.c;
+}
+
+// A column's 4 channels from d: the result where the chunk is the stream's only
+// one, else its part in the workspace.
+template <int D>
+__device__ __forceinline__ void put4(const AttnArgs &A, const Chunk &K, int col, float4 a, float l, int d)
+{
+    const int r = col_row(A, K, col), hd = col_head(A, K, col);
+    if (K.nch == 1) *reinterpret_cast<uint2 *>(A.out + ((size_t)r * A.hq + hd) * D + d) = finish4(A, a, 1.0f / l, r, hd, d);
+    else *reinterpret_cast<float4 *>(A.part + col_part(A, K, col) * D + d) = a;
+}
+
+// ---- up to 16 columns -----------------------------------------------------------
+
+constexpr int kAttnThreads = 256, kAttnWaves = 4;
+
+// Two workgroups a CU (registers and LDS), each wave with the next tile of keys
+// and of values in flight: 32 KB a wave at d = 256 in bf16.
+template <int D, bool F8>
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
+{
+    constexpr int ESZ = F8 ? 1 : 2, ROW = D * ESZ, KS = D / 64;
+    using V = VLayout<D, F8>;
+    constexpr int OP = D + 4;                      // padded LDS row of a column's channels
+    extern __shared__ __align__(16) uint8_t smem[];
+    float *o_lds = reinterpret_cast<float *>(smem);                    // [waves][kCols][OP]
+    float *m_lds = o_lds + kAttnWaves * kCols * OP;                    // [waves][kCols]
+    float *l_lds = m_lds + kAttnWaves * kCols;                         // [waves][kCols]
+    uint4 *q_lds = reinterpret_cast<uint4 *>(l_lds + kAttnWaves * kCols);   // [KS][2][64]
+    int *bad_lds = reinterpret_cast<int *>(q_lds + KS * 2 * 64);       // whether a window row's value is not finite
+    uint32_t *seen_lds = reinterpret_cast<uint32_t *>(bad_lds + 4);    // [kCols]: the window's rows that a column sees
+    int *rows16 = bad_lds + 4 + kCols;                                 // [size / 16]
+
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, g = lane >> 4;
+    Chunk K;
+    if (!find_chunk(A, false, kCols, K)) return;
+    const int col0 = K.rt * kCols, ncol = min(K.cols - col0, kCols);
+    bool ok = chunk_rows(A, K, rows16, kAttnThreads);
+    const uint32_t seen = seen_rows(A, K.r0, K.m, min((col0 + n) / A.group, K.m - 1), ok);
+    // the queries, in the order of the lanes' operands: [k-step][half][lane] of
+    // 16 bytes (column n, channels 64 k + 16 g + 8 half; zero past the last column)
+    for (int i = tid; i < KS * 2 * 64; i += kAttnThreads) {
+        const int qc = i & 15, qg = i >> 4 & 3, hh = i >> 6 & 1, k = i >> 7;
+        uint4 x = {0, 0, 0, 0};
+        if (qc < ncol)
+            x = *reinterpret_cast<const uint4 *>(A.q + ((size_t)col_row(A, K, col0 + qc) * A.hq + col_head(A, K, col0 + qc)) * D
+                                                 + 64 * k + 16 * qg + 8 * hh);
+        q_lds[i] = x;
+    }
+    const bool wave_ok = !__ballot(!ok);
+    static_assert(kAttnWaves == 4, "");
+    if (lane == 0) l_lds[wave] = wave_ok ? 1.0f : 0.0f;     // free until the waves join
+    if (tid == 0) *bad_lds = 0;
+    if (tid < kCols) seen_lds[tid] = seen;
+    __syncthreads();
+    if (l_lds[0] + l_lds[1] + l_lds[2] + l_lds[3] != 4.0f) {
+        if (K.nch > 1 && tid < ncol) A.stat[col_part(A, K, col0 + tid)] = make_float2(0.0f, kSkipped);
+        return;
+    }
+
+    Column<D, F8> C;
+    C.clear();
+    Run16<F8> kk[2][KS];
+    VPart<F8, V::W> vv[V::NL][8];
+    const uint32_t k_off = n * ROW + 16 * g * ESZ, v_off = 4 * g * ROW + n * V::W * 4;
+    auto load_k = [&](int tile) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const uint8_t *p = A.kv.k + (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]) * ROW;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) kk[u][k].load(p + (k_off + 64 * k * ESZ));
+        }
+    };
+    auto load_v = [&](int tile) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const uint8_t *p = A.kv.v + (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]) * ROW;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int hh = 0; hh < V::NL; ++hh) vv[hh][4 * u + j].load(p + (v_off + j * ROW + hh * 16 * V::W * 4));
+        }
+    };
+    const int tiles = ceil_div(K.k1 - K.k0, kTile);
+    if (wave < tiles) {
+        load_k(wave);
+        load_v(wave);
+    }
+    for (int tile = wave; tile < tiles; tile += kAttnWaves) {
+        const bool more = tile + kAttnWaves < tiles;
+        const int key0 = K.k0 + tile * kTile + 4 * g;
+        f4v acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const bf8v q = __builtin_bit_cast(bf8v, q_lds[(2 * k + hh) * 64 + lane]);
+                acc[0] = mfma(kk[0][k].get(hh), q, acc[0]);
+                acc[1] = mfma(kk[1][k].get(hh), q, acc[1]);
+            }
+        if (more) load_k(tile + kAttnWaves);
+        float4 ks[2] = {}, vs[2] = {};
+        if constexpr (F8)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const size_t row = __builtin_amdgcn_readfirstlane(rows16[2 * tile + u]);
+                ks[u] = *reinterpret_cast<const float4 *>(A.kv.k_scale + row + 4 * g);
+                vs[u] = *reinterpret_cast<const float4 *>(A.kv.v_scale + row + 4 * g);
+            }
+        if (K.k0 + tile * kTile + kTile <= K.kv) {
+            const bf8v pb = C.template weights<false>(acc, A.scale, ks, vs, key0, K.kv, seen);
+#pragma unroll
+            for (int hh = 0; hh < V::NL; ++hh) C.values(hh, vv[hh], pb);
+        } else {
+            const bf8v pb = C.template weights<true>(acc, A.scale, ks, vs, key0, K.kv, seen);
+#pragma unroll
+            for (int hh = 0; hh < V::NL; ++hh) {
+                if (clean_values(vv[hh], key0, K.len, K.m) && lane == 0) *bad_lds = 1;
+                C.values(hh, vv[hh], pb);
             }
         }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) o[i] = mfma(v_operand<D, F8>(vv, i / V::EPL, i % V::EPL), pb, o[i]);
         if (more) load_v(tile + kAttnWaves);
     }
 
     // join the waves: the column's maximum over them, each wave's O and l scaled to it
-    sum = sum_rows4(sum);
-    if (g == 0) m_lds[wave * kCols + n] = mx;
+    const float sum = sum_rows4(C.sum);
+    if (g == 0) m_lds[wave * kCols + n] = C.mx;
     __syncthreads();
     float top = m_lds[n];
 #pragma unroll
     for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, m_lds[w * kCols + n]);
-    const float f = __builtin_amdgcn_exp2f(mx - (top == -INFINITY ? 0.0f : top));
+    const float f = __builtin_amdgcn_exp2f(C.mx - (top == -INFINITY ? 0.0f : top));
     if (g == 0) l_lds[wave * kCols + n] = sum * f;
     if (n < ncol) {
         float *row = o_lds + (wave * kCols + n) * OP;
@@ -461,10 +555,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float *p = row + hh * 16 * V::EPL + (4 * g + e) * V::EPL;
+                const f4v *o = C.o + hh * V::EPL;
 #pragma unroll
                 for (int i = 0; i < V::EPL; i += 4)
-                    *reinterpret_cast<float4 *>(p + i) = make_float4(o[hh * V::EPL + i][e] * f, o[hh * V::EPL + i + 1][e] * f,
-                                                                     o[hh * V::EPL + i + 2][e] * f, o[hh * V::EPL + i + 3][e] * f);
+                    *reinterpret_cast<float4 *>(p + i) = make_float4(o[i][e] * f, o[i + 1][e] * f, o[i + 2][e] * f, o[i + 3][e] * f);
             }
     }
     __syncthreads();
@@ -479,22 +573,217 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
             l += l_lds[w * kCols + cc];
             mm = fmaxf(mm, m_lds[w * kCols + cc]);
         }
-        const int cg = rt * kCols + cc, r = r0 + cg / A.group, hd = h * A.group + cg % A.group;
-        if (*bad_lds) add_bad<D, F8>(A, a, rows16, seen_lds[cc], max(kv, k0), k1, kv, k0, d);
-        if (nch == 1) {
-            *reinterpret_cast<uint2 *>(A.out + ((size_t)r * A.hq + hd) * D + d) = finish4(A, a, 1.0f / l, r, hd, d);
-        } else {
-            const size_t at = ((size_t)r * A.hq + hd) * A.chunks + c;
-            *reinterpret_cast<float4 *>(A.part + at * D + d) = a;
-            if (d == 0) A.stat[at] = make_float2(mm, l);
-        }
+        if (*bad_lds) add_bad<D, F8>(A, a, rows16, seen_lds[cc], max(K.kv, K.k0), K.k1, K.kv, K.k0, d);
+        put4<D>(A, K, col0 + cc, a, l, d);
+        if (K.nch > 1 && d == 0) A.stat[col_part(A, K, col0 + cc)] = make_float2(mm, l);
     }
+}
+
+// ---- more columns ----------------------------------------------------------------
+
+typedef const __attribute__((address_space(1))) void global_void;
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Waits until all but the newest N vector memory operations of the wave and all
+// of its LDS reads are done, then for the workgroup's other waves.
+template <int N>
+__device__ __forceinline__ void wait_and_meet()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | (N >> 4) << 14);     // vmcnt(N) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Four stages of keys and values in LDS, filled by direct loads (16 bytes a
+// lane, 1 KB an instruction): while a stage is multiplied the next three are
+// in flight, up to 96 KB a CU, and one barrier a stage separates its readers
+// from the loads that fill it again.  K rows are stored with their 16-byte
+// pieces exchanged by a function of the row (piece ^ swizzle), so that the 16
+// rows of an operand lie in different banks.
+template <int D, bool F8>
+struct Stage {
+    static constexpr int ROW = D * (F8 ? 1 : 2);
+    static constexpr int KEYS = ROW == 512 ? 32 : 64;
+    static constexpr int BYTES = 2 * KEYS * ROW;
+    static constexpr int PIECES = ROW / 16;             // 16-byte pieces of a row
+    static constexpr int ROWS = 1024 / ROW;             // rows of one load instruction
+    static constexpr int SCALES = F8 ? 2 * KEYS * 4 : 16;
+    static __device__ __forceinline__ int swizzle(int key)
+    {
+        return ROW >= 256 ? key & 15 : ROW == 128 ? key >> 1 & 7 : key >> 2 & 3;
+    }
+};
+
+template <int D, bool F8, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : 1) void attn_wide_kernel(const AttnArgs A)
+{
+    using S = Stage<D, F8>;
+    using V = VLayout<D, F8>;
+    constexpr int ROW = S::ROW, KS = D / 64, THREADS = 64 * WAVES;
+    constexpr int NK = S::KEYS * ROW / 1024;            // load instructions of a stage's keys, and of its values
+    constexpr int PER = 2 * NK / WAVES;                 // of a wave
+    constexpr int ALL = PER + (F8 ? 1 : 0);             // with the scales
+    static_assert(2 * NK % WAVES == 0 && 3 * ALL < 64, "");
+    // separate arrays, so that loads into one are known not to touch the others
+    __shared__ __align__(1024) uint8_t st0[S::BYTES], st1[S::BYTES], st2[S::BYTES], st3[S::BYTES];
+    __shared__ __align__(16) uint8_t sc0[S::SCALES], sc1[S::SCALES], sc2[S::SCALES], sc3[S::SCALES];
+    __shared__ int wave_ok[WAVES];
+    extern __shared__ __align__(16) uint8_t smem[];
+    int *rows16 = reinterpret_cast<int *>(smem);        // [size / 16]
+
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, n = lane & 15, g = lane >> 4;
+    Chunk K;
+    if (!find_chunk(A, true, kCols * WAVES, K)) return;
+    const int col = (K.rt * WAVES + wave) * kCols + n;              // the lane's column
+    const bool busy = (K.rt * WAVES + wave) * kCols < K.cols;       // waves without columns only load
+    bool ok = chunk_rows(A, K, rows16, THREADS);
+    const uint32_t seen = seen_rows(A, K.r0, K.m, min(col / A.group, K.m - 1), ok);
+    bf8v q[KS][2];
+    {
+        const int qc = min(col, K.cols - 1);
+        const uint16_t *p = A.q + ((size_t)col_row(A, K, qc) * A.hq + col_head(A, K, qc)) * D + 16 * g;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) q[k][hh] = *reinterpret_cast<const bf8v *>(p + 64 * k + 8 * hh);
+    }
+    const bool mine_ok = !__ballot(!ok);
+    if (lane == 0) wave_ok[wave] = mine_ok;
+    __syncthreads();
+    bool all_ok = true;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) all_ok = all_ok && wave_ok[w];
+    if (!all_ok) {
+        if (K.nch > 1 && g == 0 && col < K.cols) A.stat[col_part(A, K, col)] = make_float2(0.0f, kSkipped);
+        return;
+    }
+
+    const int tiles = ceil_div(K.k1 - K.k0, S::KEYS);
+    // Past the last tile the loads are made all the same, each of one address, so
+    // that every wait can count on them.
+    auto fill = [&](int tile, uint8_t *stage, uint8_t *scales) {
+        const bool real = tile < tiles;
+        const int *list = rows16 + (real ? tile * S::KEYS / 16 : 0);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int i = j * WAVES + wave, ik = i % NK, key = ik * S::ROWS + lane / S::PIECES;
+            const bool is_k = i < NK;
+            const int piece = is_k ? (lane % S::PIECES) ^ S::swizzle(key) : lane % S::PIECES;
+            const size_t row = __builtin_amdgcn_readfirstlane(list[ik * S::ROWS / 16]);
+            const uint32_t off = (key % 16) * ROW + piece * 16;
+            const uint8_t *p = (is_k ? A.kv.k : A.kv.v) + row * ROW + (real ? off : 0);
+            __builtin_amdgcn_global_load_lds((global_void *)p, (lds_void *)(stage + i * 1024), 16, 0, 0);
+        }
+        if constexpr (F8) {        // even waves the keys' scales, odd ones the values'
+            const size_t row = list[lane / 16] + (real ? lane & 15 : 0);
+            const float *p = (wave & 1 ? A.kv.v_scale : A.kv.k_scale) + row;
+            __builtin_amdgcn_global_load_lds((global_void *)p, (lds_void *)(scales + (wave & 1) * S::KEYS * 4), 4, 0, 0);
+        }
+    };
+
+    Column<D, F8> C;
+    C.clear();
+    bool bad = false;
+    auto multiply = [&](int tile, const uint8_t *stage, const uint8_t *scales) {
+        // the lane's LDS addresses, worked out anew for each stage: kept for all
+        // four they would take the registers of the accumulators
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+        const int n = ln & 15, g = ln >> 4;
+#pragma unroll
+        for (int sub = 0; sub < S::KEYS / kTile; ++sub) {
+            const int first = K.k0 + tile * S::KEYS + sub * kTile;
+            if (sub > 0 && first >= K.k1) break;
+            const int key0 = first + 4 * g;
+            f4v acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int row = (sub * kTile + 16 * u + n) * ROW, sw = S::swizzle(n);
+                    if constexpr (F8) {
+                        Run16<true> x;
+                        x.load(stage + (row + (((4 * k + g) ^ sw) * 16)));
+                        acc[u] = mfma(x.get(0), q[k][0], acc[u]);
+                        acc[u] = mfma(x.get(1), q[k][1], acc[u]);
+                    } else {
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh)
+                            acc[u] = mfma(*reinterpret_cast<const bf8v *>(stage + (row + (((8 * (k & 1) + 2 * g + hh) ^ sw) + 16 * (k >> 1)) * 16)), q[k][hh], acc[u]);
+                    }
+                }
+            float4 ks[2] = {}, vs[2] = {};
+            if constexpr (F8)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    ks[u] = *reinterpret_cast<const float4 *>(scales + ((sub * kTile + 16 * u + 4 * g) * 4));
+                    vs[u] = *reinterpret_cast<const float4 *>(scales + ((S::KEYS + sub * kTile + 16 * u + 4 * g) * 4));
+                }
+            auto load_v = [&](VPart<F8, V::W> (&v)[8], int hh) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i].load(stage + ((S::KEYS + sub * kTile + 16 * (i / 4) + 4 * g + (i & 3)) * ROW + (hh * 16 + n) * V::W * 4));
+            };
+            if (first + kTile <= K.kv) {
+                const bf8v pb = C.template weights<false>(acc, A.scale, ks, vs, key0, K.kv, seen);
+#pragma unroll
+                for (int hh = 0; hh < V::NL; ++hh) {
+                    VPart<F8, V::W> v[8];
+                    load_v(v, hh);
+                    C.values(hh, v, pb);
+                }
+            } else {
+                const bf8v pb = C.template weights<true>(acc, A.scale, ks, vs, key0, K.kv, seen);
+#pragma unroll
+                for (int hh = 0; hh < V::NL; ++hh) {
+                    VPart<F8, V::W> v[8];
+                    load_v(v, hh);
+                    bad |= clean_values(v, key0, K.len, K.m);
+                    C.values(hh, v, pb);
+                }
+            }
+        }
+    };
+    fill(0, st0, sc0);
+    fill(1, st1, sc1);
+    fill(2, st2, sc2);
+    // A tile's loads are done once at most those of the two tiles after it are
+    // left; the stage of the tile before it is free when all waves are here.
+    auto step = [&](int tile, uint8_t *stage, uint8_t *scales, uint8_t *next, uint8_t *next_scales) {
+        wait_and_meet<2 * ALL>();
+        fill(tile + 3, next, next_scales);
+        if (busy && tile < tiles) multiply(tile, stage, scales);
+    };
+    for (int tile = 0; tile < tiles; tile += 4) {
+        step(tile, st0, sc0, st3, sc3);
+        step(tile + 1, st1, sc1, st0, sc0);
+        step(tile + 2, st2, sc2, st1, sc1);
+        step(tile + 3, st3, sc3, st2, sc2);
+    }
+    wait_vmem();      // no load may reach LDS that is no longer this workgroup's
+
+    const float l = sum_rows4(C.sum);
+    if (col >= K.cols) return;
+    if (K.nch > 1 && g == 0) A.stat[col_part(A, K, col)] = make_float2(C.mx, l);
+#pragma unroll
+    for (int hh = 0; hh < V::NL; ++hh)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < V::EPL; i += 4) {
+                const int d = hh * 16 * V::EPL + (4 * g + e) * V::EPL + i;
+                const f4v *o = C.o + hh * V::EPL + i;
+                float4 a = make_float4(o[0][e], o[1][e], o[2][e], o[3][e]);
+                if (bad) add_bad<D, F8>(A, a, rows16, seen, max(K.kv, K.k0), K.k1, K.kv, K.k0, d);
+                put4<D>(A, K, col, a, l, d);
+            }
 }
 
 // Merges a (row, head)'s chunks.  D / 4 lanes share the channels, the rest of
 // the workgroup splits the chunks.
 template <int D>
-__global__ __launch_bounds__(256) void join_kernel(const AttnArgs A)
+__global__ __launch_bounds__(256) void join_kernel(const AttnArgs A, const int is_wide)
 {
     constexpr int LANES = D / 4, PARTS = 256 / LANES;
     __shared__ float w[kMaxChunks];
@@ -508,24 +797,21 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs A)
     }
     int r0, m, kv;
     if (!stream_window(A, lo, r0, m, kv) || r < r0 || r >= r0 + m) return;
-    const int nch = chunk_count(kv + m);
+    const int nch = chunk_count(kv + m, is_wide);
     if (nch <= 1) return;
     const size_t at = ((size_t)r * A.hq + head) * A.chunks;
-    float2 st = {-INFINITY, 0.0f}, st2 = st;
+    float2 st = {-INFINITY, 0.0f};
     const int lane = tid & 63;
+    static_assert(kMaxChunks == 64, "");
     if (lane < nch) st = A.stat[at + lane];
-    if (lane + 64 < nch) st2 = A.stat[at + 64 + lane];
-    if (__ballot(st.y < 0.0f || st2.y < 0.0f)) return;      // a chunk was skipped: so is the stream
-    float top = fmaxf(st.x, st2.x);
+    if (__ballot(st.y < 0.0f)) return;                      // a chunk was skipped: so is the stream
+    float top = st.x;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
     const float base = top == -INFINITY ? 0.0f : top;
-    const float f = __builtin_amdgcn_exp2f(st.x - base), f2 = __builtin_amdgcn_exp2f(st2.x - base);
-    const float l = sum_wave(st.y * f + st2.y * f2);
-    if (tid < 64) {
-        w[lane] = f;
-        w[lane + 64] = f2;
-    }
+    const float f = __builtin_amdgcn_exp2f(st.x - base);
+    const float l = sum_wave(st.y * f);
+    if (tid < 64) w[lane] = f;
     __syncthreads();
     const int d4 = tid % LANES, part = tid / LANES;
     float4 a = {0, 0, 0, 0};
@@ -546,48 +832,79 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs A)
     }
 }
 
-template <int D, bool F8>
-hipError_t launch_d(const AttnArgs &A, hipStream_t stream)
+template <typename F>
+hipError_t allow_lds(F *kernel, int dynamic)
 {
-    const size_t lds = sizeof(float) * kAttnWaves * kCols * (D + 4 + 2) + D * 2 * kCols
-                       + sizeof(int) * (4 + kCols + chunk_keys(A.max_kv) / 16);
-    static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(attn_kernel<D, F8>),
-                                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)kRowsMaxLds);
+    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, dynamic);
+}
+
+constexpr int kMaxRows16 = kMaxAttnKeys / kMaxChunks / 16;     // cache rows a workgroup lists at most
+
+template <int D, bool F8, int WAVES>
+hipError_t launch_wide(const AttnArgs &A, unsigned blocks, size_t rows16, hipStream_t stream)
+{
+    static const hipError_t e = allow_lds(attn_wide_kernel<D, F8, WAVES>, sizeof(int) * kMaxRows16);
     if (e != hipSuccess) return e;
-    const long long blocks = (long long)A.chunks * A.kv.hkv * A.row_tiles * A.n_streams;
-    hipLaunchKernelGGL((attn_kernel<D, F8>), dim3((unsigned)blocks), dim3(kAttnThreads), lds, stream, A);
+    hipLaunchKernelGGL((attn_wide_kernel<D, F8, WAVES>), dim3(blocks), dim3(64 * WAVES), rows16, stream, A);
+    return hipSuccess;
+}
+
+template <int D, bool F8>
+hipError_t launch_d(const AttnArgs &A, bool wide, int waves, hipStream_t stream)
+{
+    const unsigned blocks = (unsigned)(A.chunks * A.kv.hkv * A.row_tiles * A.n_streams);
+    const size_t rows16 = sizeof(int) * (chunk_keys(A.max_kv, wide) / 16);
+    hipError_t e = hipSuccess;
+    if (!wide) {
+        constexpr size_t lds = sizeof(float) * kAttnWaves * kCols * (D + 4 + 2) + D * 2 * kCols + sizeof(int) * (4 + kCols);
+        static const hipError_t set = allow_lds(attn_kernel<D, F8>, lds + sizeof(int) * kMaxRows16);
+        if (set != hipSuccess) return set;
+        hipLaunchKernelGGL((attn_kernel<D, F8>), dim3(blocks), dim3(kAttnThreads), lds + rows16, stream, A);
+    } else {
+        e = waves == 4 ? launch_wide<D, F8, 4>(A, blocks, rows16, stream) : launch_wide<D, F8, 8>(A, blocks, rows16, stream);
+        if (e != hipSuccess) return e;
+    }
     if (A.chunks > 1)
-        hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)(A.total_rows * A.hq)), dim3(256), 0, stream, A);
+        hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)(A.total_rows * A.hq)), dim3(256), 0, stream, A, wide ? 1 : 0);
     return hipGetLastError();
+}
+
+// Waves of a wide workgroup: four (64 columns) where the window needs no more.
+int wide_waves(int cols) { return cols <= 4 * kCols ? 4 : 8; }
+
+int column_tiles(int max_rows, int group)
+{
+    const int cols = max_rows * group;
+    return is_wide(max_rows, group) ? ceil_div(cols, kCols * wide_waves(cols)) : 1;
 }
 
 }  // namespace
 
 size_t attn_workspace_bytes(int hq, int hkv, int d, int total_rows, int max_rows, int max_kv)
 {
-    const size_t chunks = chunk_bound(max_kv);
+    const size_t chunks = chunk_bound(max_kv, is_wide(max_rows, hq / hkv));
     if (chunks <= 1) return 0;
     return (size_t)total_rows * hq * chunks * (sizeof(float) * d + sizeof(float2));
 }
 
 bool attn_fits(const AttnArgs &A)
 {
-    const long long tiles = (A.max_rows * A.group + kCols - 1) / kCols;
-    return (long long)chunk_bound(A.max_kv) * A.kv.hkv * tiles <= 0x7fffffffLL / A.n_streams
-           && (long long)A.total_rows * A.hq <= 0x7fffffffLL;
+    const long long tiles = column_tiles(A.max_rows, A.group), chunks = chunk_bound(A.max_kv, is_wide(A.max_rows, A.group));
+    return chunks * A.kv.hkv * tiles <= 0x7fffffffLL / A.n_streams && (long long)A.total_rows * A.hq <= 0x7fffffffLL;
 }
 
 hipError_t launch_attn(AttnArgs A, void *workspace, hipStream_t stream)
 {
-    A.chunks = chunk_bound(A.max_kv);
-    A.row_tiles = (A.max_rows * A.group + kCols - 1) / kCols;
+    const bool wide = is_wide(A.max_rows, A.group), f8 = A.kv.k_scale != nullptr;
+    const int waves = wide_waves(A.max_rows * A.group);
+    A.chunks = chunk_bound(A.max_kv, wide);
+    A.row_tiles = column_tiles(A.max_rows, A.group);
     A.part = static_cast<float *>(workspace);
     A.stat = reinterpret_cast<float2 *>(A.part + (size_t)A.total_rows * A.hq * A.chunks * A.kv.d);
-    const bool f8 = A.kv.k_scale != nullptr;
     switch (A.kv.d) {
-    case 64: return f8 ? launch_d<64, true>(A, stream) : launch_d<64, false>(A, stream);
-    case 128: return f8 ? launch_d<128, true>(A, stream) : launch_d<128, false>(A, stream);
-    default: return f8 ? launch_d<256, true>(A, stream) : launch_d<256, false>(A, stream);
+    case 64: return f8 ? launch_d<64, true>(A, wide, waves, stream) : launch_d<64, false>(A, wide, waves, stream);
+    case 128: return f8 ? launch_d<128, true>(A, wide, waves, stream) : launch_d<128, false>(A, wide, waves, stream);
+    default: return f8 ? launch_d<256, true>(A, wide, waves, stream) : launch_d<256, false>(A, wide, waves, stream);
     }
 }
 
