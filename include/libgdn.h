@@ -399,7 +399,7 @@ int gdn_attn_prep(const gdn_kv_cache *cache, int32_t rows, int32_t hq, const uin
  *     out = sigmoid(gate) * softmax(scale q K^T) V.
  *   q, out [total_rows][hq][d] bf16;  gate bf16 with row and head strides in
  *     elements (multiples of 4; 8-byte aligned), or NULL
- *   max_rows 1..16 and max_kv (at most 2^22): bounds on every window's rows and
+ *   max_rows 1..16 and max_kv (at most 2^21): bounds on every window's rows and
  *     on kv_len[s] + its rows
  *   workspace: gdn_attn_workspace_bytes() of device memory, 16-byte aligned
  *     (NULL where that is 0); its contents need not be kept between calls, and

@@ -63,7 +63,7 @@ def test_bad_caches_are_refused_everywhere(L, kw, code, needle):
     (dict(n=-1), gdn.GDN_EINVAL, "negative"), (dict(total=-1), gdn.GDN_EINVAL, "negative"),
     (dict(max_rows=0), gdn.GDN_EINVAL, "max_rows"), (dict(max_rows=17), gdn.GDN_EINVAL, "max_rows"),
     (dict(total=257), gdn.GDN_EINVAL, "exceeds"), (dict(max_kv=0), gdn.GDN_EINVAL, "max_kv"),
-    (dict(max_kv=(1 << 22) + 1), gdn.GDN_EUNSUPPORTED, "max_kv"), (dict(blocks=0), gdn.GDN_EINVAL, "max_blocks"),
+    (dict(max_kv=(1 << 21) + 1), gdn.GDN_EUNSUPPORTED, "max_kv"), (dict(blocks=0), gdn.GDN_EINVAL, "max_blocks"),
     (dict(blocks=1 << 26), gdn.GDN_EUNSUPPORTED, "max_blocks"), (dict(hq=22), gdn.GDN_EINVAL, "multiple"),
     (dict(hq=0), gdn.GDN_EINVAL, "multiple"), (dict(hq=2048), gdn.GDN_EUNSUPPORTED, "hq"),
     (dict(rs=None), gdn.GDN_EINVAL, "row_start"), (dict(kv=None), gdn.GDN_EINVAL, "kv_len"),
@@ -73,7 +73,7 @@ def test_bad_caches_are_refused_everywhere(L, kw, code, needle):
     (dict(scale=float("nan")), gdn.GDN_EINVAL, "scale"), (dict(scale=float("inf")), gdn.GDN_EINVAL, "scale"),
     (dict(ws=None), gdn.GDN_EWORKSPACE, "workspace"), (dict(wsb=100), gdn.GDN_EWORKSPACE, "workspace"),
     (dict(ws=P8), gdn.GDN_EINVAL, "workspace must be"),
-    (dict(n=1 << 24, total=1, max_kv=1 << 22), gdn.GDN_EUNSUPPORTED, "too many"),
+    (dict(n=1 << 24, total=1, max_kv=1 << 21), gdn.GDN_EUNSUPPORTED, "too many"),
 ])
 def test_window_refusals(L, kw, code, needle):
     refused(L, window(L, **kw), code, needle)
@@ -142,7 +142,7 @@ def test_workspace_bytes(L):
         assert need(**bad) == 0
     assert need() > 0 and need(total_rows=512, n_streams=32) == 2 * need()
     # a longer bound never needs less
-    sizes = [need(max_kv=m) for m in (1, 100, 1000, 5000, 16000, 16384, 16385, 20000, 40000, 262144, 1 << 22)]
+    sizes = [need(max_kv=m) for m in (1, 100, 1000, 5000, 16000, 16384, 16385, 20000, 40000, 262144, 1 << 21)]
     assert sizes == sorted(sizes)
 
 

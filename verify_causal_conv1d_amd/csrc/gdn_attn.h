@@ -38,7 +38,6 @@ struct AttnArgs {
     int32_t n_streams, total_rows, max_rows, max_kv, max_blocks;
     int32_t hq, group;           // query heads, and query heads of a kv head
     int32_t chunks;              // chunks the longest stream has: partials are [total_rows][hq][chunks]
-    int32_t row_tiles;           // tiles of (row, head in group) pairs a stream's window has at most
     const int32_t *row_start, *parent, *kv_len, *table;
     const uint16_t *q, *gate;    // q [total_rows][hq][d]; gate strided, or NULL
     int64_t gate_row, gate_head;
@@ -55,7 +54,7 @@ struct AttnCommitArgs {
     int32_t *kv_len_out;
 };
 
-constexpr int kMaxAttnKeys = 1 << 22;    // of one stream: a workgroup lists its chunk's pages in LDS
+constexpr int kMaxAttnKeys = 1 << 21;    // of one stream: a workgroup lists its chunk's pages in LDS
 constexpr int kMaxTableStreams = 4096;   // a workgroup keeps six ints of each in LDS
 
 size_t attn_workspace_bytes(int hq, int hkv, int d, int total_rows, int max_rows, int max_kv);

@@ -32,29 +32,28 @@ namespace {
 
 constexpr int kTile = 32;                  // keys of a wave's step
 constexpr int kCols = 16;                  // (row, head) pairs of a column tile
-constexpr int kChunkUnit = 128;            // chunks are whole multiples of it
 constexpr int kMaxChunks = 64;             // of one stream
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 __host__ __device__ inline int at_least(int a, int b) { return a > b ? a : b; }
 __host__ __device__ inline int at_most(int a, int b) { return a < b ? a : b; }
 
-// Keys of a chunk of a stream with len keys: short chunks (lo) up to kMidChunks
-// of them, then longer ones up to mid, then up to kMaxChunks of mid, then longer.
+// Keys of a chunk of a stream with len keys: as many equal chunks, in whole
+// units, as there would be of lo keys (up to kMidChunks), then of up to mid
+// keys, then of more than that (kMaxChunks).
 constexpr int kMidChunks = 32;
 __host__ __device__ inline int chunk_lo(bool wide) { return wide ? 512 : 256; }
 __host__ __device__ inline int chunk_mid(bool wide) { return wide ? 1024 : 512; }
+__host__ __device__ inline int chunk_unit(bool wide) { return wide ? 64 : 128; }
 
 __host__ __device__ inline int chunk_keys(int len, bool wide)
 {
-    const int c = at_least(at_least(chunk_lo(wide), at_most(chunk_mid(wide), ceil_div(len, kMidChunks))), ceil_div(len, kMaxChunks));
-    return kChunkUnit * ceil_div(c, kChunkUnit);
+    const int most = at_least(at_least(chunk_lo(wide), at_most(chunk_mid(wide), ceil_div(len, kMidChunks))), ceil_div(len, kMaxChunks));
+    const int unit = chunk_unit(wide);
+    return unit * ceil_div(ceil_div(len, ceil_div(len, most)), unit);
 }
 
-__host__ __device__ inline int chunk_count(int len, bool wide)
-{
-    return len <= 0 ? 0 : ceil_div(len, chunk_keys(len, wide));
-}
+__host__ __device__ inline int chunk_count(int len, bool wide) { return len <= 0 ? 0 : ceil_div(len, chunk_keys(len, wide)); }
 
 // The most chunks that a stream of up to max_kv keys can have.
 inline int chunk_bound(int max_kv, bool wide)
@@ -90,6 +89,15 @@ __device__ __forceinline__ uint32_t seen_rows(const AttnArgs &A, int r0, int m, 
             if (p >= 0 && (bits >> u & 1)) bits |= 1u << p;
         }
     return bits;
+}
+
+// The thread's number, as a value that the compiler cannot trace: what is worked
+// out from it inside a loop stays there, instead of taking registers from the
+// accumulators all through it.
+__device__ __forceinline__ int fresh(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
 }
 
 // ---- operands in registers ---------------------------------------------------
@@ -300,7 +308,12 @@ struct Column {
         float tm = p[0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) tm = fmaxf(tm, p[i]);
-        tm = fmaxf(mx, max_rows4(tm));
+        // Any base within reach of the maximum does: it moves up only when the
+        // maximum has passed it by 2^8, so that O is rarely scaled again (with the
+        // maximum itself, by every second tile of 16 columns).  Weights stay below
+        // 2^8, and P and the sums are floating point.
+        tm = max_rows4(tm);
+        tm = tm > mx + 8.0f ? tm : mx;
         const float base = tm == -INFINITY ? 0.0f : tm;     // no key seen so far: every p is 0
         const float back = __builtin_amdgcn_exp2f(mx - base);
         mx = tm;
@@ -334,14 +347,20 @@ struct Column {
         const uint4 pw = {pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
         return __builtin_bit_cast(bf8v, pw);
     }
-
-    // O^T += V^T P^T for the channels of load h
-    __device__ __forceinline__ void values(int h, const VPart<F8, V::W> (&v)[8], bf8v pb)
-    {
-#pragma unroll
-        for (int i = 0; i < V::EPL; ++i) o[h * V::EPL + i] = mfma(v_operand(v, i), pb, o[h * V::EPL + i]);
-    }
 };
+
+// O^T += V^T P^T for the channels of load h, for each of a wave's column tiles
+template <int D, bool F8, int T>
+__device__ __forceinline__ void add_values(Column<D, F8> (&C)[T], int h, const VPart<F8, VLayout<D, F8>::W> (&v)[8], const bf8v (&pb)[T])
+{
+    constexpr int EPL = VLayout<D, F8>::EPL;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const bf8v a = v_operand(v, i);
+#pragma unroll
+        for (int t = 0; t < T; ++t) C[t].o[h * EPL + i] = mfma(a, pb[t], C[t].o[h * EPL + i]);
+    }
+}
 
 // Values of a tile that holds keys of the window or past the end.  Rows past
 // the end hold anything: zeros instead.  And 0 * inf is NaN: an infinite or NaN
@@ -363,38 +382,87 @@ __device__ __forceinline__ bool clean_values(VPart<F8, W> (&v)[8], int key0, int
     return true;
 }
 
-// The chunk of a workgroup.
+// One piece of work: a chunk of a stream's keys, for one kv head and one tile of
+// columns.
 struct Chunk {
-    int s, h, rt, c;          // stream, kv head, tile of columns, chunk
-    int r0, m, kv, len;       // the stream's window, cached rows, keys in all
+    int h, rt, c;             // kv head, tile of columns, chunk
+    int s, r0, m, kv, len;    // the stream, its window, cached rows, keys in all
     int k0, k1, nch;          // the chunk's keys, and chunks of the stream
     int size;                 // keys of a full chunk
     int cols;                 // (row, head) pairs of the stream
 };
 
-// The chunk of this workgroup, tile_cols columns wide; false if there is none.
-__device__ __forceinline__ bool find_chunk(const AttnArgs &A, bool wide, int tile_cols, Chunk &K)
-{
-    int x = blockIdx.x;
-    K.c = x % A.chunks;
-    x /= A.chunks;
-    K.h = x % A.kv.hkv;
-    x /= A.kv.hkv;
-    K.rt = x % A.row_tiles;
-    K.s = x / A.row_tiles;
-    if (!stream_window(A, K.s, K.r0, K.m, K.kv)) return false;
-    K.len = K.kv + K.m;
-    K.size = chunk_keys(K.len, wide);
-    K.k0 = K.c * K.size;
-    K.k1 = min(K.k0 + K.size, K.len);
-    K.nch = chunk_count(K.len, wide);
-    K.cols = K.m * A.group;
-    return K.k0 < K.len && K.rt * tile_cols < K.cols;
-}
+// The pieces of all streams, in stream order.  How many there are follows from
+// the lengths, which only the device knows.  Every wave finds its pieces by
+// itself, with no workgroup for a piece that is not there before those that
+// are: lane l holds stream first + l of a block of 64 streams, and the pieces of
+// the block up to and including that stream's.
+struct Pieces {
+    int first = -64, before = 0, incl = 0;    // of the block: first stream, pieces before it, running sum
+    int r0 = 0, m = 0, kv = 0;
+
+    __device__ __forceinline__ void load(const AttnArgs &A, bool wide, int tile_cols, int block)
+    {
+        const int lane = threadIdx.x & 63, s = block + lane;
+        first = block;
+        int count = 0;
+        if (s < A.n_streams && stream_window(A, s, r0, m, kv))
+            count = chunk_count(kv + m, wide) * A.kv.hkv * ceil_div(m * A.group, tile_cols);
+        incl = count;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int up = __shfl_up(incl, o);
+            if (lane >= o) incl += up;
+        }
+    }
+
+    // piece `at` of the block's
+    __device__ __forceinline__ void get(const AttnArgs &A, bool wide, int at, Chunk &K) const
+    {
+        const int l = __builtin_ctzll(__ballot(incl > at));
+        int x = at - (l ? __builtin_amdgcn_readlane(incl, l - 1) : 0);
+        K.s = first + l;
+        K.r0 = __builtin_amdgcn_readlane(r0, l);
+        K.m = __builtin_amdgcn_readlane(m, l);
+        K.kv = __builtin_amdgcn_readlane(kv, l);
+        K.len = K.kv + K.m;
+        K.nch = chunk_count(K.len, wide);
+        K.size = chunk_keys(K.len, wide);
+        K.cols = K.m * A.group;
+        K.c = x % K.nch;
+        x /= K.nch;
+        K.h = x % A.kv.hkv;
+        K.rt = x / A.kv.hkv;
+        K.k0 = K.c * K.size;
+        K.k1 = min(K.k0 + K.size, K.len);
+    }
+
+    // piece `at` of the block of 64 streams from `block`; false if it has fewer
+    __device__ __forceinline__ bool find_in_block(const AttnArgs &A, bool wide, int tile_cols, int block, int at, Chunk &K)
+    {
+        load(A, wide, tile_cols, block);
+        if (at >= __builtin_amdgcn_readlane(incl, 63)) return false;
+        get(A, wide, at, K);
+        return true;
+    }
+
+    // piece `item` of all (not less than in the call before); false if there is none
+    __device__ __forceinline__ bool find(const AttnArgs &A, bool wide, int tile_cols, int item, Chunk &K)
+    {
+        while (item >= before + __builtin_amdgcn_readlane(incl, 63)) {
+            before += __builtin_amdgcn_readlane(incl, 63);
+            if (first + 64 >= A.n_streams) return false;
+            load(A, wide, tile_cols, first + 64);
+        }
+        get(A, wide, item - before, K);
+        return true;
+    }
+};
 
 // Cache rows of the chunk's keys, 16 at a time (pages hold multiples of 16) up
 // to the chunk's full size: past the stream's end those of its last keys, so
 // that every load stays in its pages.  false if a page is not in the cache.
+// (For the caller's wave: whether its share of them is.)
 __device__ __forceinline__ bool chunk_rows(const AttnArgs &A, const Chunk &K, int *rows16, int threads)
 {
     bool ok = true;
@@ -405,7 +473,7 @@ __device__ __forceinline__ bool chunk_rows(const AttnArgs &A, const Chunk &K, in
         ok = ok && good;
         rows16[i] = good ? ((id * A.kv.hkv + K.h) << A.kv.page_shift) + (key & ((1 << A.kv.page_shift) - 1)) : 0;
     }
-    return ok;
+    return !__ballot(!ok);
 }
 
 // Packed row and query head of a stream's column.
@@ -448,9 +516,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
     uint32_t *seen_lds = reinterpret_cast<uint32_t *>(bad_lds + 4);    // [kCols]: the window's rows that a column sees
     int *rows16 = bad_lds + 4 + kCols;                                 // [size / 16]
 
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, g = lane >> 4;
+    Pieces pieces;
     Chunk K;
-    if (!find_chunk(A, false, kCols, K)) return;
+    if (!pieces.find_in_block(A, false, kCols, 64 * blockIdx.y, blockIdx.x, K)) return;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, g = lane >> 4;
     const int col0 = K.rt * kCols, ncol = min(K.cols - col0, kCols);
     bool ok = chunk_rows(A, K, rows16, kAttnThreads);
     const uint32_t seen = seen_rows(A, K.r0, K.m, min((col0 + n) / A.group, K.m - 1), ok);
@@ -464,9 +533,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
                                                  + 64 * k + 16 * qg + 8 * hh);
         q_lds[i] = x;
     }
-    const bool wave_ok = !__ballot(!ok);
     static_assert(kAttnWaves == 4, "");
-    if (lane == 0) l_lds[wave] = wave_ok ? 1.0f : 0.0f;     // free until the waves join
+    if (lane == 0) l_lds[wave] = ok ? 1.0f : 0.0f;          // free until the waves join
     if (tid == 0) *bad_lds = 0;
     if (tid < kCols) seen_lds[tid] = seen;
     __syncthreads();
@@ -475,8 +543,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
         return;
     }
 
-    Column<D, F8> C;
-    C.clear();
+    Column<D, F8> C[1];
+    C[0].clear();
     Run16<F8> kk[2][KS];
     VPart<F8, V::W> vv[V::NL][8];
     const uint32_t k_off = n * ROW + 16 * g * ESZ, v_off = 4 * g * ROW + n * V::W * 4;
@@ -525,28 +593,28 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
                 vs[u] = *reinterpret_cast<const float4 *>(A.kv.v_scale + row + 4 * g);
             }
         if (K.k0 + tile * kTile + kTile <= K.kv) {
-            const bf8v pb = C.template weights<false>(acc, A.scale, ks, vs, key0, K.kv, seen);
+            const bf8v pb[1] = {C[0].template weights<false>(acc, A.scale, ks, vs, key0, K.kv, seen)};
 #pragma unroll
-            for (int hh = 0; hh < V::NL; ++hh) C.values(hh, vv[hh], pb);
+            for (int hh = 0; hh < V::NL; ++hh) add_values(C, hh, vv[hh], pb);
         } else {
-            const bf8v pb = C.template weights<true>(acc, A.scale, ks, vs, key0, K.kv, seen);
+            const bf8v pb[1] = {C[0].template weights<true>(acc, A.scale, ks, vs, key0, K.kv, seen)};
 #pragma unroll
             for (int hh = 0; hh < V::NL; ++hh) {
                 if (clean_values(vv[hh], key0, K.len, K.m) && lane == 0) *bad_lds = 1;
-                C.values(hh, vv[hh], pb);
+                add_values(C, hh, vv[hh], pb);
             }
         }
         if (more) load_v(tile + kAttnWaves);
     }
 
     // join the waves: the column's maximum over them, each wave's O and l scaled to it
-    const float sum = sum_rows4(C.sum);
-    if (g == 0) m_lds[wave * kCols + n] = C.mx;
+    const float sum = sum_rows4(C[0].sum);
+    if (g == 0) m_lds[wave * kCols + n] = C[0].mx;
     __syncthreads();
     float top = m_lds[n];
 #pragma unroll
     for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, m_lds[w * kCols + n]);
-    const float f = __builtin_amdgcn_exp2f(C.mx - (top == -INFINITY ? 0.0f : top));
+    const float f = __builtin_amdgcn_exp2f(C[0].mx - (top == -INFINITY ? 0.0f : top));
     if (g == 0) l_lds[wave * kCols + n] = sum * f;
     if (n < ncol) {
         float *row = o_lds + (wave * kCols + n) * OP;
@@ -555,7 +623,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float *p = row + hh * 16 * V::EPL + (4 * g + e) * V::EPL;
-                const f4v *o = C.o + hh * V::EPL;
+                const f4v *o = C[0].o + hh * V::EPL;
 #pragma unroll
                 for (int i = 0; i < V::EPL; i += 4)
                     *reinterpret_cast<float4 *>(p + i) = make_float4(o[i][e] * f, o[i + 1][e] * f, o[i + 2][e] * f, o[i + 3][e] * f);
@@ -615,104 +683,106 @@ struct Stage {
     }
 };
 
-template <int D, bool F8, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : 1) void attn_wide_kernel(const AttnArgs A)
+constexpr int kWideWaves = 8, kWideThreads = 64 * kWideWaves, kWideTiles = 1;
+constexpr int kWideCols = kCols * kWideTiles * kWideWaves;
+
+template <int D, bool F8>
+__global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnArgs A, const int list_size)
 {
     using S = Stage<D, F8>;
     using V = VLayout<D, F8>;
-    constexpr int ROW = S::ROW, KS = D / 64, THREADS = 64 * WAVES;
+    constexpr int ROW = S::ROW, KS = D / 64, T = kWideTiles;
     constexpr int NK = S::KEYS * ROW / 1024;            // load instructions of a stage's keys, and of its values
-    constexpr int PER = 2 * NK / WAVES;                 // of a wave
+    constexpr int PER = 2 * NK / kWideWaves;            // of a wave
     constexpr int ALL = PER + (F8 ? 1 : 0);             // with the scales
-    static_assert(2 * NK % WAVES == 0 && 3 * ALL < 64, "");
+    static_assert(2 * NK % kWideWaves == 0 && 3 * ALL < 64, "");
     // separate arrays, so that loads into one are known not to touch the others
     __shared__ __align__(1024) uint8_t st0[S::BYTES], st1[S::BYTES], st2[S::BYTES], st3[S::BYTES];
     __shared__ __align__(16) uint8_t sc0[S::SCALES], sc1[S::SCALES], sc2[S::SCALES], sc3[S::SCALES];
-    __shared__ int wave_ok[WAVES];
+    __shared__ int wave_ok[2][kWideWaves];
     extern __shared__ __align__(16) uint8_t smem[];
-    int *rows16 = reinterpret_cast<int *>(smem);        // [size / 16]
+    int *rows16 = reinterpret_cast<int *>(smem);        // [2][list_size]
 
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, n = lane & 15, g = lane >> 4;
-    Chunk K;
-    if (!find_chunk(A, true, kCols * WAVES, K)) return;
-    const int col = (K.rt * WAVES + wave) * kCols + n;              // the lane's column
-    const bool busy = (K.rt * WAVES + wave) * kCols < K.cols;       // waves without columns only load
-    bool ok = chunk_rows(A, K, rows16, THREADS);
-    const uint32_t seen = seen_rows(A, K.r0, K.m, min(col / A.group, K.m - 1), ok);
-    bf8v q[KS][2];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Pieces pieces;
+    Chunk K, N;                 // the piece at work and the next one
+    int item = blockIdx.x, at = 0;
+    if (!pieces.find(A, true, kWideCols, item, K)) return;
+    // A piece's list of cache rows is made while the piece before it is at work,
+    // and the loads of its first tiles are under way before that one ends.
+    int list = 0, next_list = list_size;
     {
-        const int qc = min(col, K.cols - 1);
-        const uint16_t *p = A.q + ((size_t)col_row(A, K, qc) * A.hq + col_head(A, K, qc)) * D + 16 * g;
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) q[k][hh] = *reinterpret_cast<const bf8v *>(p + 64 * k + 8 * hh);
+        const bool ok = chunk_rows(A, K, rows16 + list, kWideThreads);
+        if (threadIdx.x % 64 == 0) wave_ok[at][wave] = ok;
     }
-    const bool mine_ok = !__ballot(!ok);
-    if (lane == 0) wave_ok[wave] = mine_ok;
-    __syncthreads();
-    bool all_ok = true;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) all_ok = all_ok && wave_ok[w];
-    if (!all_ok) {
-        if (K.nch > 1 && g == 0 && col < K.cols) A.stat[col_part(A, K, col)] = make_float2(0.0f, kSkipped);
-        return;
-    }
+    lds_barrier();
 
-    const int tiles = ceil_div(K.k1 - K.k0, S::KEYS);
-    // Past the last tile the loads are made all the same, each of one address, so
-    // that every wait can count on them.
-    auto fill = [&](int tile, uint8_t *stage, uint8_t *scales) {
-        const bool real = tile < tiles;
-        const int *list = rows16 + (real ? tile * S::KEYS / 16 : 0);
+    int tiles = ceil_div(K.k1 - K.k0, S::KEYS);
+    // Tile `tile` of a list of `count` into a stage.  Past the last one the loads
+    // are made all the same, each of one address, so that every wait can count
+    // on them.
+    auto fill = [&](int rows, int tile, int count, uint8_t *stage, uint8_t *scales) {
+        const bool real = tile < count;
+        const int lane = fresh(threadIdx.x) & 63;
+        rows += real ? tile * S::KEYS / 16 : 0;
+        int row[PER], scale_row = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) row[j] = rows16[rows + (j * kWideWaves + wave) % NK * S::ROWS / 16];
+        if constexpr (F8) scale_row = rows16[rows + lane / 16] + (real ? lane & 15 : 0);
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int i = j * WAVES + wave, ik = i % NK, key = ik * S::ROWS + lane / S::PIECES;
+            const int i = j * kWideWaves + wave, key = i % NK * S::ROWS + lane / S::PIECES;
             const bool is_k = i < NK;
             const int piece = is_k ? (lane % S::PIECES) ^ S::swizzle(key) : lane % S::PIECES;
-            const size_t row = __builtin_amdgcn_readfirstlane(list[ik * S::ROWS / 16]);
             const uint32_t off = (key % 16) * ROW + piece * 16;
-            const uint8_t *p = (is_k ? A.kv.k : A.kv.v) + row * ROW + (real ? off : 0);
+            const uint8_t *p = (is_k ? A.kv.k : A.kv.v) + (size_t)__builtin_amdgcn_readfirstlane(row[j]) * ROW + (real ? off : 0);
             __builtin_amdgcn_global_load_lds((global_void *)p, (lds_void *)(stage + i * 1024), 16, 0, 0);
         }
         if constexpr (F8) {        // even waves the keys' scales, odd ones the values'
-            const size_t row = list[lane / 16] + (real ? lane & 15 : 0);
-            const float *p = (wave & 1 ? A.kv.v_scale : A.kv.k_scale) + row;
+            const float *p = (wave & 1 ? A.kv.v_scale : A.kv.k_scale) + (size_t)scale_row;
             __builtin_amdgcn_global_load_lds((global_void *)p, (lds_void *)(scales + (wave & 1) * S::KEYS * 4), 4, 0, 0);
         }
     };
 
-    Column<D, F8> C;
-    C.clear();
-    bool bad = false;
+    Column<D, F8> C[T];
+    uint32_t seen[T];
+    bf8v q[T][KS][2];
+    int col0 = 0;
+    bool busy = false, bad = false;
     auto multiply = [&](int tile, const uint8_t *stage, const uint8_t *scales) {
-        // the lane's LDS addresses, worked out anew for each stage: kept for all
-        // four they would take the registers of the accumulators
-        int ln = lane;
-        asm volatile("" : "+v"(ln));
-        const int n = ln & 15, g = ln >> 4;
+        const int lane = fresh(threadIdx.x) & 63, n = lane & 15, g = lane >> 4;
 #pragma unroll
         for (int sub = 0; sub < S::KEYS / kTile; ++sub) {
             const int first = K.k0 + tile * S::KEYS + sub * kTile;
             if (sub > 0 && first >= K.k1) break;
             const int key0 = first + 4 * g;
-            f4v acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+            // all reads of the keys first, then the products as they arrive, then
+            // the reads of the first values, to be there when the weights are
+            Run16<F8> kk[2][KS];
 #pragma unroll
             for (int k = 0; k < KS; ++k)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int row = (sub * kTile + 16 * u + n) * ROW, sw = S::swizzle(n);
                     if constexpr (F8) {
-                        Run16<true> x;
-                        x.load(stage + (row + (((4 * k + g) ^ sw) * 16)));
-                        acc[u] = mfma(x.get(0), q[k][0], acc[u]);
-                        acc[u] = mfma(x.get(1), q[k][1], acc[u]);
+                        kk[u][k].load(stage + (row + (((4 * k + g) ^ sw) * 16)));
                     } else {
-#pragma unroll
-                        for (int hh = 0; hh < 2; ++hh)
-                            acc[u] = mfma(*reinterpret_cast<const bf8v *>(stage + (row + (((8 * (k & 1) + 2 * g + hh) ^ sw) + 16 * (k >> 1)) * 16)), q[k][hh], acc[u]);
+                        kk[u][k].a = *reinterpret_cast<const uint4 *>(stage + (row + (((8 * (k & 1) + 2 * g) ^ sw) + 16 * (k >> 1)) * 16));
+                        kk[u][k].b = *reinterpret_cast<const uint4 *>(stage + (row + (((8 * (k & 1) + 2 * g + 1) ^ sw) + 16 * (k >> 1)) * 16));
                     }
                 }
+            __builtin_amdgcn_sched_barrier(0);
+            f4v acc[T][2];
+#pragma unroll
+            for (int c = 0; c < T; ++c) acc[c][0] = acc[c][1] = f4v{0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int c = 0; c < T; ++c) acc[c][u] = mfma(kk[u][k].get(hh), q[c][k][hh], acc[c][u]);
             float4 ks[2] = {}, vs[2] = {};
             if constexpr (F8)
 #pragma unroll
@@ -720,64 +790,111 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : 1) void attn_wide_kern
                     ks[u] = *reinterpret_cast<const float4 *>(scales + ((sub * kTile + 16 * u + 4 * g) * 4));
                     vs[u] = *reinterpret_cast<const float4 *>(scales + ((S::KEYS + sub * kTile + 16 * u + 4 * g) * 4));
                 }
-            auto load_v = [&](VPart<F8, V::W> (&v)[8], int hh) {
+            VPart<F8, V::W> v[V::NL][8];
+            auto load_v = [&](int hh) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    v[i].load(stage + ((S::KEYS + sub * kTile + 16 * (i / 4) + 4 * g + (i & 3)) * ROW + (hh * 16 + n) * V::W * 4));
+                    v[hh][i].load(stage + ((S::KEYS + sub * kTile + 16 * (i / 4) + 4 * g + (i & 3)) * ROW + (hh * 16 + n) * V::W * 4));
             };
-            if (first + kTile <= K.kv) {
-                const bf8v pb = C.template weights<false>(acc, A.scale, ks, vs, key0, K.kv, seen);
+            load_v(0);
+            __builtin_amdgcn_sched_barrier(0);
+            bf8v pb[T];
+            const bool tail = first + kTile > K.kv;
+            if (!tail) {
 #pragma unroll
-                for (int hh = 0; hh < V::NL; ++hh) {
-                    VPart<F8, V::W> v[8];
-                    load_v(v, hh);
-                    C.values(hh, v, pb);
-                }
+                for (int c = 0; c < T; ++c) pb[c] = C[c].template weights<false>(acc[c], A.scale, ks, vs, key0, K.kv, seen[c]);
             } else {
-                const bf8v pb = C.template weights<true>(acc, A.scale, ks, vs, key0, K.kv, seen);
 #pragma unroll
-                for (int hh = 0; hh < V::NL; ++hh) {
-                    VPart<F8, V::W> v[8];
-                    load_v(v, hh);
-                    bad |= clean_values(v, key0, K.len, K.m);
-                    C.values(hh, v, pb);
-                }
+                for (int c = 0; c < T; ++c) pb[c] = C[c].template weights<true>(acc[c], A.scale, ks, vs, key0, K.kv, seen[c]);
+                bad |= clean_values(v[0], key0, K.len, K.m);
+            }
+            if constexpr (V::NL > 1) load_v(1);
+            add_values(C, 0, v[0], pb);
+            if constexpr (V::NL > 1) {
+                if (tail) bad |= clean_values(v[1], key0, K.len, K.m);
+                add_values(C, 1, v[1], pb);
             }
         }
     };
-    fill(0, st0, sc0);
-    fill(1, st1, sc1);
-    fill(2, st2, sc2);
-    // A tile's loads are done once at most those of the two tiles after it are
-    // left; the stage of the tile before it is free when all waves are here.
-    auto step = [&](int tile, uint8_t *stage, uint8_t *scales, uint8_t *next, uint8_t *next_scales) {
-        wait_and_meet<2 * ALL>();
-        fill(tile + 3, next, next_scales);
-        if (busy && tile < tiles) multiply(tile, stage, scales);
-    };
-    for (int tile = 0; tile < tiles; tile += 4) {
-        step(tile, st0, sc0, st3, sc3);
-        step(tile + 1, st1, sc1, st0, sc0);
-        step(tile + 2, st2, sc2, st1, sc1);
-        step(tile + 3, st3, sc3, st2, sc2);
+    fill(list, 0, tiles, st0, sc0);
+    fill(list, 1, tiles, st1, sc1);
+    fill(list, 2, tiles, st2, sc2);
+    while (true) {
+        const int lane = fresh(threadIdx.x) & 63, n = lane & 15, g = lane >> 4;
+        item += gridDim.x;
+        const bool more = pieces.find(A, true, kWideCols, item, N);
+        // with no next piece (no tiles) the list of this one still names real rows
+        const int after = more ? next_list + 0 : list + 0;
+        const int next_tiles = more ? ceil_div(N.k1 - N.k0, S::KEYS) : 0;
+        if (more) {
+            const bool ok = chunk_rows(A, N, rows16 + next_list, kWideThreads);
+            if (lane == 0) wave_ok[at ^ 1][wave] = ok;
+        }
+        col0 = K.rt * kWideCols + wave * kCols * T;         // the wave's first column
+        busy = col0 < K.cols;                               // waves without columns only load
+        bool ok = true;
+#pragma unroll
+        for (int c = 0; c < T; ++c) {
+            const int col = min(col0 + c * kCols + n, K.cols - 1);      // past the last one: that one again, not stored
+            seen[c] = seen_rows(A, K.r0, K.m, col / A.group, ok);
+            const uint16_t *p = A.q + ((size_t)col_row(A, K, col) * A.hq + col_head(A, K, col)) * D + 16 * g;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) q[c][k][hh] = *reinterpret_cast<const bf8v *>(p + 64 * k + 8 * hh);
+            C[c].clear();
+        }
+        bad = false;
+        // Steps in fours, so that a piece begins with the first stage.  A tile's
+        // loads are done once at most those of the two tiles after it are left;
+        // the stage of the tile before it is free when all waves are here.
+        const int steps = (tiles + 3) & ~3;
+        auto step = [&](int tile, uint8_t *stage, uint8_t *scales, uint8_t *next, uint8_t *next_scales) {
+            wait_and_meet<2 * ALL>();
+            const int f = tile + 3;
+            const bool now = f < steps;
+            fill(now ? list : after, now ? f : f - steps, now ? tiles : next_tiles, next, next_scales);
+            if (busy && tile < tiles) multiply(tile, stage, scales);
+        };
+        for (int tile = 0; tile < steps; tile += 4) {
+            step(tile, st0, sc0, st3, sc3);
+            step(tile + 1, st1, sc1, st0, sc0);
+            step(tile + 2, st2, sc2, st1, sc1);
+            step(tile + 3, st3, sc3, st2, sc2);
+        }
+
+#pragma unroll
+        for (int w = 0; w < kWideWaves; ++w) ok = ok && wave_ok[at][w];
+        const int end_lane = fresh(threadIdx.x) & 63, en = end_lane & 15, eg = end_lane >> 4;
+#pragma unroll
+        for (int c = 0; c < T; ++c) {
+            const float l = sum_rows4(C[c].sum);
+            const int col = col0 + c * kCols + en;
+            if (col >= K.cols) continue;
+            if (K.nch > 1 && eg == 0) A.stat[col_part(A, K, col)] = ok ? make_float2(C[c].mx, l) : make_float2(0.0f, kSkipped);
+            if (!ok) continue;
+#pragma unroll
+            for (int hh = 0; hh < V::NL; ++hh)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int i = 0; i < V::EPL; i += 4) {
+                        const int d = hh * 16 * V::EPL + (4 * eg + e) * V::EPL + i;
+                        const f4v *o = C[c].o + hh * V::EPL + i;
+                        float4 a = make_float4(o[0][e], o[1][e], o[2][e], o[3][e]);
+                        if (bad) add_bad<D, F8>(A, a, rows16 + list, seen[c], max(K.kv, K.k0), K.k1, K.kv, K.k0, d);
+                        put4<D>(A, K, col, a, l, d);
+                    }
+        }
+        if (!more) break;
+        lds_barrier();            // the list of this piece is made anew
+        K = N;
+        tiles = next_tiles;
+        at ^= 1;
+        list = next_list;
+        next_list = list_size - list;
     }
     wait_vmem();      // no load may reach LDS that is no longer this workgroup's
-
-    const float l = sum_rows4(C.sum);
-    if (col >= K.cols) return;
-    if (K.nch > 1 && g == 0) A.stat[col_part(A, K, col)] = make_float2(C.mx, l);
-#pragma unroll
-    for (int hh = 0; hh < V::NL; ++hh)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int i = 0; i < V::EPL; i += 4) {
-                const int d = hh * 16 * V::EPL + (4 * g + e) * V::EPL + i;
-                const f4v *o = C.o + hh * V::EPL + i;
-                float4 a = make_float4(o[0][e], o[1][e], o[2][e], o[3][e]);
-                if (bad) add_bad<D, F8>(A, a, rows16, seen, max(K.kv, K.k0), K.k1, K.kv, K.k0, d);
-                put4<D>(A, K, col, a, l, d);
-            }
 }
 
 // Merges a (row, head)'s chunks.  D / 4 lanes share the channels, the rest of
@@ -838,44 +955,44 @@ hipError_t allow_lds(F *kernel, int dynamic)
     return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, dynamic);
 }
 
-constexpr int kMaxRows16 = kMaxAttnKeys / kMaxChunks / 16;     // cache rows a workgroup lists at most
+constexpr int kMaxRows16 = (kMaxAttnKeys / kMaxChunks + 128) / 16;     // cache rows a workgroup lists at most
 
-template <int D, bool F8, int WAVES>
-hipError_t launch_wide(const AttnArgs &A, unsigned blocks, size_t rows16, hipStream_t stream)
+// Keys of the longest chunk that a stream of up to max_kv keys can have: the
+// rule's longest, and what rounding adds.
+int longest_chunk(int max_kv, bool wide)
 {
-    static const hipError_t e = allow_lds(attn_wide_kernel<D, F8, WAVES>, sizeof(int) * kMaxRows16);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attn_wide_kernel<D, F8, WAVES>), dim3(blocks), dim3(64 * WAVES), rows16, stream, A);
-    return hipSuccess;
+    const int most = at_least(at_least(chunk_lo(wide), at_most(chunk_mid(wide), ceil_div(max_kv, kMidChunks))), ceil_div(max_kv, kMaxChunks));
+    return most + chunk_unit(wide);
 }
 
+constexpr int kCUs = 256;
+
 template <int D, bool F8>
-hipError_t launch_d(const AttnArgs &A, bool wide, int waves, hipStream_t stream)
+hipError_t launch_d(const AttnArgs &A, bool wide, long long pieces, hipStream_t stream)
 {
-    const unsigned blocks = (unsigned)(A.chunks * A.kv.hkv * A.row_tiles * A.n_streams);
-    const size_t rows16 = sizeof(int) * (chunk_keys(A.max_kv, wide) / 16);
-    hipError_t e = hipSuccess;
+    const int list = longest_chunk(A.max_kv, wide) / 16;
+    const size_t list_bytes = sizeof(int) * list;
     if (!wide) {
         constexpr size_t lds = sizeof(float) * kAttnWaves * kCols * (D + 4 + 2) + D * 2 * kCols + sizeof(int) * (4 + kCols);
         static const hipError_t set = allow_lds(attn_kernel<D, F8>, lds + sizeof(int) * kMaxRows16);
         if (set != hipSuccess) return set;
-        hipLaunchKernelGGL((attn_kernel<D, F8>), dim3(blocks), dim3(kAttnThreads), lds + rows16, stream, A);
+        // 64 streams a grid row
+        const unsigned per_row = (unsigned)(pieces / A.n_streams * (A.n_streams < 64 ? A.n_streams : 64));
+        hipLaunchKernelGGL((attn_kernel<D, F8>), dim3(per_row, ceil_div(A.n_streams, 64)), dim3(kAttnThreads), lds + list_bytes, stream, A);
     } else {
-        e = waves == 4 ? launch_wide<D, F8, 4>(A, blocks, rows16, stream) : launch_wide<D, F8, 8>(A, blocks, rows16, stream);
-        if (e != hipSuccess) return e;
+        static const hipError_t set = allow_lds(attn_wide_kernel<D, F8>, 2 * sizeof(int) * kMaxRows16);
+        if (set != hipSuccess) return set;
+        const unsigned blocks = (unsigned)(pieces < kCUs ? pieces : kCUs);
+        hipLaunchKernelGGL((attn_wide_kernel<D, F8>), dim3(blocks), dim3(kWideThreads), 2 * list_bytes, stream, A, list);
     }
     if (A.chunks > 1)
         hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)(A.total_rows * A.hq)), dim3(256), 0, stream, A, wide ? 1 : 0);
     return hipGetLastError();
 }
 
-// Waves of a wide workgroup: four (64 columns) where the window needs no more.
-int wide_waves(int cols) { return cols <= 4 * kCols ? 4 : 8; }
-
 int column_tiles(int max_rows, int group)
 {
-    const int cols = max_rows * group;
-    return is_wide(max_rows, group) ? ceil_div(cols, kCols * wide_waves(cols)) : 1;
+    return is_wide(max_rows, group) ? ceil_div(max_rows * group, kWideCols) : 1;
 }
 
 }  // namespace
@@ -887,24 +1004,29 @@ size_t attn_workspace_bytes(int hq, int hkv, int d, int total_rows, int max_rows
     return (size_t)total_rows * hq * chunks * (sizeof(float) * d + sizeof(float2));
 }
 
+// at most so many pieces, or -1 if they cannot be numbered
+static long long most_pieces(const AttnArgs &A, bool wide)
+{
+    const long long per = (long long)chunk_bound(A.max_kv, wide) * A.kv.hkv * column_tiles(A.max_rows, A.group);
+    return per <= 0x7fffffffLL / A.n_streams - kCUs && A.n_streams <= 64 * 65535 ? per * A.n_streams : -1;
+}
+
 bool attn_fits(const AttnArgs &A)
 {
-    const long long tiles = column_tiles(A.max_rows, A.group), chunks = chunk_bound(A.max_kv, is_wide(A.max_rows, A.group));
-    return chunks * A.kv.hkv * tiles <= 0x7fffffffLL / A.n_streams && (long long)A.total_rows * A.hq <= 0x7fffffffLL;
+    return most_pieces(A, is_wide(A.max_rows, A.group)) >= 0 && (long long)A.total_rows * A.hq <= 0x7fffffffLL;
 }
 
 hipError_t launch_attn(AttnArgs A, void *workspace, hipStream_t stream)
 {
     const bool wide = is_wide(A.max_rows, A.group), f8 = A.kv.k_scale != nullptr;
-    const int waves = wide_waves(A.max_rows * A.group);
+    const long long pieces = most_pieces(A, wide);
     A.chunks = chunk_bound(A.max_kv, wide);
-    A.row_tiles = column_tiles(A.max_rows, A.group);
     A.part = static_cast<float *>(workspace);
     A.stat = reinterpret_cast<float2 *>(A.part + (size_t)A.total_rows * A.hq * A.chunks * A.kv.d);
     switch (A.kv.d) {
-    case 64: return f8 ? launch_d<64, true>(A, wide, waves, stream) : launch_d<64, false>(A, wide, waves, stream);
-    case 128: return f8 ? launch_d<128, true>(A, wide, waves, stream) : launch_d<128, false>(A, wide, waves, stream);
-    default: return f8 ? launch_d<256, true>(A, wide, waves, stream) : launch_d<256, false>(A, wide, waves, stream);
+    case 64: return f8 ? launch_d<64, true>(A, wide, pieces, stream) : launch_d<64, false>(A, wide, pieces, stream);
+    case 128: return f8 ? launch_d<128, true>(A, wide, pieces, stream) : launch_d<128, false>(A, wide, pieces, stream);
+    default: return f8 ? launch_d<256, true>(A, wide, pieces, stream) : launch_d<256, false>(A, wide, pieces, stream);
     }
 }
 
