@@ -23,8 +23,24 @@ def L():
     return gdn.lib()
 
 
+class _KvCache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("n_pages", C.c_int32), ("page_size", C.c_int32), ("hkv", C.c_int32), ("d", C.c_int32),
+                ("format", C.c_int32)]
+
+
+class _Rope(C.Structure):
+    _fields_ = [("inv_freq", C.c_void_p), ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("rot_scale", C.c_float)]
+
+
 def cache(k=0x10000, v=0x10000, ks=None, vs=None, pages=100, page=64, hkv=4, d=256, fmt=0):
-    return gdn._KvCache(k, v, ks, vs, pages, page, hkv, d, fmt)
+    return _KvCache(k, v, ks, vs, pages, page, hkv, d, fmt)
+
+
+def test_packed_structs_are_the_headers():
+    """The binding's packed bytes lie as the C structs do."""
+    assert gdn._pack_cache(1, 2, 3, 4, 5, 6, 7, 8, 1) == bytes(_KvCache(1, 2, 3, 4, 5, 6, 7, 8, 1))
+    assert gdn._pack_rope(1, 64, 1, 1.5) == bytes(_Rope(1, 64, 1, 1.5))
 
 
 def refused(L, rc, code, needle):
@@ -53,7 +69,7 @@ def window(L, c=None, n=16, total=256, max_rows=16, max_kv=4096, blocks=64, hq=2
 def test_bad_caches_are_refused_everywhere(L, kw, code, needle):
     c = cache(**kw)
     refused(L, window(L, c=c, hq=24 if c.hkv > 0 else 1), code, needle)
-    rope = gdn._Rope(0x10000, 64, 0, 1.0)
+    rope = _Rope(0x10000, 64, 0, 1.0)
     refused(L, L.gdn_attn_prep(C.byref(c), 3, 24, P16, 0, 0, P16, 0, 0, P16, 0, 0, None, None, 1e-6, C.byref(rope), P16, P16,
                                P16, None), code, needle)
     refused(L, L.gdn_attn_commit(C.byref(c), 2, 9, 16, 64, P16, None, P16, P16, P16, P16, None), code, needle)
@@ -82,7 +98,7 @@ def test_window_refusals(L, kw, code, needle):
 def test_nothing_to_do(L):
     assert window(L, n=0, total=0, rs=None, q=None) == gdn.GDN_OK
     assert window(L, n=4, total=0, rs=None, q=None) == gdn.GDN_OK
-    c, rope = cache(k=None, v=None), gdn._Rope(None, 64, 0, 1.0)
+    c, rope = cache(k=None, v=None), _Rope(None, 64, 0, 1.0)
     assert L.gdn_attn_prep(C.byref(c), 0, 24, None, 0, 0, None, 0, 0, None, 0, 0, None, None, 1e-6, C.byref(rope), None, None,
                            None, None) == gdn.GDN_OK
     assert L.gdn_attn_commit(C.byref(c), 0, 0, 16, 64, None, None, None, None, None, None, None) == gdn.GDN_OK
@@ -100,7 +116,7 @@ def test_nothing_to_do(L):
 def test_prep_refusals(L, kw, code, needle):
     def call(rows=3, hq=24, q=P16, k=P16, v=P16, qr=0, kh=0, vr=0, rot=64, freq=0x10000, rs=1.0, eps=1e-6, qn=None, pos=P16,
              slots=P16, out=P16):
-        c, rope = cache(), gdn._Rope(freq, rot, 0, rs)
+        c, rope = cache(), _Rope(freq, rot, 0, rs)
         return L.gdn_attn_prep(C.byref(c), rows, hq, q, qr, 0, k, 0, kh, v, vr, 0, qn, None, eps, C.byref(rope), pos, slots, out,
                                None)
     refused(L, call(**kw), code, needle)
@@ -152,20 +168,34 @@ def test_binding_refuses_before_the_library():
         gdn.kv_tables(cpu, cpu, cpu, cpu, cpu, cpu.view(1, 3), cpu, cpu, page_size=16)
     with pytest.raises(TypeError, match="device tensor"):
         gdn.attn_window(cpu, cpu, cpu.view(1, 3), torch.zeros(1, 1, 64, dtype=torch.bfloat16), None, None, None, None, max_kv=1)
-    dev = torch.device("cpu")
+    dev = -1            # torch's number for the CPU: the checks run as on a device
     k = torch.zeros((2, 1, 16, 64), dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="no scales"):
-        gdn._cache(dev, k, k, torch.zeros(1), None)
-    with pytest.raises(TypeError, match="k_cache must be"):
-        gdn._cache(dev, k.float(), k, None, None)
-    with pytest.raises(ValueError, match="v_cache must be"):
-        gdn._cache(dev, k, k[:1], None, None)
-    with pytest.raises(ValueError, match="needs k_scale"):
-        gdn._cache(dev, k.to(torch.float8_e4m3fn), k.to(torch.float8_e4m3fn), None, None)
-    with pytest.raises(ValueError, match="contiguous"):
-        gdn._cache(dev, k.transpose(2, 3), k.transpose(2, 3), None, None)
-    with pytest.raises(ValueError, match="channels"):
-        gdn._heads(dev, "q", torch.zeros((3, 64, 2), dtype=torch.bfloat16).transpose(1, 2), 3, 2, 64)
+    f8 = k.to(torch.float8_e4m3fn)
+    assert gdn._cache(dev, k, k.clone(), None, None)[1:] == (1, 64)
+    for args, error, match in [
+            ((k, k, torch.zeros(1), None), ValueError, "no scales"), ((k.float(), k, None, None), TypeError, "k_cache must be"),
+            ((k, k[:1], None, None), ValueError, "v_cache must hold"), ((k, f8, None, None), TypeError, "v_cache must be"),
+            ((f8, f8, None, None), ValueError, "needs k_scale"), ((f8, f8, torch.zeros(32), torch.zeros(31)), ValueError, "v_scale must hold"),
+            ((f8, f8, torch.zeros(32).double(), torch.zeros(32)), TypeError, "k_scale must be"),
+            ((k.transpose(2, 3), k.transpose(2, 3), None, None), ValueError, "contiguous"), ((k[0], k[0], None, None), ValueError, "k_cache must be")]:
+        with pytest.raises(error, match=match):
+            gdn._cache(dev, *args)
+    q = torch.zeros((3, 2, 64), dtype=torch.bfloat16)
+    assert gdn._heads(dev, "q", torch.zeros((3, 4, 64), dtype=torch.bfloat16)[:, ::2], (3, 2, 64))[1:] == (256, 128)
+    with pytest.raises(ValueError, match="channels must be contiguous"):
+        gdn._heads(dev, "q", torch.zeros((3, 64, 2), dtype=torch.bfloat16).transpose(1, 2), (3, 2, 64))
+    with pytest.raises(ValueError, match="q must be"):
+        gdn._heads(dev, "q", q, (3, 3, 64))
+    with pytest.raises(TypeError, match="must be torch.bfloat16"):
+        gdn._heads(dev, "q", q.float(), (3, 2, 64))
+    with pytest.raises(ValueError, match="as the cache"):
+        gdn._query(q, 128)
+    with pytest.raises(TypeError, match="must be torch.int32"):
+        gdn._i32s("kv_len", cpu.long(), dev, 3)
+    with pytest.raises(ValueError, match="must hold 4"):
+        gdn._i32s("kv_len", cpu, dev, 4)
+    with pytest.raises(TypeError, match="cuda:0"):
+        gdn._i32s("kv_len", cpu, 0, 3)
 
 
 # ---- pins of the oracle -----------------------------------------------------

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -46,16 +47,6 @@ class _Shape(C.Structure):
 
 class _Params(C.Structure):
     _fields_ = [("conv_w", C.c_void_p), ("a_log", C.c_void_p), ("dt_bias", C.c_void_p)]
-
-
-class _KvCache(C.Structure):
-    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
-                ("n_pages", C.c_int32), ("page_size", C.c_int32), ("hkv", C.c_int32), ("d", C.c_int32),
-                ("format", C.c_int32)]
-
-
-class _Rope(C.Structure):
-    _fields_ = [("inv_freq", C.c_void_p), ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("rot_scale", C.c_float)]
 
 
 _lock = threading.Lock()
@@ -330,56 +321,83 @@ def inproj_affine4(shape, x, wq, scales, biases, qkv, a, b, group: int):
 
 
 # ---- attention layers -------------------------------------------------------
+#
+# These calls sit in latency-bound loops: the checks are one expression a tensor
+# (what is wrong is worked out only when one fails), structs are packed bytes,
+# and the stream comes from torch as its raw handle.
 
-def _same(dev, dtype, name, t, shape=None):
-    """One argument of an attention-layer call: a contiguous tensor of this type
-    (and shape) on the call's device; its address."""
+_BF16, _F32, _I32, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+_pack_cache = struct.Struct("PPPPiiiii4x").pack     # gdn_kv_cache
+_pack_rope = struct.Struct("Piif4x").pack           # gdn_rope
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
+
+
+def _wrong(name, t, dtype, dev, size):
+    """Raises what is wrong with a tensor that is to be contiguous, of this type,
+    on device number ``dev`` and of ``size`` elements (or of that shape)."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise TypeError(f"{name} must be on {dev}, got {t.device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise TypeError(f"{name} must be on device cuda:{dev}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must hold {size}, got {tuple(t.shape)}")
+
+
+def _i32s(name, t, dev, size):
+    if t.dtype is not _I32 or t.get_device() != dev or t.numel() != size or not t.is_contiguous():
+        _wrong(name, t, _I32, dev, size)
     return t.data_ptr()
 
 
-def _on(t: torch.Tensor, name: str):
-    if not t.is_cuda:
+def _f32s(name, t, dev, size):
+    if t.dtype is not _F32 or t.get_device() != dev or t.numel() != size or not t.is_contiguous():
+        _wrong(name, t, _F32, dev, size)
+    return t.data_ptr()
+
+
+def _on(t: torch.Tensor, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
         raise TypeError(f"{name} must be a device tensor")
-    return t.device
+    return dev
 
 
 def _launch(dev, fn, *args):
-    """A call on torch's current stream of ``dev``, with ``dev`` current."""
+    """A call on torch's current stream of device ``dev``, with ``dev`` current."""
     f = getattr(_lib or lib(), fn)
-    if torch.cuda.current_device() == dev.index:
-        status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if _current_device() == dev:
+        status = f(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
-    if status != GDN_OK:
+            status = f(*args, _raw_stream(dev))
+    if status:
         _check(status, fn)
 
 
-def _cache(dev, k, v, k_scale, v_scale) -> _KvCache:
+def _cache(dev, k, v, k_scale, v_scale):
+    """A packed gdn_kv_cache, its kv heads and channels."""
     if k.dim() != 4:
         raise ValueError(f"k_cache must be [pages][kv heads][page size][d], got {tuple(k.shape)}")
-    pages, hkv, page, d = k.shape
-    if k.dtype is torch.bfloat16:
+    shape = k.shape
+    pages, hkv, page, d = shape
+    dtype = k.dtype
+    if dtype is not _BF16 and dtype is not _F8:
+        raise TypeError(f"k_cache must be {_BF16} or {_F8}, got {dtype}")
+    if k.get_device() != dev or not k.is_contiguous():
+        _wrong("k_cache", k, dtype, dev, tuple(shape))
+    if v.dtype is not dtype or v.get_device() != dev or v.shape != shape or not v.is_contiguous():
+        _wrong("v_cache", v, dtype, dev, tuple(shape))
+    if dtype is _BF16:
         if k_scale is not None or v_scale is not None:
             raise ValueError("a bfloat16 cache has no scales")
-        return _KvCache(_same(dev, torch.bfloat16, "k_cache", k), _same(dev, torch.bfloat16, "v_cache", v, k.shape), None,
-                        None, pages, page, hkv, d, 0)
-    if k.dtype is not torch.float8_e4m3fn:
-        raise TypeError(f"k_cache must be torch.bfloat16 or torch.float8_e4m3fn, got {k.dtype}")
+        return _pack_cache(k.data_ptr(), v.data_ptr(), 0, 0, pages, page, hkv, d, 0), hkv, d
     if k_scale is None or v_scale is None:
         raise ValueError("a float8_e4m3fn cache needs k_scale and v_scale")
-    rows = k.shape[:3]
-    return _KvCache(_same(dev, k.dtype, "k_cache", k), _same(dev, k.dtype, "v_cache", v, k.shape),
-                    _same(dev, torch.float32, "k_scale", k_scale, rows), _same(dev, torch.float32, "v_scale", v_scale, rows),
-                    pages, page, hkv, d, 1)
+    rows = pages * hkv * page
+    return _pack_cache(k.data_ptr(), v.data_ptr(), _f32s("k_scale", k_scale, dev, rows), _f32s("v_scale", v_scale, dev, rows),
+                       pages, page, hkv, d, 1), hkv, d
 
 
 def kv_tables(row_start, kv_len, page_count, free_count, free_pages, block_table, slots, positions, page_size: int,
@@ -388,33 +406,38 @@ def kv_tables(row_start, kv_len, page_count, free_count, free_pages, block_table
     one pass's packed rows, from the streams' lengths and the stack of unused
     pages; the counts are updated in place unless outputs are given."""
     dev = _on(row_start, "row_start")
-    i32 = torch.int32
-    n, total = row_start.shape[0] - 1, slots.shape[0]
-    if block_table.dim() != 2 or row_start.dim() != 1 or slots.dim() != 1 or free_pages.dim() != 1:
-        raise ValueError("block_table must be [streams][blocks]; row_start, slots and free_pages one-dimensional")
-    count_out = page_count if page_count_out is None else page_count_out
-    free_out = free_count if free_count_out is None else free_count_out
-    _launch(dev, "gdn_kv_tables", n, total, page_size, free_pages.shape[0], block_table.shape[1],
-            _same(dev, i32, "row_start", row_start), None if parent is None else _same(dev, i32, "parent", parent, (total,)),
-            _same(dev, i32, "kv_len", kv_len, (n,)), _same(dev, i32, "page_count", page_count, (n,)),
-            _same(dev, i32, "free_count", free_count, (1,)), _same(dev, i32, "free_pages", free_pages),
-            _same(dev, i32, "block_table", block_table, (n, block_table.shape[1])), _same(dev, i32, "slots", slots),
-            _same(dev, i32, "positions", positions, (total,)), _same(dev, i32, "page_count_out", count_out, (n,)),
-            _same(dev, i32, "free_count_out", free_out, (1,)))
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [streams][blocks]")
+    n, blocks = block_table.shape
+    total, pages = slots.numel(), free_pages.numel()
+    counts = _i32s("page_count", page_count, dev, n)
+    free = _i32s("free_count", free_count, dev, 1)
+    _launch(dev, "gdn_kv_tables", n, total, page_size, pages, blocks, _i32s("row_start", row_start, dev, n + 1),
+            None if parent is None else _i32s("parent", parent, dev, total), _i32s("kv_len", kv_len, dev, n), counts, free,
+            _i32s("free_pages", free_pages, dev, pages), _i32s("block_table", block_table, dev, n * blocks),
+            _i32s("slots", slots, dev, total), _i32s("positions", positions, dev, total),
+            counts if page_count_out is None else _i32s("page_count_out", page_count_out, dev, n),
+            free if free_count_out is None else _i32s("free_count_out", free_count_out, dev, 1))
 
 
-def _heads(dev, name, t, rows, heads, d):
+def _heads(dev, name, t, shape):
     """A bf16 [rows][heads][d] view with contiguous channels: address and strides."""
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.device != dev:
-        raise TypeError(f"{name} must be on {dev}, got {t.device}")
-    if t.shape != (rows, heads, d):
-        raise ValueError(f"{name} must be {(rows, heads, d)}, got {tuple(t.shape)}")
+    if t.dtype is not _BF16:
+        raise TypeError(f"{name} must be {_BF16}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise TypeError(f"{name} must be on device cuda:{dev}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     row, head, one = t.stride()
-    if one != 1 and rows:
+    if one != 1 and t.numel():
         raise ValueError(f"{name}'s channels must be contiguous")
     return t.data_ptr(), row, head
+
+
+def _query(q, d):
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q must be [rows][heads][{d}] as the cache, got {tuple(q.shape)}")
+    return q.shape
 
 
 def attn_prep(q, k, v, q_norm, k_norm, inv_freq, positions, slots, q_out, k_cache, v_cache, k_scale=None, v_scale=None,
@@ -424,30 +447,26 @@ def attn_prep(q, k, v, q_norm, k_norm, inv_freq, positions, slots, q_out, k_cach
     keys and values to the cache.  q [R][hq][d], k and v [R][hkv][d] may be
     views into one projection's rows."""
     dev = _on(q, "q")
-    cache = _cache(dev, k_cache, v_cache, k_scale, v_scale)
-    if q.dim() != 3:
-        raise ValueError(f"q must be [rows][heads][d], got {tuple(q.shape)}")
-    rows, hq, d = q.shape
-    if d != cache.d:
-        raise ValueError(f"q has {d} channels a head, the cache {cache.d}")
-    qp, qr, qh = _heads(dev, "q", q, rows, hq, d)
-    kp, kr, kh = _heads(dev, "k", k, rows, cache.hkv, d)
-    vp, vr, vh = _heads(dev, "v", v, rows, cache.hkv, d)
-    f32, i32 = torch.float32, torch.int32
-    rope = _Rope(_same(dev, f32, "inv_freq", inv_freq, (inv_freq.numel(),)), 2 * inv_freq.numel(), 1 if interleaved else 0,
-                 rot_scale)
-    _launch(dev, "gdn_attn_prep", C.byref(cache), rows, hq, qp, qr, qh, kp, kr, kh, vp, vr, vh,
-            None if q_norm is None else _same(dev, f32, "q_norm", q_norm, (d,)),
-            None if k_norm is None else _same(dev, f32, "k_norm", k_norm, (d,)), eps, C.byref(rope),
-            _same(dev, i32, "positions", positions, (rows,)), _same(dev, i32, "slots", slots, (rows,)),
-            _same(dev, torch.bfloat16, "q_out", q_out, (rows, hq, d)))
+    cache, hkv, d = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    shape = _query(q, d)
+    rows, hq, _ = shape
+    qp, qr, qh = _heads(dev, "q", q, shape)
+    kp, kr, kh = _heads(dev, "k", k, (rows, hkv, d))
+    vp, vr, vh = _heads(dev, "v", v, (rows, hkv, d))
+    if q_out.dtype is not _BF16 or q_out.get_device() != dev or q_out.shape != shape or not q_out.is_contiguous():
+        _wrong("q_out", q_out, _BF16, dev, tuple(shape))
+    half = inv_freq.numel()
+    _launch(dev, "gdn_attn_prep", cache, rows, hq, qp, qr, qh, kp, kr, kh, vp, vr, vh,
+            None if q_norm is None else _f32s("q_norm", q_norm, dev, d),
+            None if k_norm is None else _f32s("k_norm", k_norm, dev, d), eps,
+            _pack_rope(_f32s("inv_freq", inv_freq, dev, half), 2 * half, 1 if interleaved else 0, rot_scale),
+            _i32s("positions", positions, dev, rows), _i32s("slots", slots, dev, rows), q_out.data_ptr())
 
 
 def attn_workspace_bytes(hq: int, hkv: int, d: int, n_streams: int, total_rows: int, max_rows: int, max_kv: int) -> int:
     """Bytes of workspace ``attn_window`` needs for passes up to these sizes."""
-    cache = _KvCache(None, None, None, None, 1, 16, hkv, d, 0)
-    return int(lib().gdn_attn_workspace_bytes(C.byref(cache), int(n_streams), int(total_rows), int(max_rows), int(max_kv),
-                                              int(hq)))
+    return int(lib().gdn_attn_workspace_bytes(_pack_cache(0, 0, 0, 0, 1, 16, hkv, d, 0), int(n_streams), int(total_rows),
+                                              int(max_rows), int(max_kv), int(hq)))
 
 
 def attn_window(row_start, kv_len, block_table, q, k_cache, v_cache, out, workspace, max_kv: int,
@@ -456,22 +475,27 @@ def attn_window(row_start, kv_len, block_table, q, k_cache, v_cache, out, worksp
     holds this pass's rows already; ``scale`` of the scores d ** -0.5 unless
     given, ``gate`` (bf16 [R][hq][d], may be a view) applied as sigmoid(gate)."""
     dev = _on(q, "q")
-    cache = _cache(dev, k_cache, v_cache, k_scale, v_scale)
-    if q.dim() != 3 or row_start.dim() != 1 or block_table.dim() != 2:
-        raise ValueError("q must be [rows][heads][d], row_start one-dimensional, block_table [streams][blocks]")
-    total, hq, d = q.shape
-    if d != cache.d:
-        raise ValueError(f"q has {d} channels a head, the cache {cache.d}")
+    cache, _, d = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    shape = _query(q, d)
+    total, hq, _ = shape
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [streams][blocks]")
     n, blocks = block_table.shape
-    i32, bf16 = torch.int32, torch.bfloat16
-    gp, gr, gh = (None, 0, 0) if gate is None else _heads(dev, "gate", gate, total, hq, d)
-    ws, wsb = (None, 0) if workspace is None else (_same(dev, torch.uint8, "workspace", workspace), workspace.numel())
-    _launch(dev, "gdn_attn_window", C.byref(cache), n, total, max_rows, max_kv, blocks, hq,
-            _same(dev, i32, "row_start", row_start, (n + 1,)),
-            None if parent is None else _same(dev, i32, "parent", parent, (total,)),
-            _same(dev, i32, "kv_len", kv_len, (n,)), _same(dev, i32, "block_table", block_table),
-            _same(dev, bf16, "q", q), gp, gr, gh, d ** -0.5 if scale is None else scale,
-            _same(dev, bf16, "out", out, q.shape), ws, wsb)
+    if q.dtype is not _BF16 or not q.is_contiguous():
+        _wrong("q", q, _BF16, dev, tuple(shape))
+    if out.dtype is not _BF16 or out.get_device() != dev or out.shape != shape or not out.is_contiguous():
+        _wrong("out", out, _BF16, dev, tuple(shape))
+    gp, gr, gh = (None, 0, 0) if gate is None else _heads(dev, "gate", gate, shape)
+    ws, size = None, 0
+    if workspace is not None:
+        size = workspace.numel()
+        if workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+            _wrong("workspace", workspace, torch.uint8, dev, size)
+        ws = workspace.data_ptr()
+    _launch(dev, "gdn_attn_window", cache, n, total, max_rows, max_kv, blocks, hq, _i32s("row_start", row_start, dev, n + 1),
+            None if parent is None else _i32s("parent", parent, dev, total), _i32s("kv_len", kv_len, dev, n),
+            _i32s("block_table", block_table, dev, n * blocks), q.data_ptr(), gp, gr, gh,
+            d ** -0.5 if scale is None else scale, out.data_ptr(), ws, size)
 
 
 def attn_commit(row_start, accept_row, kv_len, block_table, k_cache, v_cache, k_scale=None, v_scale=None, parent=None,
@@ -480,18 +504,17 @@ def attn_commit(row_start, accept_row, kv_len, block_table, k_cache, v_cache, k_
     moves to the end of its cached rows; the lengths are updated in place unless
     ``kv_len_out`` is given."""
     dev = _on(row_start, "row_start")
-    cache = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    cache, _, _ = _cache(dev, k_cache, v_cache, k_scale, v_scale)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [streams][blocks]")
     n, blocks = block_table.shape
-    i32 = torch.int32
-    # without parents nothing tells the pass's rows: the windows are checked by row_start alone
+    # without parents nothing tells the pass's rows, and none of them is read
     total = (1 << 31) - 1 if parent is None else parent.numel()
-    _launch(dev, "gdn_attn_commit", C.byref(cache), n, total, max_rows, blocks, _same(dev, i32, "row_start", row_start, (n + 1,)),
-            None if parent is None else _same(dev, i32, "parent", parent, (total,)),
-            _same(dev, i32, "accept_row", accept_row, (n,)), _same(dev, i32, "kv_len", kv_len, (n,)),
-            _same(dev, i32, "block_table", block_table),
-            _same(dev, i32, "kv_len_out", kv_len if kv_len_out is None else kv_len_out, (n,)))
+    lens = _i32s("kv_len", kv_len, dev, n)
+    _launch(dev, "gdn_attn_commit", cache, n, total, max_rows, blocks, _i32s("row_start", row_start, dev, n + 1),
+            None if parent is None else _i32s("parent", parent, dev, total), _i32s("accept_row", accept_row, dev, n), lens,
+            _i32s("block_table", block_table, dev, n * blocks),
+            lens if kv_len_out is None else _i32s("kv_len_out", kv_len_out, dev, n))
 
 
 def check_layout(row_start, max_rows: int, total_rows: int, parent=None):
