@@ -22,10 +22,10 @@ namespace {
 // takes its share of the pages and rows.  A page taken that is released by the
 // same call is read from the releasing stream's table, not from free_pages, so
 // no workgroup waits for another's writes: nothing that one of them reads is
-// written in the launch, except the counts, which may be updated in place.
-// Those come from a second launch (counts only), or from the same one where a
-// single workgroup does it all.
-constexpr int kTablesThreads = 1024;
+// written in the launch, except the counts where they are updated in place.
+// Those then come from a second launch (counts only); the last workgroup writes
+// them where they go elsewhere, or where a single one does it all.
+constexpr int kTablesThreads = 1024, kTablesBlocks = 32;
 
 struct TableStreams {          // LDS, n entries each (start: n + 1)
     int *start, *kv, *have, *want, *drop, *grow;
@@ -50,6 +50,7 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(const TablesArgs
     const int n = A.n_streams, tid = threadIdx.x;
     const TableStreams S = {lds, lds + n + 1, lds + 2 * n + 1, lds + 3 * n + 1, lds + 4 * n + 1, lds + 5 * n + 1};
     const int page = 1 << A.page_shift;
+    const bool counts_too = do_counts && blockIdx.x == gridDim.x - 1;
 
     for (int s = tid; s <= n; s += kTablesThreads) S.start[s] = A.row_start[s];
     __syncthreads();
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(const TablesArgs
             A.positions[r] = pos;
         }
     }
-    if (do_counts) {
+    if (counts_too) {
         // taken = the end of the last served run
         for (int s = s0; s < s1; ++s) {
             A.page_count_out[s] = served(s) ? S.want[s] : S.have[s];
@@ -177,6 +178,7 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(const TablesArgs
 // position 2^18 its fp32 rounding alone is 1/64 rad), taken there to
 // revolutions and reduced, then sincospif of the fraction.
 constexpr int kPrepThreads = 256;
+constexpr int kPrepFewRows = 512;
 constexpr int kPrepMaxHalf = 128;                  // rotated pairs of a head
 constexpr float kE4m3Max = 448.0f;
 constexpr float kTinyMax = 0x1p-100f;              // the least row maximum a scale is made from (1 / 2^-100 is finite)
@@ -204,106 +206,120 @@ __device__ __forceinline__ float max_group(float x)
 }
 
 template <int D>
-__global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A)
+__global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, const int span)
 {
     constexpr int LANES = D / 8, HEADS = kPrepThreads / LANES;   // heads a workgroup handles at once
+    constexpr int BATCH = 4;                                     // and loads ahead
+    // this workgroup's heads: span of them from span * blockIdx.y
     __shared__ float cs[kPrepMaxHalf], sn[kPrepMaxHalf];
     __shared__ __align__(16) float swap[HEADS][D];
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid % LANES, grp = tid / LANES;
-    const int half = A.rot / 2;
-    const int heads = A.hq + 2 * A.kv.hkv;
+    const int half = A.rot / 2, hkv = A.kv.hkv, first = span * blockIdx.y, heads = min(A.hq + 2 * hkv, first + span);
+    const int64_t q_row = r * A.q_row, k_row = r * A.k_row, v_row = r * A.v_row;
+    auto source = [&](int h) {
+        return h < A.hq ? A.q + (q_row + h * A.q_head)
+             : h < A.hq + hkv ? A.k + (k_row + (h - A.hq) * A.k_head) : A.v + (v_row + (h - A.hq - hkv) * A.v_head);
+    };
+    uint4 raw[BATCH];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int h = h0 + i * HEADS + grp;
+            raw[i] = make_uint4(0, 0, 0, 0);
+            if (h < heads) raw[i] = *reinterpret_cast<const uint4 *>(source(h) + 8 * lane);
+        }
+    };
+    load(first);
+    const int slot = A.slots[r], pos = A.positions[r];
     if (tid < half) {
-        const double turns = (double)A.positions[r] * (double)A.inv_freq[tid] * 0.15915494309189533577;   // 1 / (2 pi)
+        const double turns = (double)pos * (double)A.inv_freq[tid] * 0.15915494309189533577;   // 1 / (2 pi)
         float s, c;
         sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
         cs[tid] = c * A.rot_scale;
         sn[tid] = s * A.rot_scale;
     }
-    const int slot = A.slots[r];
     const int page = slot >> A.kv.page_shift, off = slot & ((1 << A.kv.page_shift) - 1);
     const bool cached = slot >= 0 && page < A.kv.n_pages;
-    __syncthreads();
+    lds_barrier();
     // the trip count is the same for every lane of a wave's shuffles: heads past
     // the last are computed on zeros and not stored
-    for (int h0 = 0; h0 < heads; h0 += HEADS) {
-        const int h = h0 + grp;
-        const bool is_q = h < A.hq, is_k = !is_q && h < A.hq + A.kv.hkv, there = h < heads;
-        const int kvh = is_k ? h - A.hq : h - A.hq - A.kv.hkv;
-        const uint16_t *src = is_q ? A.q + r * A.q_row + h * A.q_head
-                            : is_k ? A.k + r * A.k_row + kvh * A.k_head : A.v + r * A.v_row + kvh * A.v_head;
-        uint4 raw = {0, 0, 0, 0};
-        if (there) raw = *reinterpret_cast<const uint4 *>(src + 8 * lane);
-        float x[8];
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    for (int h0 = first; h0 < heads; h0 += BATCH * HEADS) {
+        if (h0 > first) load(h0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-        float ss = 0.0f;
+        for (int b = 0; b < BATCH; ++b) {
+            if (h0 + b * HEADS >= heads) break;
+            const int h = h0 + b * HEADS + grp;
+            const bool is_q = h < A.hq, is_k = !is_q && h < A.hq + hkv, there = h < heads;
+            const int kvh = is_k ? h - A.hq : h - A.hq - hkv;
+            float x[8];
+            const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-        ss = sum_group<LANES>(ss);
-        if (is_q || is_k) {
-            const float *nw = is_q ? A.q_norm : A.k_norm;
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+            float ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+            ss = sum_group<LANES>(ss);
+            const float *nw = is_q ? A.q_norm : is_k ? A.k_norm : nullptr;
             if (nw) {
                 const float inv = __builtin_amdgcn_rsqf(ss * (1.0f / D) + A.eps);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * nw[8 * lane + i];
             }
-        }
-        if (A.interleaved) {
-            if (is_q || is_k) {
+            if (A.interleaved) {
+                if (is_q || is_k) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int p = 4 * lane + i;
-                    if (p < half) {
-                        const float a = x[2 * i], b = x[2 * i + 1];
-                        x[2 * i] = fmaf(a, cs[p], -(b * sn[p]));
-                        x[2 * i + 1] = fmaf(b, cs[p], a * sn[p]);
+                    for (int i = 0; i < 4; ++i) {
+                        const int p = 4 * lane + i;
+                        if (p < half) {
+                            const float a = x[2 * i], c = x[2 * i + 1];
+                            x[2 * i] = fmaf(a, cs[p], -(c * sn[p]));
+                            x[2 * i + 1] = fmaf(c, cs[p], a * sn[p]);
+                        }
                     }
                 }
-            }
-        } else {
-            // partners half a rotation apart change lanes through LDS, within the wave
-            float *row = swap[grp];
+            } else if (8 * lane < 2 * half) {
+                // partners half a rotation apart change lanes through LDS, within the wave
+                float *row = swap[grp];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) row[8 * lane + i] = x[i];
-            __builtin_amdgcn_wave_barrier();
-            if (is_q || is_k) {
+                for (int i = 0; i < 8; ++i) row[8 * lane + i] = x[i];
+                __builtin_amdgcn_wave_barrier();
+                if (is_q || is_k) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int e = 8 * lane + i;
-                    if (e < half) x[i] = fmaf(x[i], cs[e], -(row[e + half] * sn[e]));
-                    else if (e < 2 * half) x[i] = fmaf(x[i], cs[e - half], row[e - half] * sn[e - half]);
+                    for (int i = 0; i < 8; ++i) {
+                        const int e = 8 * lane + i;
+                        if (e < half) x[i] = fmaf(x[i], cs[e], -(row[e + half] * sn[e]));
+                        else if (e < 2 * half) x[i] = fmaf(x[i], cs[e - half], row[e - half] * sn[e - half]);
+                    }
                 }
+                __builtin_amdgcn_wave_barrier();
             }
-            __builtin_amdgcn_wave_barrier();
-        }
-        if (is_q) {
-            const uint4 o = {pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])};
-            *reinterpret_cast<uint4 *>(A.q_out + ((size_t)r * A.hq + h) * D + 8 * lane) = o;
-        }
-        if (A.kv.k_scale) {
-            float m = 0.0f;
+            if (is_q) {
+                const uint4 o = {pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])};
+                *reinterpret_cast<uint4 *>(A.q_out + ((size_t)r * A.hq + h) * D + 8 * lane) = o;
+            }
+            const size_t at = (((size_t)page * hkv + kvh) << A.kv.page_shift) + off;
+            if (A.kv.k_scale) {
+                float m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-            m = fmaxf(max_group<LANES>(m), kTinyMax);
-            if (there && !is_q && cached) {
-                const float to = kE4m3Max / m;
-                const size_t at = (((size_t)page * A.kv.hkv + kvh) << A.kv.page_shift) + off;
-                int lo = 0, hi = 0;
-                lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * to, x[1] * to, lo, false);
-                lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] * to, x[3] * to, lo, true);
-                hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4] * to, x[5] * to, hi, false);
-                hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6] * to, x[7] * to, hi, true);
-                *reinterpret_cast<uint2 *>((is_k ? A.kv.k : A.kv.v) + at * D + 8 * lane) = make_uint2(lo, hi);
-                if (lane == 0) (is_k ? A.kv.k_scale : A.kv.v_scale)[at] = m / kE4m3Max;
+                for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+                m = fmaxf(max_group<LANES>(m), kTinyMax);
+                if (there && !is_q && cached) {
+                    const float to = kE4m3Max / m;
+                    int lo = 0, hi = 0;
+                    lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * to, x[1] * to, lo, false);
+                    lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] * to, x[3] * to, lo, true);
+                    hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4] * to, x[5] * to, hi, false);
+                    hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6] * to, x[7] * to, hi, true);
+                    *reinterpret_cast<uint2 *>((is_k ? A.kv.k : A.kv.v) + at * D + 8 * lane) = make_uint2(lo, hi);
+                    if (lane == 0) (is_k ? A.kv.k_scale : A.kv.v_scale)[at] = m / kE4m3Max;
+                }
+            } else if (there && !is_q && cached) {
+                const uint4 o = is_k ? make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])) : raw[b];
+                *reinterpret_cast<uint4 *>((is_k ? A.kv.k : A.kv.v) + (at * D + 8 * lane) * 2) = o;
             }
-        } else if (there && !is_q && cached) {
-            const size_t at = (((size_t)page * A.kv.hkv + kvh) << A.kv.page_shift) + off;
-            const uint4 o = is_k ? make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])) : raw;
-            *reinterpret_cast<uint4 *>((is_k ? A.kv.k : A.kv.v) + (at * D + 8 * lane) * 2) = o;
         }
     }
 }
@@ -359,13 +375,13 @@ __global__ __launch_bounds__(256) void attn_commit_kernel(const AttnCommitArgs A
         const int j = i < per ? i : i - per, h = j / cols;
         uint8_t *pool = (i < per ? A.kv.k : A.kv.v) + (size_t)(j - h * cols) * 16;
         const size_t head = (size_t)h << A.kv.page_shift;
-        uint4 x[kMaxWindowRows];
+        f4v x[kMaxWindowRows];
 #pragma unroll
         for (int t = 0; t < kMaxWindowRows; ++t)
-            x[t] = *reinterpret_cast<const uint4 *>(pool + (src[min(t, n - 1)] + head) * row_bytes);
+            x[t] = *reinterpret_cast<const f4v *>(pool + (src[min(t, n - 1)] + head) * row_bytes);
 #pragma unroll
         for (int t = 0; t < kMaxWindowRows; ++t)
-            if (t >= first && t < n) *reinterpret_cast<uint4 *>(pool + (dst[t] + head) * row_bytes) = x[t];
+            if (t >= first && t < n) *reinterpret_cast<f4v *>(pool + (dst[t] + head) * row_bytes) = x[t];
     }
     if (A.kv.k_scale) {
         for (int i = tid; i < 2 * A.kv.hkv; i += 256) {
@@ -388,19 +404,31 @@ hipError_t launch_tables(const TablesArgs &A, hipStream_t stream)
     const size_t lds = sizeof(int) * (6 * (size_t)A.n_streams + 1);
     if (A.n_streams <= 64 && A.total_rows <= 2 * kTablesThreads) {
         tables_kernel<<<1, kTablesThreads, lds, stream>>>(A, 1, 1);
+    } else if (A.page_count_out != A.page_count && A.free_count_out != A.free_count) {
+        tables_kernel<<<kTablesBlocks, kTablesThreads, lds, stream>>>(A, 1, 1);
     } else {
-        tables_kernel<<<32, kTablesThreads, lds, stream>>>(A, 0, 1);
+        tables_kernel<<<kTablesBlocks, kTablesThreads, lds, stream>>>(A, 0, 1);
         tables_kernel<<<1, kTablesThreads, lds, stream>>>(A, 1, 0);
     }
     return hipGetLastError();
 }
 
+template <int D>
+static void launch_prep_d(const PrepArgs &A, hipStream_t stream)
+{
+    // a workgroup has all of a row's heads, or where the rows are few, as many as
+    // its lanes hold at once
+    const int heads = A.hq + 2 * A.kv.hkv, at_once = kPrepThreads / (D / 8);
+    const int span = A.rows <= kPrepFewRows && heads > at_once ? at_once : heads;
+    prep_kernel<D><<<dim3(A.rows, (heads + span - 1) / span), kPrepThreads, 0, stream>>>(A, span);
+}
+
 hipError_t launch_prep(const PrepArgs &A, hipStream_t stream)
 {
     switch (A.kv.d) {
-    case 64: prep_kernel<64><<<A.rows, kPrepThreads, 0, stream>>>(A); break;
-    case 128: prep_kernel<128><<<A.rows, kPrepThreads, 0, stream>>>(A); break;
-    default: prep_kernel<256><<<A.rows, kPrepThreads, 0, stream>>>(A); break;
+    case 64: launch_prep_d<64>(A, stream); break;
+    case 128: launch_prep_d<128>(A, stream); break;
+    default: launch_prep_d<256>(A, stream); break;
     }
     return hipGetLastError();
 }
