@@ -316,6 +316,7 @@ struct Column {
         tm = tm > mx + 8.0f ? tm : mx;
         const float base = tm == -INFINITY ? 0.0f : tm;     // no key seen so far: every p is 0
         const float back = __builtin_amdgcn_exp2f(mx - base);
+        const bool moved = tm != mx && mx != -INFINITY;     // before the first key O is zero
         mx = tm;
         float ps = 0.0f;
 #pragma unroll
@@ -324,7 +325,7 @@ struct Column {
             ps += p[i];
         }
         sum = fmaf(sum, back, ps);
-        if (__ballot(back != 1.0f)) {
+        if (__ballot(moved)) {
 #pragma unroll
             for (int i = 0; i < V::NT; ++i)
 #pragma unroll
@@ -718,28 +719,35 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
     lds_barrier();
 
     int tiles = ceil_div(K.k1 - K.k0, S::KEYS);
-    // Tile `tile` of a list of `count` into a stage.  Past the last one the loads
-    // are made all the same, each of one address, so that every wait can count
-    // on them.
-    auto fill = [&](int rows, int tile, int count, uint8_t *stage, uint8_t *scales) {
-        const bool real = tile < count;
+    // A stage's loads: a wave's instructions bring the same rows of PER / 2 of the
+    // stage's groups of 16 (their keys, then their values; rows of 64 bytes: the
+    // keys of one group or the values).  The cache rows of the groups are read
+    // from the list a stage ahead.
+    constexpr int GROUPS = (PER + 1) / 2;
+    static_assert(kWideWaves == 8, "");
+    int ahead[GROUPS], ahead_scale = 0;
+    // the tile after the last one again, where there is none
+    auto look = [&](int rows, int tile, int count) {
         const int lane = fresh(threadIdx.x) & 63;
-        rows += real ? tile * S::KEYS / 16 : 0;
-        int row[PER], scale_row = 0;
+        rows += min(tile, max(count - 1, 0)) * (S::KEYS / 16);
 #pragma unroll
-        for (int j = 0; j < PER; ++j) row[j] = rows16[rows + (j * kWideWaves + wave) % NK * S::ROWS / 16];
-        if constexpr (F8) scale_row = rows16[rows + lane / 16] + (real ? lane & 15 : 0);
+        for (int x = 0; x < GROUPS; ++x) ahead[x] = rows16[rows + (x * kWideWaves + wave) % NK * S::ROWS / 16];
+        if constexpr (F8) ahead_scale = rows16[rows + lane / 16] + (lane & 15);
+    };
+    auto fill = [&](uint8_t *stage, uint8_t *scales) {
+        const int lane = fresh(threadIdx.x) & 63;
+        const int in = wave * S::ROWS % 16 + lane / S::PIECES;             // row in its group
+        const uint32_t v_off = in * ROW + lane % S::PIECES * 16, k_off = in * ROW + (lane % S::PIECES ^ S::swizzle(in)) * 16;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int i = j * kWideWaves + wave, key = i % NK * S::ROWS + lane / S::PIECES;
-            const bool is_k = i < NK;
-            const int piece = is_k ? (lane % S::PIECES) ^ S::swizzle(key) : lane % S::PIECES;
-            const uint32_t off = (key % 16) * ROW + piece * 16;
-            const uint8_t *p = (is_k ? A.kv.k : A.kv.v) + (size_t)__builtin_amdgcn_readfirstlane(row[j]) * ROW + (real ? off : 0);
-            __builtin_amdgcn_global_load_lds((global_void *)p, (lds_void *)(stage + i * 1024), 16, 0, 0);
+            const bool is_k = PER == 1 ? wave < NK : j < PER / 2;
+            const int x = PER == 1 ? 0 : j % (PER / 2);
+            const uint8_t *p = (is_k ? A.kv.k : A.kv.v) + (size_t)__builtin_amdgcn_readfirstlane(ahead[x]) * ROW;
+            __builtin_amdgcn_global_load_lds((global_void *)(p + (is_k ? k_off : v_off)),
+                                             (lds_void *)(stage + (j * kWideWaves + wave) * 1024), 16, 0, 0);
         }
         if constexpr (F8) {        // even waves the keys' scales, odd ones the values'
-            const float *p = (wave & 1 ? A.kv.v_scale : A.kv.k_scale) + (size_t)scale_row;
+            const float *p = (wave & 1 ? A.kv.v_scale : A.kv.k_scale) + (size_t)ahead_scale;
             __builtin_amdgcn_global_load_lds((global_void *)p, (lds_void *)(scales + (wave & 1) * S::KEYS * 4), 4, 0, 0);
         }
     };
@@ -816,9 +824,13 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
             }
         }
     };
-    fill(list, 0, tiles, st0, sc0);
-    fill(list, 1, tiles, st1, sc1);
-    fill(list, 2, tiles, st2, sc2);
+    look(list, 0, tiles);
+    fill(st0, sc0);
+    look(list, 1, tiles);
+    fill(st1, sc1);
+    look(list, 2, tiles);
+    fill(st2, sc2);
+    look(list, 3, tiles);
     while (true) {
         const int lane = fresh(threadIdx.x) & 63, n = lane & 15, g = lane >> 4;
         item += gridDim.x;
@@ -851,9 +863,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
         const int steps = (tiles + 3) & ~3;
         auto step = [&](int tile, uint8_t *stage, uint8_t *scales, uint8_t *next, uint8_t *next_scales) {
             wait_and_meet<2 * ALL>();
-            const int f = tile + 3;
+            fill(next, next_scales);                        // tile + 3
+            const int f = tile + 4;
             const bool now = f < steps;
-            fill(now ? list : after, now ? f : f - steps, now ? tiles : next_tiles, next, next_scales);
+            look(now ? list : after, now ? f : f - steps, now ? tiles : next_tiles);
             if (busy && tile < tiles) multiply(tile, stage, scales);
         };
         for (int tile = 0; tile < steps; tile += 4) {
