@@ -40,7 +40,8 @@ __host__ __device__ inline int at_most(int a, int b) { return a < b ? a : b; }
 
 // Keys of a chunk of a stream with len keys: as many equal chunks, in whole
 // units, as there would be of lo keys (up to kMidChunks), then of up to mid
-// keys, then of more than that (kMaxChunks).
+// keys, then of more than that (kMaxChunks).  A sixteenth more is allowed, so
+// that a few rows past a round number of keys do not make another chunk.
 constexpr int kMidChunks = 32;
 __host__ __device__ inline int chunk_lo(bool wide) { return wide ? 512 : 256; }
 __host__ __device__ inline int chunk_mid(bool wide) { return wide ? 1024 : 512; }
@@ -50,7 +51,7 @@ __host__ __device__ inline int chunk_keys(int len, bool wide)
 {
     const int most = at_least(at_least(chunk_lo(wide), at_most(chunk_mid(wide), ceil_div(len, kMidChunks))), ceil_div(len, kMaxChunks));
     const int unit = chunk_unit(wide);
-    return unit * ceil_div(ceil_div(len, ceil_div(len, most)), unit);
+    return unit * ceil_div(ceil_div(len, ceil_div(len, most + most / 16)), unit);
 }
 
 __host__ __device__ inline int chunk_count(int len, bool wide) { return len <= 0 ? 0 : ceil_div(len, chunk_keys(len, wide)); }
@@ -223,12 +224,17 @@ __device__ __forceinline__ float max_rows4(float x)     // over lanes l, l ^ 16,
     return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
 
+// the gates of 4 channels (none: all ones, which finish4 does not look at)
+__device__ __forceinline__ uint2 gates4(const AttnArgs &A, int r, int head, int d)
+{
+    return A.gate ? *reinterpret_cast<const uint2 *>(A.gate + r * A.gate_row + head * A.gate_head + d) : make_uint2(0, 0);
+}
+
 // the result of one (row, head) column's 4 channels: o / l, gated, in bf16
-__device__ __forceinline__ uint2 finish4(const AttnArgs &A, float4 o, float inv, int r, int head, int d)
+__device__ __forceinline__ uint2 finish4(const AttnArgs &A, float4 o, float inv, uint2 g)
 {
     float x[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
     if (A.gate) {
-        const uint2 g = *reinterpret_cast<const uint2 *>(A.gate + r * A.gate_row + head * A.gate_head + d);
         x[0] *= sigmoid_f(__uint_as_float(g.x << 16));
         x[1] *= sigmoid_f(__uint_as_float(g.x & 0xffff0000u));
         x[2] *= sigmoid_f(__uint_as_float(g.y << 16));
@@ -492,7 +498,7 @@ template <int D>
 __device__ __forceinline__ void put4(const AttnArgs &A, const Chunk &K, int col, float4 a, float l, int d)
 {
     const int r = col_row(A, K, col), hd = col_head(A, K, col);
-    if (K.nch == 1) *reinterpret_cast<uint2 *>(A.out + ((size_t)r * A.hq + hd) * D + d) = finish4(A, a, 1.0f / l, r, hd, d);
+    if (K.nch == 1) *reinterpret_cast<uint2 *>(A.out + ((size_t)r * A.hq + hd) * D + d) = finish4(A, a, 1.0f / l, gates4(A, r, hd, d));
     else *reinterpret_cast<float4 *>(A.part + col_part(A, K, col) * D + d) = a;
 }
 
@@ -911,45 +917,64 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
 }
 
 // Merges a (row, head)'s chunks.  D / 4 lanes share the channels, the rest of
-// the workgroup splits the chunks.
+// the workgroup splits the chunks.  What it reads does not wait for the stream
+// to be found: the first parts, the sums and the gates are asked for at once, by
+// the row alone (a stream has at most A.chunks chunks; what lies past its own is
+// not used), and the streams' windows are looked at 64 at a time.
 template <int D>
 __global__ __launch_bounds__(256) void join_kernel(const AttnArgs A, const int is_wide)
 {
-    constexpr int LANES = D / 4, PARTS = 256 / LANES;
+    constexpr int LANES = D / 4, PARTS = 256 / LANES, EARLY = 16 / PARTS;
     __shared__ float w[kMaxChunks];
     __shared__ float4 acc[PARTS][LANES];
-    const int r = blockIdx.x / A.hq, head = blockIdx.x % A.hq, tid = threadIdx.x;
-    int lo = 0, hi = A.n_streams - 1;           // the last stream that starts at or before r
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (A.row_start[mid] <= r) lo = mid;
-        else hi = mid - 1;
-    }
-    int r0, m, kv;
-    if (!stream_window(A, lo, r0, m, kv) || r < r0 || r >= r0 + m) return;
-    const int nch = chunk_count(kv + m, is_wide);
-    if (nch <= 1) return;
+    const int r = blockIdx.x / A.hq, head = blockIdx.x % A.hq, tid = threadIdx.x, lane = tid & 63;
+    const int d4 = tid % LANES, part = tid / LANES;
     const size_t at = ((size_t)r * A.hq + head) * A.chunks;
-    float2 st = {-INFINITY, 0.0f};
-    const int lane = tid & 63;
+    const float4 *parts = reinterpret_cast<const float4 *>(A.part + at * D) + d4;
+    float4 early[EARLY];
+#pragma unroll
+    for (int i = 0; i < EARLY; ++i)
+        if (part + i * PARTS < A.chunks) early[i] = parts[(size_t)(part + i * PARTS) * LANES];
     static_assert(kMaxChunks == 64, "");
-    if (lane < nch) st = A.stat[at + lane];
+    float2 st = {-INFINITY, 0.0f};
+    if (lane < A.chunks) st = A.stat[at + lane];
+    const uint2 gates = gates4(A, r, head, 4 * d4);
+
+    int block = 0;
+    if (A.n_streams > 64) {                     // the last block that starts at or before r
+        int hi = (A.n_streams - 1) / 64;
+        while (block < hi) {
+            const int mid = (block + hi + 1) >> 1;
+            if (A.row_start[64 * mid] <= r) block = mid;
+            else hi = mid - 1;
+        }
+    }
+    int r0 = 0, m = 0, kv = 0;
+    const int s = 64 * block + lane;
+    const bool mine = s < A.n_streams && stream_window(A, s, r0, m, kv) && r >= r0 && r < r0 + m;
+    const uint64_t found = __ballot(mine);
+    if (!found) return;
+    const int l = __builtin_ctzll(found);
+    const int nch = chunk_count(__builtin_amdgcn_readlane(kv, l) + __builtin_amdgcn_readlane(m, l), is_wide);
+    if (nch <= 1) return;
+    if (lane >= nch) st = {-INFINITY, 0.0f};
     if (__ballot(st.y < 0.0f)) return;                      // a chunk was skipped: so is the stream
     float top = st.x;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
     const float base = top == -INFINITY ? 0.0f : top;
     const float f = __builtin_amdgcn_exp2f(st.x - base);
-    const float l = sum_wave(st.y * f);
+    const float sum = sum_wave(st.y * f);
     if (tid < 64) w[lane] = f;
     __syncthreads();
-    const int d4 = tid % LANES, part = tid / LANES;
     float4 a = {0, 0, 0, 0};
-    for (int c = part; c < nch; c += PARTS) {
-        const float4 b = *reinterpret_cast<const float4 *>(A.part + (at + c) * D + 4 * d4);
-        const float f0 = w[c];
+    auto add = [&](float4 b, float f0) {
         a.x = fmaf(b.x, f0, a.x), a.y = fmaf(b.y, f0, a.y), a.z = fmaf(b.z, f0, a.z), a.w = fmaf(b.w, f0, a.w);
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < EARLY; ++i)
+        if (part + i * PARTS < nch) add(early[i], w[part + i * PARTS]);
+    for (int c = part + EARLY * PARTS; c < nch; c += PARTS) add(parts[(size_t)c * LANES], w[c]);
     acc[part][d4] = a;
     __syncthreads();
     if (part == 0) {
@@ -958,7 +983,7 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs A, const int i
             const float4 b = acc[p][d4];
             a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
         }
-        *reinterpret_cast<uint2 *>(A.out + ((size_t)r * A.hq + head) * D + 4 * d4) = finish4(A, a, 1.0f / l, r, head, 4 * d4);
+        *reinterpret_cast<uint2 *>(A.out + ((size_t)r * A.hq + head) * D + 4 * d4) = finish4(A, a, 1.0f / sum, gates);
     }
 }
 
@@ -968,14 +993,14 @@ hipError_t allow_lds(F *kernel, int dynamic)
     return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, dynamic);
 }
 
-constexpr int kMaxRows16 = (kMaxAttnKeys / kMaxChunks + 128) / 16;     // cache rows a workgroup lists at most
+constexpr int kMaxRows16 = (kMaxAttnKeys / kMaxChunks * 17 / 16 + 128) / 16;     // cache rows a workgroup lists at most
 
 // Keys of the longest chunk that a stream of up to max_kv keys can have: the
 // rule's longest, and what rounding adds.
 int longest_chunk(int max_kv, bool wide)
 {
     const int most = at_least(at_least(chunk_lo(wide), at_most(chunk_mid(wide), ceil_div(max_kv, kMidChunks))), ceil_div(max_kv, kMaxChunks));
-    return most + chunk_unit(wide);
+    return most + most / 16 + chunk_unit(wide);
 }
 
 constexpr int kCUs = 256;
