@@ -35,6 +35,20 @@ constexpr int kCols = 16;                  // (row, head) pairs of a column tile
 constexpr int kMaxChunks = 64;             // of one stream
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// a / b for 0 <= a < 2^22 and 0 < b: on the device by a reciprocal, whose
+// quotient is off by one at most, and a correction (the integer sequence is four
+// times as long, and a short call is little else).
+__host__ __device__ inline int small_div(int a, int b)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    const int q = (int)((float)a * __builtin_amdgcn_rcpf((float)b)), r = a - q * b;
+    return q + (r >= b) - (r < 0);
+#else
+    return a / b;
+#endif
+}
+__host__ __device__ inline int small_ceil_div(int a, int b) { return small_div(a + b - 1, b); }
 __host__ __device__ inline int at_least(int a, int b) { return a > b ? a : b; }
 __host__ __device__ inline int at_most(int a, int b) { return a < b ? a : b; }
 
@@ -51,10 +65,10 @@ __host__ __device__ inline int chunk_keys(int len, bool wide)
 {
     const int most = at_least(at_least(chunk_lo(wide), at_most(chunk_mid(wide), ceil_div(len, kMidChunks))), ceil_div(len, kMaxChunks));
     const int unit = chunk_unit(wide);
-    return unit * ceil_div(ceil_div(len, ceil_div(len, most + most / 16)), unit);
+    return unit * ceil_div(small_ceil_div(len, small_ceil_div(len, most + most / 16)), unit);
 }
 
-__host__ __device__ inline int chunk_count(int len, bool wide) { return len <= 0 ? 0 : ceil_div(len, chunk_keys(len, wide)); }
+__host__ __device__ inline int chunk_count(int len, bool wide) { return len <= 0 ? 0 : small_ceil_div(len, chunk_keys(len, wide)); }
 
 // The most chunks that a stream of up to max_kv keys can have.
 inline int chunk_bound(int max_kv, bool wide)
@@ -389,6 +403,19 @@ __device__ __forceinline__ bool clean_values(VPart<F8, W> (&v)[8], int key0, int
     return true;
 }
 
+// Sum over the lanes up to and including this one: row_shr within the 16-lane
+// rows, then row_bcast of a row's last lane to the rows after it.
+__device__ __forceinline__ int wave_running_sum(int x)
+{
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
+    return x;
+}
+
 // One piece of work: a chunk of a stream's keys, for one kv head and one tile of
 // columns.
 struct Chunk {
@@ -415,31 +442,27 @@ struct Pieces {
         int count = 0;
         if (s < A.n_streams && stream_window(A, s, r0, m, kv))
             count = chunk_count(kv + m, wide) * A.kv.hkv * ceil_div(m * A.group, tile_cols);
-        incl = count;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int up = __shfl_up(incl, o);
-            if (lane >= o) incl += up;
-        }
+        incl = wave_running_sum(count);
     }
 
     // piece `at` of the block's
     __device__ __forceinline__ void get(const AttnArgs &A, bool wide, int at, Chunk &K) const
     {
         const int l = __builtin_ctzll(__ballot(incl > at));
-        int x = at - (l ? __builtin_amdgcn_readlane(incl, l - 1) : 0);
+        const int x = at - (l ? __builtin_amdgcn_readlane(incl, l - 1) : 0);
         K.s = first + l;
         K.r0 = __builtin_amdgcn_readlane(r0, l);
         K.m = __builtin_amdgcn_readlane(m, l);
         K.kv = __builtin_amdgcn_readlane(kv, l);
         K.len = K.kv + K.m;
-        K.nch = chunk_count(K.len, wide);
         K.size = chunk_keys(K.len, wide);
+        K.nch = small_ceil_div(K.len, K.size);
         K.cols = K.m * A.group;
-        K.c = x % K.nch;
-        x /= K.nch;
-        K.h = x % A.kv.hkv;
-        K.rt = x / A.kv.hkv;
+        // the stream's pieces: chunks innermost (at most 64 * 1024 * 128 of them)
+        const int y = x < 1 << 22 ? small_div(x, K.nch) : x / K.nch;
+        K.c = x - y * K.nch;
+        K.rt = small_div(y, A.kv.hkv);
+        K.h = y - K.rt * A.kv.hkv;
         K.k0 = K.c * K.size;
         K.k1 = min(K.k0 + K.size, K.len);
     }
@@ -484,8 +507,8 @@ __device__ __forceinline__ bool chunk_rows(const AttnArgs &A, const Chunk &K, in
 }
 
 // Packed row and query head of a stream's column.
-__device__ __forceinline__ int col_row(const AttnArgs &A, const Chunk &K, int col) { return K.r0 + col / A.group; }
-__device__ __forceinline__ int col_head(const AttnArgs &A, const Chunk &K, int col) { return K.h * A.group + col % A.group; }
+__device__ __forceinline__ int col_row(const AttnArgs &A, const Chunk &K, int col) { return K.r0 + small_div(col, A.group); }
+__device__ __forceinline__ int col_head(const AttnArgs &A, const Chunk &K, int col) { return K.h * A.group + col - small_div(col, A.group) * A.group; }
 // and its place in the workspace
 __device__ __forceinline__ size_t col_part(const AttnArgs &A, const Chunk &K, int col)
 {
@@ -529,7 +552,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, g = lane >> 4;
     const int col0 = K.rt * kCols, ncol = min(K.cols - col0, kCols);
     bool ok = chunk_rows(A, K, rows16, kAttnThreads);
-    const uint32_t seen = seen_rows(A, K.r0, K.m, min((col0 + n) / A.group, K.m - 1), ok);
+    const uint32_t seen = seen_rows(A, K.r0, K.m, min(small_div(col0 + n, A.group), K.m - 1), ok);
     // the queries, in the order of the lanes' operands: [k-step][half][lane] of
     // 16 bytes (column n, channels 64 k + 16 g + 8 half; zero past the last column)
     for (int i = tid; i < KS * 2 * 64; i += kAttnThreads) {
@@ -854,7 +877,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
 #pragma unroll
         for (int c = 0; c < T; ++c) {
             const int col = min(col0 + c * kCols + n, K.cols - 1);      // past the last one: that one again, not stored
-            seen[c] = seen_rows(A, K.r0, K.m, col / A.group, ok);
+            seen[c] = seen_rows(A, K.r0, K.m, small_div(col, A.group), ok);
             const uint16_t *p = A.q + ((size_t)col_row(A, K, col) * A.hq + col_head(A, K, col)) * D + 16 * g;
 #pragma unroll
             for (int k = 0; k < KS; ++k)
