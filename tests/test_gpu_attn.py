@@ -137,6 +137,25 @@ def test_long_streams_beside_short_ones(n, e4m3, d):
     close(c.run(), *c.oracle())
 
 
+def test_many_streams_and_pieces():
+    """More streams than a wave looks at together, and more pieces of work than workgroups."""
+    g = torch.Generator().manual_seed(25)
+    lens = torch.randint(0, 1400, (70,), generator=g).tolist()
+    for rows, hq, e4m3, tree in (([1] * 70, 16, False, False), ([1 + i % 3 for i in range(70)], 32, True, True),
+                                 ([(5 * i) % 9 for i in range(70)], 16, False, True)):
+        announce(f"attention of 70 streams, up to {max(rows)} rows, {hq} heads, e4m3 {e4m3}")
+        c = Case(lens, rows, hq, 4, 64, 32, e4m3=e4m3, tree=tree, seed=26, spare=9)
+        close(c.run(), *c.oracle())
+
+
+def test_longest_bound():
+    """The largest max_kv: short streams under it give the same bits as under their own bound."""
+    announce("attention under the largest max_kv")
+    for rows in ([1, 2], [16, 9]):
+        c = Case([600, 70], rows, 8, 2, 256, 64, seed=27)
+        assert torch.equal(c.run(max_kv=1 << 21), c.run())
+
+
 def test_peaked_scores_and_scales():
     announce("attention, peaked rows, given scale")
     c = Case([500, 80], [5, 1], 4, 2, 128, 32, seed=13, amp=30.0)

@@ -939,29 +939,34 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
     wait_vmem();      // no load may reach LDS that is no longer this workgroup's
 }
 
-// Merges a (row, head)'s chunks.  D / 4 lanes share the channels, the rest of
-// the workgroup splits the chunks.  What it reads does not wait for the stream
-// to be found: the first parts, the sums and the gates are asked for at once, by
-// the row alone (a stream has at most A.chunks chunks; what lies past its own is
-// not used), and the streams' windows are looked at 64 at a time.
+// Merges a (row, head)'s chunks, one wave each, D / 64 channels a lane.  What it
+// reads does not wait for the stream to be found: the first parts, the sums and
+// the gates are asked for at once, by the row alone (a stream has at most
+// A.chunks chunks; what lies past its own is not used), and the streams' windows
+// are looked at 64 at a time.
+constexpr int kJoinWaves = 4, kJoinBatch = 16;      // loads in flight
+
 template <int D>
-__global__ __launch_bounds__(256) void join_kernel(const AttnArgs A, const int is_wide)
+__global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const AttnArgs A, const int is_wide)
 {
-    constexpr int LANES = D / 4, PARTS = 256 / LANES, EARLY = 16 / PARTS;
-    __shared__ float w[kMaxChunks];
-    __shared__ float4 acc[PARTS][LANES];
-    const int r = blockIdx.x / A.hq, head = blockIdx.x % A.hq, tid = threadIdx.x, lane = tid & 63;
-    const int d4 = tid % LANES, part = tid / LANES;
-    const size_t at = ((size_t)r * A.hq + head) * A.chunks;
-    const float4 *parts = reinterpret_cast<const float4 *>(A.part + at * D) + d4;
-    float4 early[EARLY];
+    constexpr int VEC = D / 64;
+    typedef float part_t __attribute__((ext_vector_type(VEC)));
+    typedef uint16_t half_t __attribute__((ext_vector_type(VEC)));
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int item = blockIdx.x * kJoinWaves + wave;
+    if (item >= A.total_rows * A.hq) return;
+    const int r = item / A.hq, head = item - r * A.hq;
+    const size_t at = (size_t)item * A.chunks;
+    const part_t *parts = reinterpret_cast<const part_t *>(A.part + at * D) + lane;
+    part_t b[kJoinBatch];
 #pragma unroll
-    for (int i = 0; i < EARLY; ++i)
-        if (part + i * PARTS < A.chunks) early[i] = parts[(size_t)(part + i * PARTS) * LANES];
+    for (int i = 0; i < kJoinBatch; ++i)
+        if (i < A.chunks) b[i] = parts[(size_t)i * 64];
     static_assert(kMaxChunks == 64, "");
     float2 st = {-INFINITY, 0.0f};
     if (lane < A.chunks) st = A.stat[at + lane];
-    const uint2 gates = gates4(A, r, head, 4 * d4);
+    half_t gate = {};
+    if (A.gate) gate = *reinterpret_cast<const half_t *>(A.gate + r * A.gate_row + head * A.gate_head + VEC * lane);
 
     int block = 0;
     if (A.n_streams > 64) {                     // the last block that starts at or before r
@@ -974,8 +979,7 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs A, const int i
     }
     int r0 = 0, m = 0, kv = 0;
     const int s = 64 * block + lane;
-    const bool mine = s < A.n_streams && stream_window(A, s, r0, m, kv) && r >= r0 && r < r0 + m;
-    const uint64_t found = __ballot(mine);
+    const uint64_t found = __ballot(s < A.n_streams && stream_window(A, s, r0, m, kv) && r >= r0 && r < r0 + m);
     if (!found) return;
     const int l = __builtin_ctzll(found);
     const int nch = chunk_count(__builtin_amdgcn_readlane(kv, l) + __builtin_amdgcn_readlane(m, l), is_wide);
@@ -984,39 +988,29 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs A, const int i
     if (__ballot(st.y < 0.0f)) return;                      // a chunk was skipped: so is the stream
     float top = st.x;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-    const float base = top == -INFINITY ? 0.0f : top;
-    const float f = __builtin_amdgcn_exp2f(st.x - base);
-    const float sum = sum_wave(st.y * f);
-    if (tid < 64) w[lane] = f;
-    __syncthreads();
-    float4 a = {0, 0, 0, 0};
-    auto add = [&](float4 b, float f0) {
-        a.x = fmaf(b.x, f0, a.x), a.y = fmaf(b.y, f0, a.y), a.z = fmaf(b.z, f0, a.z), a.w = fmaf(b.w, f0, a.w);
-    };
+    for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+    top = max_rows4(top);
+    const float f = __builtin_amdgcn_exp2f(st.x - (top == -INFINITY ? 0.0f : top));
+    const float inv = 1.0f / sum_wave(st.y * f);
+    part_t a = {};
+    for (int c = 0; c < nch; c += kJoinBatch) {
+        if (c > 0)
 #pragma unroll
-    for (int i = 0; i < EARLY; ++i)
-        if (part + i * PARTS < nch) add(early[i], w[part + i * PARTS]);
-    for (int c = part + EARLY * PARTS; c < nch; c += PARTS) add(parts[(size_t)c * LANES], w[c]);
-    acc[part][d4] = a;
-    __syncthreads();
-    if (part == 0) {
+            for (int i = 0; i < kJoinBatch; ++i)
+                if (c + i < nch) b[i] = parts[(size_t)(c + i) * 64];
 #pragma unroll
-        for (int p = 1; p < PARTS; ++p) {
-            const float4 b = acc[p][d4];
-            a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
-        }
-        *reinterpret_cast<uint2 *>(A.out + ((size_t)r * A.hq + head) * D + 4 * d4) = finish4(A, a, 1.0f / sum, gates);
+        for (int i = 0; i < kJoinBatch; ++i)
+            if (c + i < nch) {
+                const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), c + i));
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) a[e] = fmaf(b[i][e], w, a[e]);
+            }
     }
+    half_t o;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[e] = f2bf(A.gate ? a[e] * inv * sigmoid_f(bf16f(gate[e])) : a[e] * inv);
+    *reinterpret_cast<half_t *>(A.out + ((size_t)item * D + VEC * lane)) = o;
 }
-
-template <typename F>
-hipError_t allow_lds(F *kernel, int dynamic)
-{
-    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, dynamic);
-}
-
-constexpr int kMaxRows16 = (kMaxAttnKeys / kMaxChunks * 17 / 16 + 128) / 16;     // cache rows a workgroup lists at most
 
 // Keys of the longest chunk that a stream of up to max_kv keys can have: the
 // rule's longest, and what rounding adds.
@@ -1035,19 +1029,15 @@ hipError_t launch_d(const AttnArgs &A, bool wide, long long pieces, hipStream_t 
     const size_t list_bytes = sizeof(int) * list;
     if (!wide) {
         constexpr size_t lds = sizeof(float) * kAttnWaves * kCols * (D + 4 + 2) + D * 2 * kCols + sizeof(int) * (4 + kCols);
-        static const hipError_t set = allow_lds(attn_kernel<D, F8>, lds + sizeof(int) * kMaxRows16);
-        if (set != hipSuccess) return set;
         // 64 streams a grid row
         const unsigned per_row = (unsigned)(pieces / A.n_streams * (A.n_streams < 64 ? A.n_streams : 64));
         hipLaunchKernelGGL((attn_kernel<D, F8>), dim3(per_row, ceil_div(A.n_streams, 64)), dim3(kAttnThreads), lds + list_bytes, stream, A);
     } else {
-        static const hipError_t set = allow_lds(attn_wide_kernel<D, F8>, 2 * sizeof(int) * kMaxRows16);
-        if (set != hipSuccess) return set;
         const unsigned blocks = (unsigned)(pieces < kCUs ? pieces : kCUs);
         hipLaunchKernelGGL((attn_wide_kernel<D, F8>), dim3(blocks), dim3(kWideThreads), 2 * list_bytes, stream, A, list);
     }
     if (A.chunks > 1)
-        hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)(A.total_rows * A.hq)), dim3(256), 0, stream, A, wide ? 1 : 0);
+        hipLaunchKernelGGL((join_kernel<D>), dim3(ceil_div(A.total_rows * A.hq, kJoinWaves)), dim3(64 * kJoinWaves), 0, stream, A, wide ? 1 : 0);
     return hipGetLastError();
 }
 
@@ -1074,7 +1064,7 @@ static long long most_pieces(const AttnArgs &A, bool wide)
 
 bool attn_fits(const AttnArgs &A)
 {
-    return most_pieces(A, is_wide(A.max_rows, A.group)) >= 0 && (long long)A.total_rows * A.hq <= 0x7fffffffLL;
+    return most_pieces(A, is_wide(A.max_rows, A.group)) >= 0 && (long long)A.total_rows * A.hq <= 0x7fffffffLL - kJoinWaves;
 }
 
 hipError_t launch_attn(AttnArgs A, void *workspace, hipStream_t stream)
