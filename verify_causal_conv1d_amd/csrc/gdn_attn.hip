@@ -711,7 +711,39 @@ struct Stage {
     {
         return ROW >= 256 ? key & 15 : ROW == 128 ? key >> 1 & 7 : key >> 2 & 3;
     }
+    // V rows in bf16 likewise, in 32-byte pieces (the 16 channels of a tile): the
+    // transposing reads take 8 rows at once
+    static __device__ __forceinline__ int v_swizzle(int key) { return F8 ? 0 : ROW >= 256 ? key & 7 : key >> 1 & 3; }
 };
+
+typedef short s4v __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s4v lds_s4v;
+
+// Transposing LDS read: each group of 16 lanes brings four 16-element rows, lane
+// 4 r + c elements 4 c .. 4 c + 3 of row r; lane i gets element i of the four.
+__device__ __forceinline__ s4v read_transposed(const uint8_t *p)
+{
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(s4v *)p);
+}
+
+// clean_values of one operand in bf16 (element j: key key0 + 16 (j / 4) + j % 4);
+// under the mask `drop`, values that are not finite are left out, and true is
+// returned.
+__device__ __forceinline__ bool clean_operand(bf8v &v, int key0, int len, uint32_t drop)
+{
+    uint4 x = __builtin_bit_cast(uint4, v);
+    uint32_t w[4] = {x.x, x.y, x.z, x.w}, bad = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int key = key0 + 16 * (q / 2) + 2 * (q & 1);
+        w[q] &= key + 1 < len ? 0xffffffffu : key < len ? 0xffffu : 0u;
+        const uint32_t b = VPart<false, 1>::bad(w[q]) & drop;
+        w[q] &= ~b;
+        bad |= b;
+    }
+    v = __builtin_bit_cast(bf8v, make_uint4(w[0], w[1], w[2], w[3]));
+    return bad != 0;
+}
 
 constexpr int kWideWaves = 8, kWideThreads = 64 * kWideWaves, kWideTiles = 1;
 constexpr int kWideCols = kCols * kWideTiles * kWideWaves;
@@ -766,7 +798,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
     auto fill = [&](uint8_t *stage, uint8_t *scales) {
         const int lane = fresh(threadIdx.x) & 63;
         const int in = wave * S::ROWS % 16 + lane / S::PIECES;             // row in its group
-        const uint32_t v_off = in * ROW + lane % S::PIECES * 16, k_off = in * ROW + (lane % S::PIECES ^ S::swizzle(in)) * 16;
+        const uint32_t v_off = in * ROW + (lane % S::PIECES ^ 2 * S::v_swizzle(in)) * 16, k_off = in * ROW + (lane % S::PIECES ^ S::swizzle(in)) * 16;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             const bool is_k = PER == 1 ? wave < NK : j < PER / 2;
@@ -827,29 +859,60 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
                     ks[u] = *reinterpret_cast<const float4 *>(scales + ((sub * kTile + 16 * u + 4 * g) * 4));
                     vs[u] = *reinterpret_cast<const float4 *>(scales + ((S::KEYS + sub * kTile + 16 * u + 4 * g) * 4));
                 }
-            VPart<F8, V::W> v[V::NL][8];
-            auto load_v = [&](int hh) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[hh][i].load(stage + ((S::KEYS + sub * kTile + 16 * (i / 4) + 4 * g + (i & 3)) * ROW + (hh * 16 + n) * V::W * 4));
-            };
-            load_v(0);
-            __builtin_amdgcn_sched_barrier(0);
-            bf8v pb[T];
             const bool tail = first + kTile > K.kv;
-            if (!tail) {
+            bf8v pb[T];
+            auto get_weights = [&] {
 #pragma unroll
-                for (int c = 0; c < T; ++c) pb[c] = C[c].template weights<false>(acc[c], A.scale, ks, vs, key0, K.kv, seen[c]);
+                for (int c = 0; c < T; ++c)
+                    pb[c] = tail ? C[c].template weights<true>(acc[c], A.scale, ks, vs, key0, K.kv, seen[c])
+                                 : C[c].template weights<false>(acc[c], A.scale, ks, vs, key0, K.kv, seen[c]);
+            };
+            if constexpr (F8) {
+                VPart<F8, V::W> v[V::NL][8];
+                auto load_v = [&](int hh) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[hh][i].load(stage + ((S::KEYS + sub * kTile + 16 * (i / 4) + 4 * g + (i & 3)) * ROW + (hh * 16 + n) * V::W * 4));
+                };
+                load_v(0);
+                __builtin_amdgcn_sched_barrier(0);
+                get_weights();
+                if (tail) bad |= clean_values(v[0], key0, K.len, K.m);
+                if constexpr (V::NL > 1) load_v(1);
+                add_values(C, 0, v[0], pb);
+                if constexpr (V::NL > 1) {
+                    if (tail) bad |= clean_values(v[1], key0, K.len, K.m);
+                    add_values(C, 1, v[1], pb);
+                }
             } else {
+                // the operand of channels 16 i .. 16 i + 15, transposed by the read:
+                // row 4 g + n / 4 (and 16 on), channels 4 (n % 4) ..
+                const int vr = 4 * g + (n >> 2);
+                const int base = (S::KEYS + sub * kTile + vr) * ROW + S::v_swizzle(vr) * 32 + (n & 3) * 8;
+                constexpr int HALF = V::NT / 2;
+                bf8v v[V::NT];
+                auto load_v = [&](int from) {
 #pragma unroll
-                for (int c = 0; c < T; ++c) pb[c] = C[c].template weights<true>(acc[c], A.scale, ks, vs, key0, K.kv, seen[c]);
-                bad |= clean_values(v[0], key0, K.len, K.m);
-            }
-            if constexpr (V::NL > 1) load_v(1);
-            add_values(C, 0, v[0], pb);
-            if constexpr (V::NL > 1) {
-                if (tail) bad |= clean_values(v[1], key0, K.len, K.m);
-                add_values(C, 1, v[1], pb);
+                    for (int i = from; i < from + HALF; ++i) {
+                        const int at = (base ^ (i & 7) * 32) + (i & ~7) * 32;
+                        const s4v lo = read_transposed(stage + at), hi = read_transposed(stage + (at + 16 * ROW));
+                        v[i] = __builtin_bit_cast(bf8v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                    }
+                };
+                load_v(0);
+                __builtin_amdgcn_sched_barrier(0);
+                get_weights();
+                load_v(HALF);
+                if (tail) {
+                    bool any = false;
+#pragma unroll
+                    for (int i = 0; i < V::NT; ++i) any |= clean_operand(v[i], key0, K.len, K.m > 1 ? ~0u : 0u);
+                    bad |= __ballot(any) != 0;
+                }
+#pragma unroll
+                for (int i = 0; i < V::NT; ++i)
+#pragma unroll
+                    for (int c = 0; c < T; ++c) C[c].o[i] = mfma(v[i], pb[c], C[c].o[i]);
             }
         }
     };
@@ -915,18 +978,27 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
             if (col >= K.cols) continue;
             if (K.nch > 1 && eg == 0) A.stat[col_part(A, K, col)] = ok ? make_float2(C[c].mx, l) : make_float2(0.0f, kSkipped);
             if (!ok) continue;
+            auto put = [&](float4 a, int d) {
+                if (bad) add_bad<D, F8>(A, a, rows16 + list, seen[c], max(K.kv, K.k0), K.k1, K.kv, K.k0, d);
+                put4<D>(A, K, col, a, l, d);
+            };
+            if constexpr (F8) {
 #pragma unroll
-            for (int hh = 0; hh < V::NL; ++hh)
+                for (int hh = 0; hh < V::NL; ++hh)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int i = 0; i < V::EPL; i += 4) {
-                        const int d = hh * 16 * V::EPL + (4 * eg + e) * V::EPL + i;
-                        const f4v *o = C[c].o + hh * V::EPL + i;
-                        float4 a = make_float4(o[0][e], o[1][e], o[2][e], o[3][e]);
-                        if (bad) add_bad<D, F8>(A, a, rows16 + list, seen[c], max(K.kv, K.k0), K.k1, K.kv, K.k0, d);
-                        put4<D>(A, K, col, a, l, d);
-                    }
+                        for (int i = 0; i < V::EPL; i += 4) {
+                            const f4v *o = C[c].o + hh * V::EPL + i;
+                            put(make_float4(o[0][e], o[1][e], o[2][e], o[3][e]), hh * 16 * V::EPL + (4 * eg + e) * V::EPL + i);
+                        }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V::NT; ++i) {
+                    const f4v o = C[c].o[i];
+                    put(make_float4(o[0], o[1], o[2], o[3]), 16 * i + 4 * eg);
+                }
+            }
         }
         if (!more) break;
         lds_barrier();            // the list of this piece is made anew
