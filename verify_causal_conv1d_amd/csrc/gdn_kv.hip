@@ -205,6 +205,18 @@ __device__ __forceinline__ float max_group(float x)
     return x;
 }
 
+// The rows pass through once and what is stored is read by other kernels, on
+// whichever XCD: loads and stores that do not stay in this XCD's cache (the
+// prompt pass of 8,306 rows takes 63 us with them and 68 us without).
+__device__ __forceinline__ uint4 load_once(const void *p)
+{
+    return __builtin_bit_cast(uint4, __builtin_nontemporal_load(static_cast<const f4v *>(p)));
+}
+__device__ __forceinline__ void store_once(void *p, uint4 x)
+{
+    __builtin_nontemporal_store(__builtin_bit_cast(f4v, x), static_cast<f4v *>(p));
+}
+
 template <int D>
 __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, const int span)
 {
@@ -226,7 +238,7 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, co
         for (int i = 0; i < BATCH; ++i) {
             const int h = h0 + i * HEADS + grp;
             raw[i] = make_uint4(0, 0, 0, 0);
-            if (h < heads) raw[i] = *reinterpret_cast<const uint4 *>(source(h) + 8 * lane);
+            if (h < heads) raw[i] = load_once(source(h) + 8 * lane);
         }
     };
     load(first);
@@ -298,7 +310,7 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, co
             }
             if (is_q) {
                 const uint4 o = {pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])};
-                *reinterpret_cast<uint4 *>(A.q_out + ((size_t)r * A.hq + h) * D + 8 * lane) = o;
+                store_once(A.q_out + ((size_t)r * A.hq + h) * D + 8 * lane, o);
             }
             const size_t at = (((size_t)page * hkv + kvh) << A.kv.page_shift) + off;
             if (A.kv.k_scale) {
@@ -318,7 +330,7 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, co
                 }
             } else if (there && !is_q && cached) {
                 const uint4 o = is_k ? make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])) : raw[b];
-                *reinterpret_cast<uint4 *>((is_k ? A.kv.k : A.kv.v) + (at * D + 8 * lane) * 2) = o;
+                store_once((is_k ? A.kv.k : A.kv.v) + (at * D + 8 * lane) * 2, o);
             }
         }
     }
