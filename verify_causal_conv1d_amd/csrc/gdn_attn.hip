@@ -123,10 +123,10 @@ struct Run16;
 template <>
 struct Run16<false> {
     uint4 a, b;
-    __device__ __forceinline__ void load(const uint8_t *p)
+    __device__ __forceinline__ void load_from_cache(const uint8_t *p)
     {
-        a = reinterpret_cast<const uint4 *>(p)[0];
-        b = reinterpret_cast<const uint4 *>(p)[1];
+        a = load_once(p);
+        b = load_once(p + 16);
     }
     __device__ __forceinline__ bf8v get(int h) const { return __builtin_bit_cast(bf8v, h ? b : a); }
 };
@@ -140,7 +140,7 @@ __device__ __forceinline__ uint32_t cvt2(uint32_t codes, bool hi)
 template <>
 struct Run16<true> {
     uint4 a;
-    __device__ __forceinline__ void load(const uint8_t *p) { a = reinterpret_cast<const uint4 *>(p)[0]; }
+    __device__ __forceinline__ void load_from_cache(const uint8_t *p) { a = load_once(p); }
     __device__ __forceinline__ bf8v get(int h) const
     {
         const uint32_t x = h ? a.z : a.x, y = h ? a.w : a.y;
@@ -162,18 +162,21 @@ struct VLayout {
 
 template <bool F8, int W>
 struct VPart {
+    typedef uint32_t vec_t __attribute__((ext_vector_type(W)));
     uint32_t w[W];
-    __device__ __forceinline__ void load(const uint8_t *p)
+    __device__ __forceinline__ void set(vec_t x)
     {
-        if constexpr (W == 4) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(p);
-            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-        } else if constexpr (W == 2) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(p);
-            w[0] = x.x, w[1] = x.y;
+        if constexpr (W == 1) {
+            w[0] = __builtin_bit_cast(uint32_t, x);
         } else {
-            w[0] = *reinterpret_cast<const uint32_t *>(p);
+#pragma unroll
+            for (int i = 0; i < W; ++i) w[i] = x[i];
         }
+    }
+    __device__ __forceinline__ void load(const uint8_t *p) { set(*reinterpret_cast<const vec_t *>(p)); }
+    __device__ __forceinline__ void load_from_cache(const uint8_t *p)
+    {
+        set(__builtin_nontemporal_load(reinterpret_cast<const vec_t *>(p)));
     }
     // a dword's elements that are infinite or NaN, as a mask of their bits
     static __device__ __forceinline__ uint32_t bad(uint32_t x)
@@ -583,7 +586,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
         for (int u = 0; u < 2; ++u) {
             const uint8_t *p = A.kv.k + (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]) * ROW;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) kk[u][k].load(p + (k_off + 64 * k * ESZ));
+            for (int k = 0; k < KS; ++k) kk[u][k].load_from_cache(p + (k_off + 64 * k * ESZ));
         }
     };
     auto load_v = [&](int tile) {
@@ -593,7 +596,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int hh = 0; hh < V::NL; ++hh) vv[hh][4 * u + j].load(p + (v_off + j * ROW + hh * 16 * V::W * 4));
+                for (int hh = 0; hh < V::NL; ++hh) vv[hh][4 * u + j].load_from_cache(p + (v_off + j * ROW + hh * 16 * V::W * 4));
         }
     };
     const int tiles = ceil_div(K.k1 - K.k0, kTile);
@@ -681,6 +684,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
 
 typedef const __attribute__((address_space(1))) void global_void;
 typedef __attribute__((address_space(3))) void lds_void;
+constexpr int kOnce = 2;        // the nontemporal bit of a load's cache policy
 
 // Waits until all but the newest N vector memory operations of the wave and all
 // of its LDS reads are done, then for the workgroup's other waves.
@@ -805,7 +809,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
             const int x = PER == 1 ? 0 : j % (PER / 2);
             const uint8_t *p = (is_k ? A.kv.k : A.kv.v) + (size_t)__builtin_amdgcn_readfirstlane(ahead[x]) * ROW;
             __builtin_amdgcn_global_load_lds((global_void *)(p + (is_k ? k_off : v_off)),
-                                             (lds_void *)(stage + (j * kWideWaves + wave) * 1024), 16, 0, 0);
+                                             (lds_void *)(stage + (j * kWideWaves + wave) * 1024), 16, 0, kOnce);
         }
         if constexpr (F8) {        // even waves the keys' scales, odd ones the values'
             const float *p = (wave & 1 ? A.kv.v_scale : A.kv.k_scale) + (size_t)ahead_scale;
@@ -834,7 +838,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
                 for (int u = 0; u < 2; ++u) {
                     const int row = (sub * kTile + 16 * u + n) * ROW, sw = S::swizzle(n);
                     if constexpr (F8) {
-                        kk[u][k].load(stage + (row + (((4 * k + g) ^ sw) * 16)));
+                        kk[u][k].a = *reinterpret_cast<const uint4 *>(stage + (row + (((4 * k + g) ^ sw) * 16)));
                     } else {
                         kk[u][k].a = *reinterpret_cast<const uint4 *>(stage + (row + (((8 * (k & 1) + 2 * g) ^ sw) + 16 * (k >> 1)) * 16));
                         kk[u][k].b = *reinterpret_cast<const uint4 *>(stage + (row + (((8 * (k & 1) + 2 * g + 1) ^ sw) + 16 * (k >> 1)) * 16));

@@ -205,18 +205,9 @@ __device__ __forceinline__ float max_group(float x)
     return x;
 }
 
-// The rows pass through once and what is stored is read by other kernels, on
-// whichever XCD: loads and stores that do not stay in this XCD's cache (the
-// prompt pass of 8,306 rows takes 63 us with them and 68 us without).
-__device__ __forceinline__ uint4 load_once(const void *p)
-{
-    return __builtin_bit_cast(uint4, __builtin_nontemporal_load(static_cast<const f4v *>(p)));
-}
-__device__ __forceinline__ void store_once(void *p, uint4 x)
-{
-    __builtin_nontemporal_store(__builtin_bit_cast(f4v, x), static_cast<f4v *>(p));
-}
-
+// The rows pass through once, and what is stored is read by other kernels on
+// whichever XCD: load_once and store_once (the prompt pass of 8,306 rows takes
+// 62 us with them and 68 us without).
 template <int D>
 __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, const int span)
 {
