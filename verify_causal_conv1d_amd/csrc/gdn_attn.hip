@@ -52,20 +52,28 @@ __host__ __device__ inline int small_ceil_div(int a, int b) { return small_div(a
 __host__ __device__ inline int at_least(int a, int b) { return a > b ? a : b; }
 __host__ __device__ inline int at_most(int a, int b) { return a < b ? a : b; }
 
-// Keys of a chunk of a stream with len keys: as many equal chunks, in whole
-// units, as there would be of lo keys (up to kMidChunks), then of up to mid
-// keys, then of more than that (kMaxChunks).  A sixteenth more is allowed, so
-// that a few rows past a round number of keys do not make another chunk.
-constexpr int kMidChunks = 32;
-__host__ __device__ inline int chunk_lo(bool wide) { return wide ? 512 : 256; }
-__host__ __device__ inline int chunk_mid(bool wide) { return wide ? 1024 : 512; }
-__host__ __device__ inline int chunk_unit(bool wide) { return wide ? 64 : 128; }
+// The most keys that a chunk of a stream with len keys is to have: at least
+// kChunkLeast; more once there are 4 of them, up to chunk_usual; more again once
+// there are 32, up to chunk_long; and more than that once there are kMaxChunks.
+constexpr int kChunkLeast = 128;
+__host__ __device__ inline int chunk_usual(bool wide) { return wide ? 512 : 256; }
+__host__ __device__ inline int chunk_long(bool wide) { return wide ? 1024 : 512; }
 
+__host__ __device__ inline int chunk_most(int len, bool wide)
+{
+    const int a = at_least(kChunkLeast, at_most(chunk_usual(wide), ceil_div(len, 4)));
+    const int b = at_least(a, at_most(chunk_long(wide), ceil_div(len, 32)));
+    return at_least(b, ceil_div(len, kMaxChunks));
+}
+
+// Its keys: equal chunks, in whole units.  A sixteenth more than the most is
+// allowed (in whole units, too), so that a few rows past a round number do not
+// make another chunk.
+__host__ __device__ inline int chunk_unit(bool wide) { return wide ? 64 : 128; }
 __host__ __device__ inline int chunk_keys(int len, bool wide)
 {
-    const int most = at_least(at_least(chunk_lo(wide), at_most(chunk_mid(wide), ceil_div(len, kMidChunks))), ceil_div(len, kMaxChunks));
-    const int unit = chunk_unit(wide);
-    return unit * ceil_div(small_ceil_div(len, small_ceil_div(len, most + most / 16)), unit);
+    const int most = chunk_most(len, wide), unit = chunk_unit(wide);
+    return unit * ceil_div(small_ceil_div(len, small_ceil_div(len, most + most / 16 / unit * unit)), unit);
 }
 
 __host__ __device__ inline int chunk_count(int len, bool wide) { return len <= 0 ? 0 : small_ceil_div(len, chunk_keys(len, wide)); }
@@ -73,7 +81,8 @@ __host__ __device__ inline int chunk_count(int len, bool wide) { return len <= 0
 // The most chunks that a stream of up to max_kv keys can have.
 inline int chunk_bound(int max_kv, bool wide)
 {
-    return at_most(kMaxChunks, at_least(ceil_div(max_kv, chunk_mid(wide)), at_most(kMidChunks, ceil_div(max_kv, chunk_lo(wide)))));
+    const int n = at_least(at_most(4, ceil_div(max_kv, kChunkLeast)), at_most(32, ceil_div(max_kv, chunk_usual(wide))));
+    return at_most(kMaxChunks, at_least(n, ceil_div(max_kv, chunk_long(wide))));
 }
 
 inline bool is_wide(int max_rows, int group) { return max_rows * group > kCols; }
@@ -1092,7 +1101,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const AttnArgs A,
 // rule's longest, and what rounding adds.
 int longest_chunk(int max_kv, bool wide)
 {
-    const int most = at_least(at_least(chunk_lo(wide), at_most(chunk_mid(wide), ceil_div(max_kv, kMidChunks))), ceil_div(max_kv, kMaxChunks));
+    const int most = chunk_most(max_kv, wide);
     return most + most / 16 + chunk_unit(wide);
 }
 
