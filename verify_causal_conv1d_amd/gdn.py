@@ -330,7 +330,7 @@ _BF16, _F32, _I32, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.float
 _pack_cache = struct.Struct("PPPPiiiii4x").pack     # gdn_kv_cache
 _pack_rope = struct.Struct("Piif4x").pack           # gdn_rope
 _raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch.cuda.current_device
+_current_device = torch._C._cuda_getDevice     # of a process that holds device tensors already
 
 
 def _wrong(name, t, dtype, dev, size):
