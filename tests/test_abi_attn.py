@@ -87,6 +87,7 @@ def test_bad_caches_are_refused_everywhere(L, kw, code, needle):
     (dict(out=None), gdn.GDN_EINVAL, "out is NULL"), (dict(gate=P4), gdn.GDN_EINVAL, "gate must be 8"),
     (dict(gate=P8, gr=6), gdn.GDN_EINVAL, "strides"), (dict(gate=P8, gh=-4), gdn.GDN_EINVAL, "strides"),
     (dict(scale=float("nan")), gdn.GDN_EINVAL, "scale"), (dict(scale=float("inf")), gdn.GDN_EINVAL, "scale"),
+    (dict(scale=3e38), gdn.GDN_EINVAL, "scale"),
     (dict(ws=None), gdn.GDN_EWORKSPACE, "workspace"), (dict(wsb=100), gdn.GDN_EWORKSPACE, "workspace"),
     (dict(ws=P8), gdn.GDN_EINVAL, "workspace must be"),
     (dict(n=1 << 24, total=1, max_kv=1 << 21), gdn.GDN_EUNSUPPORTED, "too many"),

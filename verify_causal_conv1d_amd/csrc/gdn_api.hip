@@ -800,7 +800,8 @@ int gdn_attn_window(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_
     if (rc) return rc;
     if ((long long)total_rows > (long long)n_streams * max_rows)
         return fail(GDN_EINVAL, "total_rows %d exceeds n_streams * max_rows", total_rows);
-    if (!isfinite(scale)) return fail(GDN_EINVAL, "scale must be finite");
+    const float scale2 = scale * 1.44269504088896340736f;       // for exponentials to base 2
+    if (!isfinite(scale2)) return fail(GDN_EINVAL, "scale must be finite, also times log2(e)");
     if (n_streams == 0 || total_rows == 0) {
         g_err[0] = '\0';
         return GDN_OK;
@@ -834,7 +835,7 @@ int gdn_attn_window(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_
     A.gate = gate;
     A.gate_row = gate_row_stride;
     A.gate_head = gate_head_stride;
-    A.scale = scale * 1.44269504088896340736f;
+    A.scale = scale2;
     A.out = out;
     if (!gdn::attn_fits(A)) return fail(GDN_EUNSUPPORTED, "too many streams and chunks for one launch");
     return launched(gdn::launch_attn(A, workspace, static_cast<hipStream_t>(stream)));
