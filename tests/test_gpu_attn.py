@@ -208,6 +208,24 @@ def test_values_of_unseen_rows_reach_nobody():
                             assert torch.equal(got[t], clean[t]), t
 
 
+def test_cached_rows_that_are_not_finite_reach_all_rows():
+    """An infinite or NaN value of a cached row, in the window's tile of keys or before it, is seen by every row of its stream."""
+    for e4m3, rows, d in ((False, 2, 64), (False, 9, 128), (False, 9, 256), (True, 2, 256), (True, 9, 64), (True, 9, 256)):
+        announce(f"cached rows that are not finite, e4m3 {e4m3}, {rows} rows, d {d}")
+        c = Case([70, 333], [rows, rows], 6, 2, d, 16, e4m3=e4m3, seed=30)
+        clean = c.run()
+        for value in (float("nan"),) if e4m3 else (float("nan"), float("inf"), float("-inf")):
+            for s, key in ((0, 69), (0, 64), (0, 63), (0, 0), (1, 332), (1, 320), (1, 319)):
+                page = int(c.table[s, key // 16])
+                keep = c.v[page, :, key % 16].clone()
+                c.v[page, :, key % 16] = torch.full((2, d), value).to(c.v.dtype)
+                got = c.run()
+                c.v[page, :, key % 16] = keep
+                hit, other = (got[:rows], got[rows:]) if s == 0 else (got[rows:], got[:rows])
+                assert torch.equal(other, clean[rows:] if s == 0 else clean[:rows]), (value, s, key)
+                assert torch.isnan(hit).all() if value != value else (hit == value).all(), (value, s, key)
+
+
 def test_streams_do_not_depend_on_each_other():
     """Each stream alone gives the bits it gives in the batch, wherever it is packed."""
     for tree in (False, True):

@@ -277,13 +277,14 @@ __device__ __forceinline__ uint2 finish4(const AttnArgs &A, float4 o, float inv,
     return make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
 }
 
-// Adds the infinite and NaN values of the window's rows in [key0, key1) that a
-// column sees (bits of seen) to its channels d .. d + 3.
+// Adds the infinite and NaN values that the products of a chunk's keys [k0, k1)
+// left out to a column's channels d .. d + 3: those of the rows that it sees (of
+// the window, bits of seen) in the tiles that hold rows of the window.
 template <int D, bool F8>
-__device__ void add_bad(const AttnArgs &A, float4 &a, const int *rows16, uint32_t seen, int key0, int key1, int kv, int k0, int d)
+__device__ void add_bad(const AttnArgs &A, float4 &a, const int *rows16, uint32_t seen, int kv, int k0, int k1, int d)
 {
-    for (int key = key0; key < key1; ++key) {
-        if (!(seen >> (key - kv) & 1)) continue;
+    for (int key = max(k0, kv & -kTile); key < k1; ++key) {
+        if (key >= kv && !(seen >> (key - kv) & 1)) continue;
         const size_t row = (size_t)rows16[(key - k0) >> 4] + (key & 15);
         float v[4];
         if constexpr (F8) {
@@ -696,7 +697,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
             l += l_lds[w * kCols + cc];
             mm = fmaxf(mm, m_lds[w * kCols + cc]);
         }
-        if (*bad_lds) add_bad<D, F8>(A, a, rows16, seen_lds[cc], max(K.kv, K.k0), K.k1, K.kv, K.k0, d);
+        if (*bad_lds) add_bad<D, F8>(A, a, rows16, seen_lds[cc], K.kv, K.k0, K.k1, d);
         put4<D>(A, K, col0 + cc, a, l, d);
         if (K.nch > 1 && d == 0) A.stat[col_part(A, K, col0 + cc)] = make_float2(mm, l);
     }
@@ -1012,7 +1013,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
             if (K.nch > 1 && eg == 0) A.stat[col_part(A, K, col)] = ok ? make_float2(C[c].mx, l) : make_float2(0.0f, kSkipped);
             if (!ok) continue;
             auto put = [&](float4 a, int d) {
-                if (bad) add_bad<D, F8>(A, a, rows16 + list, seen[c], max(K.kv, K.k0), K.k1, K.kv, K.k0, d);
+                if (bad) add_bad<D, F8>(A, a, rows16 + list, seen[c], K.kv, K.k0, K.k1, d);
                 put4<D>(A, K, col, a, l, d);
             };
             if constexpr (F8) {
