@@ -290,6 +290,23 @@ def test_broken_streams_are_skipped():
                 same_but(c.run(parent=p), {2})
 
 
+def test_a_falling_row_start_skips_its_two_streams_only():
+    announce("attention of 70 streams, one falling row_start")
+    rows = [2] * 70
+    c = Case([300 + 7 * s for s in range(70)], rows, 4, 2, 64, 32, seed=31)
+    good = c.run()
+    for at in (64, 3):
+        for value in (-5, 0, 10 ** 6):
+            rs = c.row_start.clone()
+            rs[at] = value
+            got = c.run(row_start=rs)
+            for s in range(70):
+                if s in (at - 1, at):
+                    assert torch.isnan(got[2 * s:2 * s + 2]).all(), (at, value, s)
+                else:
+                    assert torch.equal(got[2 * s:2 * s + 2], good[2 * s:2 * s + 2]), (at, value, s)
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 4 GiB, its pages at the far end."""
     announce("attention, 6 GiB pools")
@@ -501,6 +518,26 @@ def test_tables_edges():
     for fc in (-1, 10 ** 6):
         got = run_tables(dict(c, free_count=np.array([fc], np.int32)), 16, False)
         assert 0 <= got["free_count"].item() <= c["free_pages"].shape[0]
+
+
+@pytest.mark.parametrize("n", [5, 70])
+def test_tables_with_a_falling_row_start(n):
+    """Its two streams keep their pages and get no slots; the others are served as ever."""
+    announce(f"tables of {n} streams, one falling row_start")
+    c = tables_case(n, 16, 8, free=400)
+    c["kv_len"] = np.maximum(c["kv_len"], 0)
+    at = n // 2
+    # the oracle's two streams do not fit their tables instead: the same outputs
+    kv = c["kv_len"].copy()
+    kv[at - 1:at + 1] = 10 ** 6
+    want = ref.tables(16, c["row_start"], None, kv, c["page_count"], 400, c["free_pages"], c["block_table"], c["slots"], c["positions"])
+    for value in (-5, 10 ** 6, 2 ** 31 - 1):
+        rs = c["row_start"].copy()
+        rs[at] = value
+        for in_place in (False, True):
+            got = run_tables(dict(c, row_start=rs), 16, in_place)
+            for k, w in want.items():
+                assert np.array_equal(got[k].cpu().numpy().reshape(-1), np.asarray(w).reshape(-1)), (k, value, in_place)
 
 
 # ---- commits --------------------------------------------------------------------

@@ -58,6 +58,7 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(const TablesArgs
     const int per = (n + kTablesThreads - 1) / kTablesThreads;
     const int s0 = min(tid * per, n), s1 = min(s0 + per, n);
     long long mine = 0;
+    bool falls = false;
     for (int s = s0; s < s1; ++s) {
         const int a = S.start[s], b = S.start[s + 1], kv = A.kv_len[s], have = A.page_count[s];
         const int cap = A.max_blocks << A.page_shift;      // checked on the host to fit 31 bits
@@ -66,6 +67,7 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(const TablesArgs
         const bool ok = a >= 0 && b >= a && b <= A.total_rows && have >= 0 && have <= A.max_blocks
                         && kv <= cap && b - a <= cap - max(kv, 0);
         if (ok) want = kv < 0 ? 0 : (kv + (b - a) + page - 1) >> A.page_shift;
+        falls |= b < a;
         S.kv[s] = ok ? kv : -1;
         S.have[s] = have;
         S.want[s] = want;
@@ -78,7 +80,7 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(const TablesArgs
         if ((tid & 63) >= o) incl += up;
     }
     if ((tid & 63) == 63) wave_sum[tid >> 6] = incl;
-    __syncthreads();
+    falls = __syncthreads_or(falls);
     long long before = incl - mine, all = 0;
     for (int w = 0; w < kTablesThreads / 64; ++w) {
         if (w < (tid >> 6)) before += wave_sum[w];
@@ -120,7 +122,10 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(const TablesArgs
         // every packed row: a captured pass with fewer rows than it has room for
         // must not leave the slots of an earlier one behind
         for (int r = first; r < A.total_rows; r += step) {
-            const int s = n > 0 ? find_last(S.start, n, r) : 0, a = S.start[s], t = r - a;
+            int s = n > 0 ? find_last(S.start, n, r) : 0;
+            if (falls)               // a broken layout does not hide the streams that keep the rules
+                for (s = 0; s < n - 1 && !(S.kv[s] >= 0 && r >= S.start[s] && r < S.start[s + 1]);) ++s;
+            const int a = S.start[s], t = r - a;
             int slot = -1, pos = -1;
             if (n > 0 && t >= 0 && r < S.start[s + 1] && S.kv[s] >= 0 && served(s)) {
                 const int kv = S.kv[s];
