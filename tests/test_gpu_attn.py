@@ -156,6 +156,28 @@ def test_longest_bound():
         assert torch.equal(c.run(max_kv=1 << 21), c.run())
 
 
+@pytest.mark.parametrize("hq,hkv,rows", [(1024, 1, 16), (1024, 1024, 2), (1024, 512, 9)])
+def test_the_most_heads(hq, hkv, rows):
+    announce(f"attention, {hq} heads over {hkv}")
+    c = Case([40, 150], [rows, 1], hq, hkv, 64, 16, seed=32)
+    close(c.run(), *c.oracle())
+
+
+def test_streams_that_share_pages():
+    """Two streams and a third that begin with the same pages: as if each had its own copy."""
+    announce("attention over shared pages")
+    for rows in (1, 9):
+        c = Case([640, 700, 655], [rows] * 3, 6, 2, 128, 64, tree=rows > 1, seed=33)
+        for s in (1, 2):
+            for j in range(10):
+                for pool in (c.k, c.v):
+                    pool[c.table[s, j]] = pool[c.table[0, j]]
+        want = c.run()
+        table = c.table.clone()
+        table[1:, :10] = table[0, :10]
+        assert torch.equal(c.run(table=table), want)
+
+
 def test_peaked_scores_and_scales():
     announce("attention, peaked rows, given scale")
     c = Case([500, 80], [5, 1], 4, 2, 128, 32, seed=13, amp=30.0)
@@ -745,6 +767,48 @@ def test_captured_rounds_equal_eager_rounds():
         for name in ("kv_len", "page_count", "free_count", "table", "slots", "positions"):
             assert torch.equal(getattr(a, name), getattr(b, name)), (i, name)
         assert torch.equal(a.k.view(torch.int16), b.k.view(torch.int16)) and torch.equal(a.v.view(torch.int16), b.v.view(torch.int16)), i
+
+
+def test_captured_rounds_of_many_streams():
+    """40 streams of e4m3 rows, counts in place, captured and replayed on a HIP stream that is not the default one."""
+    announce("graph capture of attention rounds, 40 streams")
+    args = dict(n=40, hq=8, hkv=2, d=256, page=16, e4m3=True, pages=300, blocks=12, rows=6, max_kv=180, rot=64, seed=34)
+    a, b = Server(**args), Server(**args)
+    side = torch.cuda.Stream()
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    a.draw([6] * 40)
+    b.draw([6] * 40)
+    a.forward(), a.commit(), b.forward(), b.commit()
+    torch.cuda.synchronize()
+    for graph, part in zip(graphs, (a.forward, a.commit)):
+        with torch.cuda.graph(graph):
+            part()
+    torch.cuda.synchronize()
+    for i in range(6):
+        lens = [(3 * s + 5 * i) % 7 for s in range(40)]
+        a.draw(lens)
+        b.draw(lens)
+        if i == 3:
+            a.kv_len[7:20] = -1                 # they end: their pages go to the others
+            b.kv_len[7:20] = -1
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for graph in graphs:
+                graph.replay()
+            b.forward()
+            b.commit()
+        torch.cuda.synchronize()
+        rs = a.row_start.cpu().tolist()
+        for s in range(40):
+            if a.kv_len[s].item() >= 0:
+                out = a.out[rs[s]:rs[s + 1]]
+                assert torch.equal(out, b.out[rs[s]:rs[s + 1]]) and not torch.isnan(out).any(), (i, s)
+        for name in ("kv_len", "page_count", "free_count", "table", "slots", "positions", "ks", "vs"):
+            assert torch.equal(torch.nan_to_num(getattr(a, name)), torch.nan_to_num(getattr(b, name))), (i, name)
+        assert torch.equal(a.k.view(torch.uint8), b.k.view(torch.uint8)) and torch.equal(a.v.view(torch.uint8), b.v.view(torch.uint8)), i
+        held = a.page_count.cpu().tolist()
+        used = [int(x) for s in range(40) for x in a.table[s, :held[s]].tolist()] + a.free_pages[:a.free_count.item()].cpu().tolist()
+        assert sorted(used) == list(range(300)), i
 
 
 def test_two_streams_at_once():
