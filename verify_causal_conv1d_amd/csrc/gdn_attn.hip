@@ -315,6 +315,8 @@ struct Column {
     using V = VLayout<D, F8>;
     f4v o[V::NT];
     float mx, sum;
+    float back;       // what O is to be multiplied by before a tile's values are added
+    bool moved;       // and whether that is not 1 for any column
 
     __device__ __forceinline__ void clear()
     {
@@ -325,7 +327,7 @@ struct Column {
     }
 
     // Weights of a tile's keys from its scores (before scale and k_scale): the
-    // maximum, the sum and O brought up to date, P times v_scale in bf16.  key0: the lane's first key; seen: the window's rows that the column sees.
+    // maximum and the sum brought up to date, P times v_scale in bf16.  key0: the lane's first key; seen: the window's rows that the column sees.
     // TAIL: the tile holds keys of the window or past the end.
     template <bool TAIL>
     __device__ __forceinline__ bf8v weights(const f4v (&acc)[2], float scale, const float4 (&ks)[2], const float4 (&vs)[2], int key0,
@@ -356,8 +358,8 @@ struct Column {
         tm = max_rows4(tm);
         tm = tm > mx + 8.0f ? tm : mx;
         const float base = tm == -INFINITY ? 0.0f : tm;     // no key seen so far: every p is 0
-        const float back = __builtin_amdgcn_exp2f(mx - base);
-        const bool moved = tm != mx && mx != -INFINITY;     // before the first key O is zero
+        back = __builtin_amdgcn_exp2f(mx - base);
+        moved = __ballot(tm != mx && mx != -INFINITY);      // before the first key O is zero
         mx = tm;
         float ps = 0.0f;
 #pragma unroll
@@ -366,12 +368,6 @@ struct Column {
             ps += p[i];
         }
         sum = fmaf(sum, back, ps);
-        if (__ballot(moved)) {
-#pragma unroll
-            for (int i = 0; i < V::NT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][e] *= back;
-        }
         if constexpr (F8) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -387,7 +383,19 @@ struct Column {
         // P in bf16, rounded to nearest: its error is at most 2^-8 of each term,
         // that of the bf16 result's own rounding; the sum keeps the fp32 values
         const uint4 pw = {pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
+        if constexpr (!F8) rescale();
         return __builtin_bit_cast(bf8v, pw);
+    }
+
+    // O brought up to date, after weights
+    __device__ __forceinline__ void rescale()
+    {
+        if (moved) {
+#pragma unroll
+            for (int i = 0; i < V::NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] *= back;
+        }
     }
 };
 
@@ -650,10 +658,12 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
             }
         if (K.k0 + tile * kTile + kTile <= K.kv) {
             const bf8v pb[1] = {C[0].template weights<false>(acc, A.scale, ks, vs, key0, K.kv, seen)};
+            if constexpr (F8) C[0].rescale();
 #pragma unroll
             for (int hh = 0; hh < V::NL; ++hh) add_values(C, hh, vv[hh], pb);
         } else {
             const bf8v pb[1] = {C[0].template weights<true>(acc, A.scale, ks, vs, key0, K.kv, seen)};
+            if constexpr (F8) C[0].rescale();
 #pragma unroll
             for (int hh = 0; hh < V::NL; ++hh) {
                 if (clean_values(vv[hh], key0, K.len, K.m) && lane == 0) *bad_lds = 1;
@@ -745,9 +755,13 @@ struct Stage {
     {
         return ROW >= 256 ? key & 15 : ROW == 128 ? key >> 1 & 7 : key >> 2 & 3;
     }
-    // V rows in bf16 likewise, in 32-byte pieces (the 16 channels of a tile): the
+    // V rows likewise, the 16 channels of a tile (32 bytes in bf16) together: the
     // transposing reads take 8 rows at once
-    static __device__ __forceinline__ int v_swizzle(int key) { return F8 ? 0 : ROW >= 256 ? key & 7 : key >> 1 & 3; }
+    static __device__ __forceinline__ int v_swizzle(int key)
+    {
+        if (F8) return ROW == 256 ? key & 7 : ROW == 128 ? key >> 1 & 7 : key >> 2 & 3;
+        return 2 * (ROW >= 256 ? key & 7 : key >> 1 & 3);
+    }
 };
 
 typedef short s4v __attribute__((ext_vector_type(4)));
@@ -760,9 +774,31 @@ __device__ __forceinline__ s4v read_transposed(const uint8_t *p)
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(s4v *)p);
 }
 
-// clean_values of one operand in bf16 (element j: key key0 + 16 (j / 4) + j % 4);
+// The same of bytes: eight 16-byte rows, lane 2 r + c bytes 8 c .. 8 c + 7 of row
+// r; lane i gets byte i of the eight.
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) v2i lds_v2i;
+__device__ __forceinline__ v2i read_transposed_codes(const uint8_t *p)
+{
+    return __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)(v2i *)p);
+}
+
+// clean_values of one operand in e4m3 codes (byte j: key key0 + 16 (j / 4) + j %
+// 4) or in bf16 (element j likewise);
 // under the mask `drop`, values that are not finite are left out, and true is
 // returned.
+__device__ __forceinline__ bool clean_operand(v2i &v, int key0, int len, uint32_t drop)
+{
+    uint32_t bad = 0;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int left = len - key0 - 16 * u;               // keys of the stream among the four
+        const uint32_t x = v[u] & (left >= 4 ? 0xffffffffu : left > 0 ? (1u << 8 * left) - 1 : 0u), b = VPart<true, 1>::bad(x) & drop;
+        v[u] = x & ~b;
+        bad |= b;
+    }
+    return bad != 0;
+}
 __device__ __forceinline__ bool clean_operand(bf8v &v, int key0, int len, uint32_t drop)
 {
     uint4 x = __builtin_bit_cast(uint4, v);
@@ -832,7 +868,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
     auto fill = [&](uint8_t *stage, uint8_t *scales) {
         const int lane = fresh(threadIdx.x) & 63;
         const int in = wave * S::ROWS % 16 + lane / S::PIECES;             // row in its group
-        const uint32_t v_off = in * ROW + (lane % S::PIECES ^ 2 * S::v_swizzle(in)) * 16, k_off = in * ROW + (lane % S::PIECES ^ S::swizzle(in)) * 16;
+        const uint32_t v_off = in * ROW + (lane % S::PIECES ^ S::v_swizzle(in)) * 16, k_off = in * ROW + (lane % S::PIECES ^ S::swizzle(in)) * 16;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             const bool is_k = PER == 1 ? wave < NK : j < PER / 2;
@@ -900,29 +936,37 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
                 for (int c = 0; c < T; ++c)
                     pb[c] = tail ? C[c].template weights<true>(acc[c], A.scale, ks, vs, key0, K.kv, seen[c])
                                  : C[c].template weights<false>(acc[c], A.scale, ks, vs, key0, K.kv, seen[c]);
+                if constexpr (F8)
+#pragma unroll
+                    for (int c = 0; c < T; ++c) C[c].rescale();
             };
             if constexpr (F8) {
-                VPart<F8, V::W> v[V::NL][8];
-                auto load_v = [&](int hh) {
+                // the codes of channels 16 i .. 16 i + 15, transposed by the read: this
+                // lane brings 8 channels of the (n / 2)th of its 8 keys
+                const int vr = 16 * (n >> 3) + 4 * g + (n >> 1 & 3);
+                const int base = (S::KEYS + sub * kTile + vr) * ROW + S::v_swizzle(vr & 15) * 16 + (n & 1) * 8;
+                v2i v[V::NT];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[hh][i].load(stage + ((S::KEYS + sub * kTile + 16 * (i / 4) + 4 * g + (i & 3)) * ROW + (hh * 16 + n) * V::W * 4));
-                };
-                load_v(0);
+                for (int i = 0; i < V::NT; ++i) v[i] = read_transposed_codes(stage + ((base ^ (i & 7) * 16) + (i & ~7) * 16));
                 __builtin_amdgcn_sched_barrier(0);
                 get_weights();
-                if (tail) bad |= clean_values(v[0], key0, K.len, K.m);
-                if constexpr (V::NL > 1) load_v(1);
-                add_values(C, 0, v[0], pb);
-                if constexpr (V::NL > 1) {
-                    if (tail) bad |= clean_values(v[1], key0, K.len, K.m);
-                    add_values(C, 1, v[1], pb);
+                if (tail) {
+                    bool any = false;
+#pragma unroll
+                    for (int i = 0; i < V::NT; ++i) any |= clean_operand(v[i], key0, K.len, K.m > 1 ? ~0u : 0u);
+                    bad |= __ballot(any) != 0;
+                }
+#pragma unroll
+                for (int i = 0; i < V::NT; ++i) {
+                    const uint4 x = {cvt2(v[i][0], false), cvt2(v[i][0], true), cvt2(v[i][1], false), cvt2(v[i][1], true)};
+#pragma unroll
+                    for (int c = 0; c < T; ++c) C[c].o[i] = mfma(__builtin_bit_cast(bf8v, x), pb[c], C[c].o[i]);
                 }
             } else {
                 // the operand of channels 16 i .. 16 i + 15, transposed by the read:
                 // row 4 g + n / 4 (and 16 on), channels 4 (n % 4) ..
                 const int vr = 4 * g + (n >> 2);
-                const int base = (S::KEYS + sub * kTile + vr) * ROW + S::v_swizzle(vr) * 32 + (n & 3) * 8;
+                const int base = (S::KEYS + sub * kTile + vr) * ROW + S::v_swizzle(vr) * 16 + (n & 3) * 8;
                 constexpr int HALF = V::NT / 2;
                 bf8v v[V::NT];
                 auto load_v = [&](int from) {
@@ -1016,22 +1060,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
                 if (bad) add_bad<D, F8>(A, a, rows16 + list, seen[c], K.kv, K.k0, K.k1, d);
                 put4<D>(A, K, col, a, l, d);
             };
-            if constexpr (F8) {
 #pragma unroll
-                for (int hh = 0; hh < V::NL; ++hh)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-#pragma unroll
-                        for (int i = 0; i < V::EPL; i += 4) {
-                            const f4v *o = C[c].o + hh * V::EPL + i;
-                            put(make_float4(o[0][e], o[1][e], o[2][e], o[3][e]), hh * 16 * V::EPL + (4 * eg + e) * V::EPL + i);
-                        }
-            } else {
-#pragma unroll
-                for (int i = 0; i < V::NT; ++i) {
-                    const f4v o = C[c].o[i];
-                    put(make_float4(o[0], o[1], o[2], o[3]), 16 * i + 4 * eg);
-                }
+            for (int i = 0; i < V::NT; ++i) {
+                const f4v o = C[c].o[i];
+                put(make_float4(o[0], o[1], o[2], o[3]), 16 * i + 4 * eg);
             }
         }
         if (!more) break;
