@@ -308,8 +308,9 @@ constexpr float kSkipped = -1.0f;
 
 // The running state of a wave's column tile.  Lane (n, g) = (lane % 16, lane /
 // 16) holds column n: of S^T the keys 16 u + 4 g + i of a tile of 32 (u < 2, i <
-// 4), which are also the 8 keys it feeds into O^T's product, and of O^T the
-// channels given by VLayout with row 4 g + e for lane % 16.
+// 4), which are also the 8 keys it feeds into O^T's product, and of O^T rows 4 g
+// + e of every tile: channels 16 i + 4 g + e where V is transposed by LDS reads,
+// else VLayout's, with 4 g + e for lane % 16.
 template <int D, bool F8>
 struct Column {
     using V = VLayout<D, F8>;
@@ -387,7 +388,9 @@ struct Column {
         return __builtin_bit_cast(bf8v, pw);
     }
 
-    // O brought up to date, after weights
+    // O brought up to date, after weights: by the caller for e4m3, once for tiles
+    // with and without TAIL (16 trees of 16 e4m3 rows 80 us, in weights 84), in
+    // weights for bf16 (69.7 us, by the caller 71.5)
     __device__ __forceinline__ void rescale()
     {
         if (moved) {
@@ -890,7 +893,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
     bool busy = false, bad = false;
     auto multiply = [&](int tile, const uint8_t *stage, const uint8_t *scales) {
         const int lane = fresh(threadIdx.x) & 63, n = lane & 15, g = lane >> 4;
-#pragma unroll
+        // e4m3: a loop, since in two copies the compiler moves all of O between
+        // registers (16 trees 75.8 us, unrolled 77.5); bf16 rows of 128: 69, unrolled 67.4
+        constexpr int COPIES = F8 ? 1 : 2;
+#pragma unroll COPIES
         for (int sub = 0; sub < S::KEYS / kTile; ++sub) {
             const int first = K.k0 + tile * S::KEYS + sub * kTile;
             if (sub > 0 && first >= K.k1) break;
