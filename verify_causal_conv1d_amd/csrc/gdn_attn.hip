@@ -29,6 +29,7 @@
 #include "gdn_attn.h"
 #include "gdn_device.h"
 #include "gdn_internal.h"
+#include "gdn_once.h"
 
 namespace gdn {
 namespace {

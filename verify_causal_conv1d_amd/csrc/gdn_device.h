@@ -101,17 +101,6 @@ __device__ __forceinline__ float sum_wave(float x)
 // instruction, which the compiler's own wait insertion takes into account.
 __device__ __forceinline__ void wait_vmem() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 
-// 16-byte loads and stores of what passes through once: nothing of it is kept
-// in the XCD's cache for longer than it has to be.
-__device__ __forceinline__ uint4 load_once(const void *p)
-{
-    return __builtin_bit_cast(uint4, __builtin_nontemporal_load(static_cast<const f4v *>(p)));
-}
-__device__ __forceinline__ void store_once(void *p, uint4 x)
-{
-    __builtin_nontemporal_store(__builtin_bit_cast(f4v, x), static_cast<f4v *>(p));
-}
-
 // Workgroup barrier that orders LDS only.  __syncthreads() also waits for
 // every outstanding global load and store of the thread (its fence covers
 // global memory), which would hold each barrier on loads and stores in flight.
