@@ -48,18 +48,19 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(const TablesArgs
 {
     extern __shared__ int lds[];
     __shared__ long long wave_sum[kTablesThreads / 64];
+    __shared__ int falls;                                  // row_start decreases somewhere
     const int n = A.n_streams, tid = threadIdx.x;
     const TableStreams S = {lds, lds + n + 1, lds + 2 * n + 1, lds + 3 * n + 1, lds + 4 * n + 1, lds + 5 * n + 1};
     const int page = 1 << A.page_shift;
     const bool counts_too = do_counts && blockIdx.x == gridDim.x - 1;
 
     for (int s = tid; s <= n; s += kTablesThreads) S.start[s] = A.row_start[s];
+    if (tid == 0) falls = 0;
     __syncthreads();
     // each thread a run of streams: (drop | grow << 32) summed over it
     const int per = (n + kTablesThreads - 1) / kTablesThreads;
     const int s0 = min(tid * per, n), s1 = min(s0 + per, n);
     long long mine = 0;
-    bool falls = false;
     for (int s = s0; s < s1; ++s) {
         const int a = S.start[s], b = S.start[s + 1], kv = A.kv_len[s], have = A.page_count[s];
         const int cap = A.max_blocks << A.page_shift;      // checked on the host to fit 31 bits
@@ -68,7 +69,7 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(const TablesArgs
         const bool ok = a >= 0 && b >= a && b <= A.total_rows && have >= 0 && have <= A.max_blocks
                         && kv <= cap && b - a <= cap - max(kv, 0);
         if (ok) want = kv < 0 ? 0 : (kv + (b - a) + page - 1) >> A.page_shift;
-        falls |= b < a;
+        if (b < a) falls = 1;
         S.kv[s] = ok ? kv : -1;
         S.have[s] = have;
         S.want[s] = want;
@@ -81,7 +82,7 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(const TablesArgs
         if ((tid & 63) >= o) incl += up;
     }
     if ((tid & 63) == 63) wave_sum[tid >> 6] = incl;
-    falls = __syncthreads_or(falls);
+    __syncthreads();
     long long before = incl - mine, all = 0;
     for (int w = 0; w < kTablesThreads / 64; ++w) {
         if (w < (tid >> 6)) before += wave_sum[w];
