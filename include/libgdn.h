@@ -321,7 +321,7 @@ enum gdn_kv_format {
 
 typedef struct gdn_kv_cache {
     void *k, *v;                /* [n_pages][hkv][page_size][d], 16-byte aligned  */
-    float *k_scale, *v_scale;   /* [n_pages][hkv][page_size], GDN_KV_E4M3 only    */
+    float *k_scale, *v_scale;   /* [n_pages][hkv][page_size], 16-byte aligned, GDN_KV_E4M3 only */
     int32_t n_pages, page_size;
     int32_t hkv, d;
     int32_t format;             /* enum gdn_kv_format */
@@ -347,8 +347,10 @@ typedef struct gdn_kv_cache {
  * takes none.  Rows of a stream that got none, has finished, would need more
  * than max_blocks pages, or breaks the layout rules, and rows of no stream, get
  * slot and position -1.  Entries of block_table past a stream's pages and
- * entries of free_pages past those pushed are left as they were.
- * n <= 4096.
+ * entries of free_pages past those pushed are left as they were.  A stream that
+ * got none has no place for this pass's rows: leave it out of the attention and
+ * the commit that follow (no rows, or kv_len -1 there).
+ * n <= 4096, total_rows and n * max_blocks <= 2^30.
  */
 int gdn_kv_tables(int32_t n_streams, int32_t total_rows, int32_t page_size, int32_t n_pages,
                   int32_t max_blocks, const int32_t *row_start, const int32_t *parent,
@@ -375,7 +377,7 @@ int gdn_kv_tables(int32_t n_streams, int32_t total_rows, int32_t page_size, int3
  *     the cache stores no key and value
  *   q_out [rows][hq][d] bf16
  * GDN_KV_E4M3 rows get scale = max(max|y|, 2^-100) / 448 and codes y / scale
- * rounded to nearest.  No two rows may have the same slot.
+ * rounded to nearest.  No two rows may have the same slot.  rows < 2^24.
  */
 typedef struct gdn_rope {
     const float *inv_freq;   /* [rot_dim / 2], device */
@@ -409,7 +411,7 @@ int gdn_attn_prep(const gdn_kv_cache *cache, int32_t rows, int32_t hq, const uin
  * they were, and so are rows of no stream.  A stream's results depend on
  * neither the other streams of the call nor its place in it, bit for bit, for
  * the same max_rows.  A row takes nothing from rows that it does not see,
- * whatever they hold.
+ * whatever they hold.  total_rows * hq <= 2^26 - 4.
  */
 size_t gdn_attn_workspace_bytes(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,
                                 int32_t max_rows, int32_t max_kv, int32_t hq);
@@ -428,7 +430,7 @@ int gdn_attn_window(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_
  * rows kv_len[s], kv_len[s] + 1, ..., and kv_len_out[s] = kv_len[s] + their
  * number.  parent NULL: chains (nothing moves).  kv_len_out may be kv_len.  A
  * stream whose accepted row or layout breaks the rules keeps its length, and
- * none of its rows move.
+ * none of its rows move.  n_streams < 2^24.
  */
 int gdn_attn_commit(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,
                     int32_t max_rows, int32_t max_blocks, const int32_t *row_start,

@@ -91,6 +91,7 @@ def test_bad_caches_are_refused_everywhere(L, kw, code, needle):
     (dict(ws=None), gdn.GDN_EWORKSPACE, "workspace"), (dict(wsb=100), gdn.GDN_EWORKSPACE, "workspace"),
     (dict(ws=P8), gdn.GDN_EINVAL, "workspace must be"),
     (dict(n=1 << 24, total=1, max_kv=1 << 21), gdn.GDN_EUNSUPPORTED, "too many"),
+    (dict(n=1 << 20, total=1 << 22, wsb=1 << 50), gdn.GDN_EUNSUPPORTED, "too many"),
 ])
 def test_window_refusals(L, kw, code, needle):
     refused(L, window(L, **kw), code, needle)
@@ -113,6 +114,7 @@ def test_nothing_to_do(L):
     (dict(q=None), gdn.GDN_EINVAL, "q is NULL"), (dict(k=P8), gdn.GDN_EINVAL, "k must be"), (dict(v=None), gdn.GDN_EINVAL, "v is NULL"),
     (dict(qn=P4), gdn.GDN_EINVAL, "q_norm"), (dict(freq=None), gdn.GDN_EINVAL, "inv_freq"), (dict(pos=None), gdn.GDN_EINVAL, "positions"),
     (dict(slots=None), gdn.GDN_EINVAL, "slots"), (dict(out=P8), gdn.GDN_EINVAL, "q_out"),
+    (dict(rows=1 << 24), gdn.GDN_EUNSUPPORTED, "rows"),
 ])
 def test_prep_refusals(L, kw, code, needle):
     def call(rows=3, hq=24, q=P16, k=P16, v=P16, qr=0, kh=0, vr=0, rot=64, freq=0x10000, rs=1.0, eps=1e-6, qn=None, pos=P16,
@@ -131,6 +133,7 @@ def test_prep_refusals(L, kw, code, needle):
     (dict(rs=None), gdn.GDN_EINVAL, "row_start"), (dict(kv=None), gdn.GDN_EINVAL, "kv_len"), (dict(pc=None), gdn.GDN_EINVAL, "page_count"),
     (dict(fc=None), gdn.GDN_EINVAL, "free_count"), (dict(fp=None), gdn.GDN_EINVAL, "free_pages"), (dict(tb=None), gdn.GDN_EINVAL, "block_table"),
     (dict(sl=None), gdn.GDN_EINVAL, "slots"), (dict(pos=None), gdn.GDN_EINVAL, "positions"),
+    (dict(total=(1 << 30) + 1), gdn.GDN_EUNSUPPORTED, "total_rows"), (dict(n=4096, blocks=(1 << 18) + 1), gdn.GDN_EUNSUPPORTED, "table"),
 ])
 def test_tables_refusals(L, kw, code, needle):
     def call(n=16, total=256, page=16, pages=1000, blocks=64, rs=P16, kv=P16, pc=P16, fc=P16, fp=P16, tb=P16, sl=P16, pos=P16):
@@ -141,7 +144,7 @@ def test_tables_refusals(L, kw, code, needle):
 @pytest.mark.parametrize("kw,code,needle", [
     (dict(n=-1), gdn.GDN_EINVAL, "n_streams"), (dict(max_rows=17), gdn.GDN_EINVAL, "max_rows"), (dict(blocks=0), gdn.GDN_EINVAL, "max_blocks"),
     (dict(rs=None), gdn.GDN_EINVAL, "row_start"), (dict(acc=None), gdn.GDN_EINVAL, "accept_row"), (dict(kv=None), gdn.GDN_EINVAL, "kv_len"),
-    (dict(tb=None), gdn.GDN_EINVAL, "block_table"),
+    (dict(tb=None), gdn.GDN_EINVAL, "block_table"), (dict(n=1 << 24), gdn.GDN_EUNSUPPORTED, "n_streams"),
 ])
 def test_commit_refusals(L, kw, code, needle):
     def call(n=2, total=9, max_rows=16, blocks=64, rs=P16, acc=P16, kv=P16, tb=P16):

@@ -686,8 +686,10 @@ int gdn_kv_tables(int32_t n_streams, int32_t total_rows, int32_t page_size, int3
     if (rc) return rc;
     if (n_pages < 1) return fail(GDN_EINVAL, "n_pages %d must be positive", n_pages);
     if (n_streams > gdn::kMaxTableStreams) return fail(GDN_EUNSUPPORTED, "at most %d streams a call", gdn::kMaxTableStreams);
-    if ((long long)n_pages * page_size > 0x7fffffffLL || (long long)n_streams * max_blocks > 0x7fffffffLL)
+    // the kernel steps through pages and rows in 31 bits
+    if ((long long)n_pages * page_size > 0x7fffffffLL || (long long)n_streams * max_blocks > 1 << 30)
         return fail(GDN_EUNSUPPORTED, "the pool or the block table is too large");
+    if (total_rows > 1 << 30) return fail(GDN_EUNSUPPORTED, "total_rows %d: at most %d", total_rows, 1 << 30);
     if (!row_start) return fail(GDN_EINVAL, "row_start is NULL");
     if (!free_count || !free_count_out) return fail(GDN_EINVAL, "free_count or free_count_out is NULL");
     if (!free_pages) return fail(GDN_EINVAL, "free_pages is NULL");
@@ -732,6 +734,7 @@ int gdn_attn_prep(const gdn_kv_cache *cache, int32_t rows, int32_t hq, const uin
     if (!rc) rc = check_strides("v", v_row_stride, v_head_stride, 8);
     if (rc) return rc;
     if (rows < 0) return fail(GDN_EINVAL, "rows %d is negative", rows);
+    if (rows > gdn::kMaxGroups) return fail(GDN_EUNSUPPORTED, "rows %d: at most %d", rows, gdn::kMaxGroups);
     if (!rope) return fail(GDN_EINVAL, "rope is NULL");
     if (rope->rot_dim < 0 || rope->rot_dim > cache->d || rope->rot_dim % 2 != 0)
         return fail(GDN_EINVAL, "rot_dim %d must be even and in 0..%d", rope->rot_dim, cache->d);
@@ -850,6 +853,7 @@ int gdn_attn_commit(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_
     int rc = check_cache_sizes(cache, A.kv);
     if (!rc) rc = check_counts(n_streams, total_rows, max_rows, max_blocks, cache->page_size);
     if (rc) return rc;
+    if (n_streams > gdn::kMaxGroups) return fail(GDN_EUNSUPPORTED, "n_streams %d: at most %d", n_streams, gdn::kMaxGroups);
     if (n_streams == 0) {
         g_err[0] = '\0';
         return GDN_OK;

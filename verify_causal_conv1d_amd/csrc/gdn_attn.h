@@ -55,6 +55,7 @@ struct AttnCommitArgs {
 };
 
 constexpr int kMaxAttnKeys = 1 << 21;    // of one stream: a workgroup lists its chunk's pages in LDS
+constexpr int kMaxGroups = (1 << 24) - 1;  // workgroups of 256 threads: a launch has less than 2^32 threads
 constexpr int kMaxTableStreams = 4096;   // a workgroup keeps six ints of each in LDS
 
 size_t attn_workspace_bytes(int hq, int hkv, int d, int total_rows, int max_rows, int max_kv);

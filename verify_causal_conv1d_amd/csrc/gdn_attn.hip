@@ -1215,7 +1215,7 @@ static long long most_pieces(const AttnArgs &A, bool wide)
 
 bool attn_fits(const AttnArgs &A)
 {
-    return most_pieces(A, is_wide(A.max_rows, A.group)) >= 0 && (long long)A.total_rows * A.hq <= 0x7fffffffLL - kJoinWaves;
+    return most_pieces(A, is_wide(A.max_rows, A.group)) >= 0 && (long long)A.total_rows * A.hq <= (long long)kMaxGroups * kJoinWaves;
 }
 
 hipError_t launch_attn(AttnArgs A, void *workspace, hipStream_t stream)
