@@ -746,7 +746,8 @@ __device__ __forceinline__ void wait_and_meet()
 // with the join, which has 27 MB of parts to read (12 us).  A tile of 32 keys
 // takes a CU about 1.2 us when nothing else runs there (each wave reads the
 // tile's 32 KB from LDS, and two of the waves with columns share a SIMD); how
-// evenly the pieces fall on the CUs costs the rest.
+// evenly the pieces fall on the CUs costs the rest.  Over e4m3 rows (110 MB) they
+// take 76 us, bound by instructions: each wave converts every code it multiplies.
 template <int D, bool F8>
 struct Stage {
     static constexpr int ROW = D * (F8 ? 1 : 2);
