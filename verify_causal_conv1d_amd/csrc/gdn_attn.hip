@@ -743,11 +743,12 @@ __device__ __forceinline__ void wait_and_meet()
 //
 // One workgroup of 8 waves stays on each CU and goes through its pieces.  16
 // draft trees of up to 16 rows over 700 to 8,191 keys (96 columns, 212 MB): 70 us
-// with the join, which has 27 MB of parts to read (12 us).  A tile of 32 keys
+// with the join, which has 27 MB of parts to read (11 us).  A tile of 32 keys
 // takes a CU about 1.2 us when nothing else runs there (each wave reads the
 // tile's 32 KB from LDS, and two of the waves with columns share a SIMD); how
 // evenly the pieces fall on the CUs costs the rest.  Over e4m3 rows (110 MB) they
-// take 76 us, bound by instructions: each wave converts every code it multiplies.
+// take 76 us: a wave's chain from the keys through the weights to the values, with
+// every code converted on the way, and at most two waves a SIMD to hide it.
 template <int D, bool F8>
 struct Stage {
     static constexpr int ROW = D * (F8 ? 1 : 2);
