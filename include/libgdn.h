@@ -347,9 +347,12 @@ typedef struct gdn_kv_cache {
  * takes none.  Rows of a stream that got none, has finished, would need more
  * than max_blocks pages, or breaks the layout rules, and rows of no stream, get
  * slot and position -1.  Entries of block_table past a stream's pages and
- * entries of free_pages past those pushed are left as they were.  A stream that
- * got none has no place for this pass's rows: leave it out of the attention and
- * the commit that follow (no rows, or kv_len -1 there).
+ * entries of free_pages past those pushed are left as they were, except that a
+ * stream that got none has no room for this pass's rows: of the entries that
+ * its pages would have taken, those that name a page of the pool (perhaps
+ * another stream's by now) become -1.  gdn_attn_window and gdn_attn_commit then
+ * skip the stream, and its kv_len stays.  The mixer's commits do not look at
+ * pages: give them accept_row -1 for a stream whose slots are -1.
  * n <= 4096, total_rows and n * max_blocks <= 2^30.
  */
 int gdn_kv_tables(int32_t n_streams, int32_t total_rows, int32_t page_size, int32_t n_pages,
@@ -429,8 +432,9 @@ int gdn_attn_window(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_
  * row of the stream's window, or -1 to keep none), root first, move to cache
  * rows kv_len[s], kv_len[s] + 1, ..., and kv_len_out[s] = kv_len[s] + their
  * number.  parent NULL: chains (nothing moves).  kv_len_out may be kv_len.  A
- * stream whose accepted row or layout breaks the rules keeps its length, and
- * none of its rows move.  n_streams < 2^24.
+ * stream whose accepted row or layout breaks the rules, or whose window has a
+ * page outside the cache, keeps its length, and none of its rows move.
+ * n_streams < 2^24.
  */
 int gdn_attn_commit(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,
                     int32_t max_rows, int32_t max_blocks, const int32_t *row_start,

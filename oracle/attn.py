@@ -58,6 +58,9 @@ def tables(page, row_start, parent, kv_len, page_count, free_count, free_pages, 
         out_of_pages = out_of_pages or grow > top
         if out_of_pages:
             served[s] = False
+            for j in range(int(page_count[s]), want[s]):     # no pages: and none that an earlier round named
+                if 0 <= table[s, j] < len(free):
+                    table[s, j] = -1
             continue
         for j in range(int(page_count[s]), want[s]):
             top -= 1

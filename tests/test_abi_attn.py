@@ -262,3 +262,13 @@ def test_oracle_commit_moves_the_path():
     row = lambda p, i: p[table[0, i // 4], 0, i % 4]  # noqa: E731
     assert [row(got, i) for i in (2, 3, 4)] == [row(pool, i) for i in (2, 4, 5)]
     assert row(got, 5) == row(pool, 5)
+
+
+def test_oracle_tables_without_pages():
+    # page 4, nothing free: stream 0 asks for a second page where its table still names page 2, which stream 1 holds
+    table = np.array([[7, 2, 9, -5], [5, 2, -1, -1]], np.int32)
+    r = ref.tables(4, [0, 9, 10], None, np.array([3, 5]), np.array([1, 2]), 0, np.array([-1] * 9, np.int32), table,
+                   np.zeros(10, np.int32), np.zeros(10, np.int32))
+    assert r["block_table"].tolist() == [[7, -1, 9, -5], [5, 2, -1, -1]]
+    assert r["page_count"].tolist() == [1, 2] and r["free_count"] == 0
+    assert r["slots"].tolist() == [-1] * 9 + [2 * 4 + 1]

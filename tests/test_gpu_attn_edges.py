@@ -1,0 +1,119 @@
+"""The attention-layer calls where they can go wrong together or at the ends of
+their ranges: pools that run out, long wide windows, prompts, extreme values,
+broken layouts."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import attn as ref
+from verify_causal_conv1d_amd import gdn
+
+from gpu_util import announce
+from test_gpu_attn import BF16, F8, I32, Server, check_tables, close, f64, i32, tables_case, values
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- pools that run out -----------------------------------------------------------
+
+def bits(t):
+    return t.view(torch.uint8).cpu()
+
+
+def test_tables_of_a_stream_without_pages_name_no_page():
+    """Entries that an unserved stream asked for and that still name a page become -1; others stay."""
+    announce("tables, unserved streams with page numbers of earlier rounds")
+    for n, tree in ((7, True), (16, False), (90, False)):
+        for seed in range(3):
+            c = tables_case(n, 16, 40 + seed, tree=tree, free=2)
+            g = np.random.default_rng(seed)
+            table, have = c["block_table"], c["page_count"]
+            pool = c["free_pages"].shape[0]
+            for s in range(n):      # what lies past a stream's pages: anything, of the pool and not
+                past = table[s, have[s]:]
+                past[:] = np.where(g.random(past.shape) < 0.7, g.integers(0, pool, past.shape), pool + 5)
+            check_tables(c, 16)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("e4m3,hq", [(False, 2), (True, 6), (False, 6)])
+def test_a_round_in_which_the_pool_is_empty(captured, e4m3, hq):
+    """A stream that gets no page: its results, rows and length stay, and no other
+    stream's page is read or written for it, although its table still holds the
+    number of a page that it gave back and another stream took."""
+    announce(f"a round without pages, e4m3 {e4m3}, {hq} heads over 2, captured {captured}")
+    sv = Server(3, hq, 2, 128, 16, e4m3, 4, 3, 12, 48, 32, seed=41)
+    side, graphs = torch.cuda.Stream(), None
+
+    def go(part):
+        if graphs is None:
+            part()
+        else:
+            with torch.cuda.stream(side):
+                graphs[part.__name__].replay()
+        torch.cuda.synchronize()
+
+    def setup(lens, parents, accept):
+        """Windows of these lengths; a stream's parents (None: a chain) and accepted local row."""
+        R = sv.draw(lens)
+        starts = sv.row_start.cpu().tolist()
+        parent = sv.parent.cpu()
+        for s, p in enumerate(parents):
+            parent[starts[s]:starts[s + 1]] = torch.tensor(range(-1, lens[s] - 1) if p is None else p, dtype=I32)
+        sv.parent.copy_(parent)
+        sv.accept.copy_(torch.tensor([-1 if a is None else starts[s] + a for s, a in enumerate(accept)], dtype=I32))
+        sv.out.fill_(float("nan"))
+        return R, starts
+
+    setup([12, 12, 12], [None] * 3, [11, 11, 0])
+    go(sv.forward), go(sv.commit)
+    if captured:
+        graphs = {}
+        sv.accept.fill_(-1)
+        for part in (sv.forward, sv.commit):
+            graphs[part.__name__] = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graphs[part.__name__]):
+                part()
+    assert sv.kv_len.tolist() == [12, 12, 1] and sv.free_count.item() == 1
+    setup([12, 0, 0], [None] * 3, [None] * 3)               # the first stream takes the last page and keeps no row
+    go(sv.forward), go(sv.commit)
+    given = sv.table[0, 1].item()
+    assert sv.kv_len.tolist() == [12, 12, 1] and sv.free_count.item() == 0
+    setup([1, 12, 0], [None] * 3, [0, 11, None])            # it gives the page back, and the second stream takes it
+    go(sv.forward), go(sv.commit)
+    assert sv.kv_len.tolist() == [13, 24, 1] and sv.table[1, 1].item() == given and sv.page_count.tolist() == [1, 2, 1]
+
+    tree = [-1, 0, 0, 2, 3, 4, 5, 6, 7, 8, 9, 10]
+    for last in (11, 0):                                    # its path: rows past the page that it holds, or one within it
+        R, rs = setup([12, 4, 3], [tree, None, None], [last, None, None])
+        before = [t.clone() for t in (sv.k, sv.v, sv.ks, sv.vs) if t is not None]
+        go(sv.forward)
+        assert (sv.slots[:12] == -1).all() and (sv.slots[12:R] >= 0).all()
+        assert sv.table[0, 1].item() == -1 and sv.page_count.tolist() == [1, 2, 1] and sv.free_count.item() == 0
+        assert torch.isnan(sv.out[:12]).all() and torch.isnan(sv.out[R:]).all()
+        # the others: against the oracle over the cache's own values
+        kv, table = sv.kv_len.cpu().tolist(), sv.table.cpu().numpy()
+        x = f64(sv.x)
+        o, m, reach = ref.window(16, [0, 4, 7], None, kv[1:], table[1:], f64(sv.q)[12:R], values(sv.k, sv.ks), values(sv.v, sv.vs),
+                                 128 ** -0.5, x[12:R, hq:2 * hq])
+        close(sv.out[12:R], o, ref.window_bound(o, m, reach, 128))
+        after = [t.clone() for t in (sv.k, sv.v, sv.ks, sv.vs) if t is not None]
+        go(sv.commit)
+        assert sv.kv_len.tolist() == [13, 24, 1]
+        slots = sv.slots[12:R].long().cpu()
+        for t, mid, old in zip((t for t in (sv.k, sv.v, sv.ks, sv.vs) if t is not None), after, before):
+            assert torch.equal(bits(t), bits(mid))          # the commit moved nothing
+            now, was = (y.view(torch.uint8 if y.dtype == F8 else torch.int16 if y.dtype == BF16 else I32).cpu() for y in (t, old))
+            keep = torch.ones(4 * 16, dtype=torch.bool)     # cache rows that the two streams did not store
+            keep[slots] = False
+            assert torch.equal(now.transpose(1, 2).flatten(0, 1)[keep], was.transpose(1, 2).flatten(0, 1)[keep])
+
+    sv.kv_len[1] = -1                                       # the second stream ends: the first is served again
+    R, rs = setup([12, 0, 3], [tree, None, None], [11, None, None])
+    go(sv.forward)
+    assert (sv.slots[:R] >= 0).all() and sv.page_count.tolist() == [2, 0, 1] and not torch.isnan(sv.out[:R]).any()
+    go(sv.commit)
+    assert sv.kv_len.tolist() == [13 + 11, -1, 1]
+    held = sv.page_count.tolist()
+    used = [int(p) for s in range(3) for p in sv.table[s, :held[s]].tolist()] + sv.free_pages[:sv.free_count.item()].tolist()
+    assert sorted(used) == list(range(4))

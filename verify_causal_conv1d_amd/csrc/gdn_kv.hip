@@ -17,7 +17,10 @@ namespace {
 //     D_s = sum_{i<s} max(have_i - want_i, 0),   G_s = sum_{i<s} max(want_i - have_i, 0)
 // the released pages go to free_pages[free + D_s ...] and, with avail = free +
 // sum of all drops, page have_s + i of a growing stream is
-// free_pages[avail - 1 - G_s - i].  A stream with G_s + grow_s > avail gets none.
+// free_pages[avail - 1 - G_s - i].  A stream with G_s + grow_s > avail gets none,
+// and page numbers that earlier rounds left in the entries it asked for become
+// -1: they may be pages that other streams hold by now, and attention and commit
+// know a stream without room by these entries alone.
 //
 // Every workgroup computes the sums for itself (n streams are a few KB) and
 // takes its share of the pages and rows.  A page taken that is released by the
@@ -117,9 +120,11 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(const TablesArgs
             if (free0 + i < A.n_pages)
                 A.free_pages[free0 + i] = A.table[(size_t)s * A.max_blocks + S.want[s] + (i - S.drop[s])];
         }
-        for (int i = first; i < min(grows, avail); i += step) {
+        for (int i = first; i < grows; i += step) {
             const int s = find_last(S.grow, n, i);
-            if (served(s)) A.table[(size_t)s * A.max_blocks + S.have[s] + (i - S.grow[s])] = free_page(avail - 1 - i);
+            int32_t &entry = A.table[(size_t)s * A.max_blocks + S.have[s] + (i - S.grow[s])];
+            if (served(s)) entry = free_page(avail - 1 - i);
+            else if (entry >= 0 && entry < A.n_pages) entry = -1;
         }
         // every packed row: a captured pass with fewer rows than it has room for
         // must not leave the slots of an earlier one behind
@@ -364,8 +369,9 @@ __global__ __launch_bounds__(256) void attn_commit_kernel(const AttnCommitArgs A
         const int n = __popc(path), rank = __popc(path & ((1u << (tid & 31)) - 1));
         const int id_to = __shfl(id, rank);
         const bool on = tid < kMaxWindowRows && (path >> tid & 1);
-        // every page that the path leaves or enters has to be in the cache
-        ok = ok && !__ballot(on && (id < 0 || id >= A.kv.n_pages || id_to < 0 || id_to >= A.kv.n_pages));
+        // every page of the window has to be in the cache: a stream that got none
+        // for this pass may hold those of a short path
+        ok = ok && !__ballot(there && (id < 0 || id >= A.kv.n_pages));
         kept = ok ? n : 0;
         if (on && ok) {
             src[rank] = ((id * A.kv.hkv) << A.kv.page_shift) + ((kv + tid) & mask);
