@@ -28,11 +28,15 @@ def test_tables_of_a_stream_without_pages_name_no_page():
             c = tables_case(n, 16, 40 + seed, tree=tree, free=2)
             g = np.random.default_rng(seed)
             table, have = c["block_table"], c["page_count"]
-            pool = c["free_pages"].shape[0]
+            pool, blocks = c["free_pages"].shape[0], table.shape[1]
+            # every stream grows by a page or more, where its table has room
+            c["kv_len"] = np.minimum(np.maximum(c["kv_len"], 16 * have), 16 * blocks - 16).astype(np.int32)
             for s in range(n):      # what lies past a stream's pages: anything, of the pool and not
                 past = table[s, have[s]:]
                 past[:] = np.where(g.random(past.shape) < 0.7, g.integers(0, pool, past.shape), pool + 5)
             check_tables(c, 16)
+            want = ref.tables(16, c["row_start"], c["parent"], c["kv_len"], have, 2, c["free_pages"], table, c["slots"], c["positions"])
+            assert (want["block_table"] == -1).any()
 
 
 @pytest.mark.parametrize("captured", [False, True])
