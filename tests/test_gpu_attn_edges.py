@@ -39,6 +39,20 @@ def test_tables_of_a_stream_without_pages_name_no_page():
             assert (want["block_table"] == -1).any()
 
 
+@pytest.mark.parametrize("n", [3, 40])
+def test_a_finished_stream_with_more_rows_than_its_table_holds(n):
+    """It needs no room for them, and gives its pages back."""
+    announce(f"tables of {n} streams, a finished one with many packed rows")
+    c = tables_case(n, 16, 50, free=100)
+    blocks, rows = c["block_table"].shape[1], np.diff(c["row_start"])
+    c["kv_len"] = np.maximum(c["kv_len"], 0)
+    c["kv_len"][1], rows[1] = -1, 16 * blocks + 1
+    c["row_start"] = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    c["slots"], c["positions"] = (np.full(int(c["row_start"][-1]), -9, np.int32) for _ in range(2))
+    assert c["page_count"][1] > 0
+    check_tables(c, 16)
+
+
 @pytest.mark.parametrize("captured", [False, True])
 @pytest.mark.parametrize("e4m3,hq", [(False, 2), (True, 6), (False, 6)])
 def test_a_round_in_which_the_pool_is_empty(captured, e4m3, hq):

@@ -70,7 +70,7 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(const TablesArgs
         int want = have;
         // a stream that breaks the rules keeps its pages and gets no slots (kv = -1)
         const bool ok = a >= 0 && b >= a && b <= A.total_rows && have >= 0 && have <= A.max_blocks
-                        && kv <= cap && b - a <= cap - max(kv, 0);
+                        && (kv < 0 || (kv <= cap && b - a <= cap - kv));     // finished: no room needed
         if (ok) want = kv < 0 ? 0 : (kv + (b - a) + page - 1) >> A.page_shift;
         if (b < a) falls = 1;
         S.kv[s] = ok ? kv : -1;
