@@ -408,7 +408,9 @@ int gdn_attn_prep(const gdn_kv_cache *cache, int32_t rows, int32_t hq, const uin
  *     on kv_len[s] + its rows
  *   workspace: gdn_attn_workspace_bytes() of device memory, 16-byte aligned
  *     (NULL where that is 0); its contents need not be kept between calls, and
- *     calls that may overlap need their own
+ *     calls that may overlap need their own.  A size serves every call with the
+ *     same hq, hkv and d whose n_streams, total_rows, max_rows and max_kv are no
+ *     larger (a call may need less than it); 0 also for what is refused
  * A stream that breaks a rule (window, parents, lengths over max_kv or
  * max_blocks, a page outside the cache) is skipped: its rows of out are left as
  * they were, and so are rows of no stream.  A stream's results depend on

@@ -166,6 +166,29 @@ def test_workspace_bytes(L):
     assert sizes == sorted(sizes)
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(24, 4, 256), (4, 2, 64), (8, 8, 128), (16, 1, 64), (17, 1, 128), (64, 2, 64)])
+def test_a_workspace_serves_every_smaller_call(L, hq, hkv, d):
+    """Sized once for the largest call, it is enough for all with fewer rows, shorter windows or shorter streams."""
+    def need(total, rows, kv):
+        return gdn.attn_workspace_bytes(hq, hkv, d, 256, total, rows, kv)
+    lengths = (1, 128, 129, 1000, 4096, 8192, 16384, 40000, 262144, 1 << 21)
+    for total in (16, 256):
+        for kv in lengths:
+            sizes = [need(total, r, kv) for r in range(1, 17)]
+            assert sizes == sorted(sizes)                   # more rows a window never need less
+    for most in (4096, 262144, 1 << 21):
+        size = need(256, 16, most)
+        for kv in (k for k in lengths if k <= most):
+            for rows in (1, 2, 3, 5, 9, 16):
+                for total in (1, 64, 256):
+                    if need(total, rows, kv) == 0:
+                        continue
+                    # enough: what is refused is the address, which is looked at after the size
+                    rc = window(L, c=cache(hkv=hkv, d=d), n=256, total=total, max_rows=rows, max_kv=kv, blocks=1 << 16, hq=hq, ws=P8,
+                                wsb=size)
+                    refused(L, rc, gdn.GDN_EINVAL, "workspace must be")
+
+
 def test_binding_refuses_before_the_library():
     cpu = torch.zeros(3, dtype=torch.int32)
     with pytest.raises(TypeError, match="device tensor"):

@@ -785,7 +785,8 @@ size_t gdn_attn_workspace_bytes(const gdn_kv_cache *cache, int32_t n_streams, in
     if (check_cache_sizes(cache, K) != GDN_OK || check_heads(cache, hq, max_kv) != GDN_OK
         || check_counts(n_streams, total_rows, max_rows, 1, cache->page_size) != GDN_OK)
         return 0;
-    return gdn::attn_workspace_bytes(hq, cache->hkv, cache->d, total_rows, max_rows, max_kv);
+    // for any call up to these sizes: windows of fewer rows are never cut into fewer chunks
+    return gdn::attn_workspace_bytes(hq, cache->hkv, cache->d, total_rows, 1, max_kv);
 }
 
 int gdn_attn_window(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,

@@ -58,6 +58,7 @@ constexpr int kMaxAttnKeys = 1 << 21;    // of one stream: a workgroup lists its
 constexpr int kMaxGroups = (1 << 24) - 1;  // workgroups of 256 threads: a launch has less than 2^32 threads
 constexpr int kMaxTableStreams = 4096;   // a workgroup keeps six ints of each in LDS
 
+// of a pass with just these bounds; it does not grow with max_rows
 size_t attn_workspace_bytes(int hq, int hkv, int d, int total_rows, int max_rows, int max_kv);
 
 bool attn_fits(const AttnArgs &A);   // the launch's workgroups can be numbered

@@ -464,7 +464,8 @@ def attn_prep(q, k, v, q_norm, k_norm, inv_freq, positions, slots, q_out, k_cach
 
 
 def attn_workspace_bytes(hq: int, hkv: int, d: int, n_streams: int, total_rows: int, max_rows: int, max_kv: int) -> int:
-    """Bytes of workspace ``attn_window`` needs for passes up to these sizes."""
+    """Bytes of workspace that serve every ``attn_window`` call with these heads and
+    up to these sizes: any total_rows, max_rows and max_kv that are no larger."""
     return int(lib().gdn_attn_workspace_bytes(_pack_cache(0, 0, 0, 0, 1, 16, hkv, d, 0), int(n_streams), int(total_rows),
                                               int(max_rows), int(max_kv), int(hq)))
 
