@@ -9,7 +9,7 @@ from oracle import attn as ref
 from verify_causal_conv1d_amd import gdn
 
 from gpu_util import announce
-from test_gpu_attn import BF16, F8, I32, Server, check_tables, close, f64, i32, tables_case, values
+from test_gpu_attn import BF16, F8, I32, Case, Server, check_tables, close, f64, i32, tables_case, values
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +135,42 @@ def test_a_round_in_which_the_pool_is_empty(captured, e4m3, hq):
     held = sv.page_count.tolist()
     used = [int(p) for s in range(3) for p in sv.table[s, :held[s]].tolist()] + sv.free_pages[:sv.free_count.item()].tolist()
     assert sorted(used) == list(range(4))
+
+
+# ---- extreme values -----------------------------------------------------------------
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("rows,hq,d", [(1, 2, 64), (9, 4, 64), (2, 2, 256), (16, 8, 128)])
+def test_values_near_the_largest(rows, hq, d, e4m3):
+    """Values of up to 2^126 under scores that rise from tile to tile: no sum of weighted values overflows that does not for weights of at most 1."""
+    announce(f"values near the largest, {rows} rows, {hq} heads, d {d}, e4m3 {e4m3}")
+    n = 2200
+    c = Case([n], [rows], hq, 2, d, 64, seed=42)
+    # base-2 scores of -120, but 0 and 7 for two keys of tiles that the same wave takes
+    score = torch.full((n + rows,), -120.0)
+    score[3], score[128 + 5], score[600], score[640 + 200] = 0.0, 7.0, 1.0, 6.0
+    x = torch.randn((n + rows, 2, d), generator=c.g).clamp(-3, 3) * 2.0 ** 124
+    at = torch.arange(n + rows)
+    page, off = c.table[0, at // 64].long(), at % 64
+    c.k[page, :, off] = 0
+    c.k[page, :, off, 0] = score[:, None].to(BF16)
+    c.v[page, :, off] = x.to(BF16)
+    c.q = torch.zeros_like(c.q)
+    c.q[:, :, 0] = 8
+    if e4m3:
+        for name in "kv":
+            p = getattr(c, name).float()
+            sc = p.abs().amax(-1).clamp(min=2.0 ** -100) / 448.0
+            setattr(c, name, (p / sc[..., None]).to(F8))
+            setattr(c, name + "s", sc)
+    scale = np.log(2.0) / 8
+    close(c.run(scale=scale), *c.oracle(scale=scale))
+
+
+@pytest.mark.parametrize("rows,hq", [(1, 2), (9, 4)])
+def test_e4m3_values_near_the_smallest(rows, hq):
+    """Rows with the least scale: weights times scales lie near the least normal number."""
+    announce(f"e4m3 values near the smallest, {rows} rows")
+    c = Case([1500], [rows], hq, 2, 128, 32, e4m3=True, seed=43, amp=3.0)
+    c.vs = torch.where(torch.isnan(c.vs), c.vs, torch.full_like(c.vs, 2.0 ** -100 / 448))
+    close(c.run(), *c.oracle())

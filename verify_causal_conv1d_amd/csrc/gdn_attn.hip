@@ -353,12 +353,13 @@ struct Column {
         float tm = p[0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) tm = fmaxf(tm, p[i]);
-        // Any base within reach of the maximum does: it moves up only when the
-        // maximum has passed it by 2^8, so that O is rarely scaled again (with the
-        // maximum itself, by every second tile of 16 columns).  Weights stay below
-        // 2^8, and P and the sums are floating point.
+        // Any base within reach of the maximum does: it moves only when the maximum
+        // has passed it, and then to 2^8 above that, so that O is rarely scaled again
+        // (with the maximum itself, by every second tile of 16 columns).  Weights are
+        // at most 1, so that no sum of weighted values overflows that would not with
+        // the maximum as the base; P and the sums are floating point.
         tm = max_rows4(tm);
-        tm = tm > mx + 8.0f ? tm : mx;
+        tm = tm > mx ? tm + 8.0f : mx;
         const float base = tm == -INFINITY ? 0.0f : tm;     // no key seen so far: every p is 0
         back = __builtin_amdgcn_exp2f(mx - base);
         moved = __ballot(tm != mx && mx != -INFINITY);      // before the first key O is zero
