@@ -413,7 +413,10 @@ int gdn_attn_prep(const gdn_kv_cache *cache, int32_t rows, int32_t hq, const uin
  *     larger (a call may need less than it); 0 also for what is refused
  * A stream that breaks a rule (window, parents, lengths over max_kv or
  * max_blocks, a page outside the cache) is skipped: its rows of out are left as
- * they were, and so are rows of no stream.  A stream's results depend on
+ * they were, and so are rows of no stream.  Scores, softmax statistics and sums
+ * are in fp32; the weights go into the product with the values to 2^-15 where a
+ * window has up to 16 columns (max_rows * hq / hkv), and in bf16 (2^-8, as the
+ * result's own rounding) where it has more.  A stream's results depend on
  * neither the other streams of the call nor its place in it, bit for bit, for
  * the same max_rows.  A row takes nothing from rows that it does not see,
  * whatever they hold.  total_rows * hq <= 2^26 - 4.

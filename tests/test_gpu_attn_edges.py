@@ -137,6 +137,28 @@ def test_a_round_in_which_the_pool_is_empty(captured, e4m3, hq):
     assert sorted(used) == list(range(4))
 
 
+# ---- precision ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kw", [
+    dict(lens=[0, 5, 300, 700], rows=[1, 1, 1, 1], hq=8, hkv=2, d=256, page=64, gate=True),
+    dict(lens=[17, 640], rows=[1, 1], hq=32, hkv=2, d=128, page=16, amp=6.0),
+    dict(lens=[0, 5, 300, 700], rows=[1, 1, 1, 1], hq=8, hkv=2, d=256, page=64, e4m3=True),
+    dict(lens=[260, 31], rows=[4, 3], hq=8, hkv=2, d=64, page=32, e4m3=True, tree=True, gate=True),
+    dict(lens=[500, 3], rows=[8, 5], hq=4, hkv=2, d=128, page=32, tree=True)], ids=range(5))
+def test_weights_of_few_columns_keep_more_than_bf16(kw):
+    """Up to 16 columns: the only rounding to bf16 is the result's own."""
+    announce(f"precision of the weights {kw}")
+    c = Case(seed=44, **kw)
+    gate = None if c.gate is None else f64(c.gate[:, :, c.d:])
+    want, mag, reach = ref.window(c.page, c.row_start.tolist(), None if c.parent is None else c.parent.tolist(), c.lens, c.table.numpy(),
+                                  f64(c.q), values(c.k, c.ks), values(c.v, c.vs), ref.default_scale(c.d), gate)
+    # half a bf16 step of the result; of the terms 2^-15 from the weights' two bf16 parts (what the first
+    # leaves, less than 2^-7 of the weight, is off by 2^-8 of itself), 2^-24 for each addition of a key, 2^-18 for the fp32 exponentials, sums and gate, and the scores' error (the oracle's window_bound)
+    n = max(a + b for a, b in zip(c.lens, c.rows))
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -15 + 2.0 ** -18 + n * 2.0 ** -24 + 2 * (c.d + 8) * 2.0 ** -24 * reach[..., None]) * 1.01 * mag
+    close(c.run(), want, bound)
+
+
 # ---- extreme values -----------------------------------------------------------------
 
 @pytest.mark.parametrize("e4m3", [False, True])

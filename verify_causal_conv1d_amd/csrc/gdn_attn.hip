@@ -329,11 +329,13 @@ struct Column {
     }
 
     // Weights of a tile's keys from its scores (before scale and k_scale): the
-    // maximum and the sum brought up to date, P times v_scale in bf16.  key0: the lane's first key; seen: the window's rows that the column sees.
-    // TAIL: the tile holds keys of the window or past the end.
-    template <bool TAIL>
+    // maximum and the sum brought up to date, P times v_scale in bf16, and with
+    // SPLIT what that rounding leaves of it in rest, in bf16 again.  key0: the
+    // lane's first key; seen: the window's rows that the column sees.  TAIL: the
+    // tile holds keys of the window or past the end.
+    template <bool TAIL, bool SPLIT>
     __device__ __forceinline__ bf8v weights(const f4v (&acc)[2], float scale, const float4 (&ks)[2], const float4 (&vs)[2], int key0,
-                                            int kv, uint32_t seen)
+                                            int kv, uint32_t seen, bf8v &rest)
     {
         float p[8];
 #pragma unroll
@@ -383,9 +385,36 @@ struct Column {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) p[i] = vis[i] ? p[i] : 0.0f;
         }
-        // P in bf16, rounded to nearest: its error is at most 2^-8 of each term,
-        // that of the bf16 result's own rounding; the sum keeps the fp32 values
-        const uint4 pw = {pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
+        // P goes into the product in bf16, rounded to nearest, while the sum keeps the
+        // fp32 values: an error of up to 2^-8 of each term.  The rest of each weight
+        // in a second product makes that 2^-15, at no cost where memory is the bound
+        // (up to 16 columns: 16 steps 76.4 us, without it 76.5; one of 262,143 e4m3
+        // keys 104.8 and 103.8).  The wide kernel, which is bound by its own
+        // instructions, leaves it out: 16 trees would take 74.6 us instead of 70.4,
+        // over e4m3 rows 82.4 instead of 75.8, for an error that is that of the bf16
+        // result's own rounding.
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = __float_as_uint(p[2 * i]), hi = __float_as_uint(p[2 * i + 1]);
+            w[i] = SPLIT && !F8 ? __builtin_amdgcn_perm(hi, lo, 0x07060302u) : pack2(p[2 * i], p[2 * i + 1]);
+        }
+        if constexpr (SPLIT) {
+            // bf16 values may be infinite, which times a rest of 0 or less is not the
+            // infinity that the weight makes of them: the weight is cut there, not
+            // rounded (its rest is less than 2^-7 of it), and the rest at least 2^-24
+            // of it.  e4m3 codes have no infinities.
+            const uint32_t top = 0xffff0000u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float lo = p[2 * i] - __uint_as_float(w[i] << 16), hi = p[2 * i + 1] - __uint_as_float(w[i] & top);
+                p[2 * i] = F8 ? lo : fmaxf(lo, p[2 * i] * 0x1p-24f);
+                p[2 * i + 1] = F8 ? hi : fmaxf(hi, p[2 * i + 1] * 0x1p-24f);
+            }
+            const uint4 x = {pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
+            rest = __builtin_bit_cast(bf8v, x);
+        }
+        const uint4 pw = {w[0], w[1], w[2], w[3]};
         if constexpr (!F8) rescale();
         return __builtin_bit_cast(bf8v, pw);
     }
@@ -404,16 +433,15 @@ struct Column {
     }
 };
 
-// O^T += V^T P^T for the channels of load h, for each of a wave's column tiles
-template <int D, bool F8, int T>
-__device__ __forceinline__ void add_values(Column<D, F8> (&C)[T], int h, const VPart<F8, VLayout<D, F8>::W> (&v)[8], const bf8v (&pb)[T])
+// O^T += V^T P^T for the channels of load h, P as the sum of its two parts
+template <int D, bool F8>
+__device__ __forceinline__ void add_values(Column<D, F8> &C, int h, const VPart<F8, VLayout<D, F8>::W> (&v)[8], bf8v pb, bf8v rest)
 {
     constexpr int EPL = VLayout<D, F8>::EPL;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         const bf8v a = v_operand(v, i);
-#pragma unroll
-        for (int t = 0; t < T; ++t) C[t].o[h * EPL + i] = mfma(a, pb[t], C[t].o[h * EPL + i]);
+        C.o[h * EPL + i] = mfma(a, rest, mfma(a, pb, C.o[h * EPL + i]));
     }
 }
 
@@ -612,8 +640,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
         return;
     }
 
-    Column<D, F8> C[1];
-    C[0].clear();
+    Column<D, F8> C;
+    C.clear();
     Run16<F8> kk[2][KS];
     VPart<F8, V::W> vv[V::NL][8];
     const uint32_t k_off = n * ROW + 16 * g * ESZ, v_off = 4 * g * ROW + n * V::W * 4;
@@ -661,31 +689,32 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
                 ks[u] = *reinterpret_cast<const float4 *>(A.kv.k_scale + row + 4 * g);
                 vs[u] = *reinterpret_cast<const float4 *>(A.kv.v_scale + row + 4 * g);
             }
+        bf8v pb, rest;
         if (K.k0 + tile * kTile + kTile <= K.kv) {
-            const bf8v pb[1] = {C[0].template weights<false>(acc, A.scale, ks, vs, key0, K.kv, seen)};
-            if constexpr (F8) C[0].rescale();
+            pb = C.template weights<false, true>(acc, A.scale, ks, vs, key0, K.kv, seen, rest);
+            if constexpr (F8) C.rescale();
 #pragma unroll
-            for (int hh = 0; hh < V::NL; ++hh) add_values(C, hh, vv[hh], pb);
+            for (int hh = 0; hh < V::NL; ++hh) add_values(C, hh, vv[hh], pb, rest);
         } else {
-            const bf8v pb[1] = {C[0].template weights<true>(acc, A.scale, ks, vs, key0, K.kv, seen)};
-            if constexpr (F8) C[0].rescale();
+            pb = C.template weights<true, true>(acc, A.scale, ks, vs, key0, K.kv, seen, rest);
+            if constexpr (F8) C.rescale();
 #pragma unroll
             for (int hh = 0; hh < V::NL; ++hh) {
                 if (clean_values(vv[hh], key0, K.len, K.m) && lane == 0) *bad_lds = 1;
-                add_values(C, hh, vv[hh], pb);
+                add_values(C, hh, vv[hh], pb, rest);
             }
         }
         if (more) load_v(tile + kAttnWaves);
     }
 
     // join the waves: the column's maximum over them, each wave's O and l scaled to it
-    const float sum = sum_rows4(C[0].sum);
-    if (g == 0) m_lds[wave * kCols + n] = C[0].mx;
+    const float sum = sum_rows4(C.sum);
+    if (g == 0) m_lds[wave * kCols + n] = C.mx;
     __syncthreads();
     float top = m_lds[n];
 #pragma unroll
     for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, m_lds[w * kCols + n]);
-    const float f = __builtin_amdgcn_exp2f(C[0].mx - (top == -INFINITY ? 0.0f : top));
+    const float f = __builtin_amdgcn_exp2f(C.mx - (top == -INFINITY ? 0.0f : top));
     if (g == 0) l_lds[wave * kCols + n] = sum * f;
     if (n < ncol) {
         float *row = o_lds + (wave * kCols + n) * OP;
@@ -694,7 +723,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float *p = row + hh * 16 * V::EPL + (4 * g + e) * V::EPL;
-                const f4v *o = C[0].o + hh * V::EPL;
+                const f4v *o = C.o + hh * V::EPL;
 #pragma unroll
                 for (int i = 0; i < V::EPL; i += 4)
                     *reinterpret_cast<float4 *>(p + i) = make_float4(o[i][e] * f, o[i + 1][e] * f, o[i + 2][e] * f, o[i + 3][e] * f);
@@ -943,9 +972,11 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
             bf8v pb[T];
             auto get_weights = [&] {
 #pragma unroll
-                for (int c = 0; c < T; ++c)
-                    pb[c] = tail ? C[c].template weights<true>(acc[c], A.scale, ks, vs, key0, K.kv, seen[c])
-                                 : C[c].template weights<false>(acc[c], A.scale, ks, vs, key0, K.kv, seen[c]);
+                for (int c = 0; c < T; ++c) {
+                    bf8v none;
+                    pb[c] = tail ? C[c].template weights<true, false>(acc[c], A.scale, ks, vs, key0, K.kv, seen[c], none)
+                                 : C[c].template weights<false, false>(acc[c], A.scale, ks, vs, key0, K.kv, seen[c], none);
+                }
                 if constexpr (F8)
 #pragma unroll
                     for (int c = 0; c < T; ++c) C[c].rescale();
