@@ -225,6 +225,26 @@ def test_binding_refuses_before_the_library():
         gdn._i32s("kv_len", cpu, 0, 3)
 
 
+def test_binding_imports_on_a_torch_without_raw_calls(L):
+    """A torch built without a GPU lacks its private stream and device calls: what needs no device still works."""
+    import subprocess
+    import sys
+    code = """
+import torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+from verify_causal_conv1d_amd import gdn
+gdn.check_layout([0, 3, 5], 16, 5, [-1, 0, 1, -1, 0])
+assert gdn.attn_workspace_bytes(24, 4, 256, 16, 256, 16, 4096) > 0
+torch.cuda.current_stream = lambda dev: type("S", (), {"cuda_stream": 40 + dev})
+assert gdn._raw_stream(2) == 42 and gdn._current_device is torch.cuda.current_device
+"""
+    root = __file__.rsplit("/tests/", 1)[0]
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert done.returncode == 0, done.stderr
+
+
 # ---- pins of the oracle -----------------------------------------------------
 
 def test_oracle_tables_worked_by_hand():

@@ -329,8 +329,11 @@ def inproj_affine4(shape, x, wq, scales, biases, qkv, a, b, group: int):
 _BF16, _F32, _I32, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
 _pack_cache = struct.Struct("PPPPiiiii4x").pack     # gdn_kv_cache
 _pack_rope = struct.Struct("Piif4x").pack           # gdn_rope
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice     # of a process that holds device tensors already
+# the current stream's handle and the current device, of a process that holds device
+# tensors already: by torch's raw calls where it has them (a build without a GPU does
+# not): 0.2 us a call instead of 1.3
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _wrong(name, t, dtype, dev, size):
