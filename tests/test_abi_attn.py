@@ -225,6 +225,17 @@ def test_binding_refuses_before_the_library():
         gdn._i32s("kv_len", cpu, 0, 3)
 
 
+def test_strides_of_single_rows_and_heads_do_not_count():
+    """One row, or one head, of a tensor whose rows have an odd length: its stride is not looked at."""
+    x = torch.zeros((5, 133), dtype=torch.bfloat16)
+    assert gdn._heads(-1, "q", x[2:3, :128].view(1, 2, 64), (1, 2, 64))[1:] == (0, 64)
+    y = torch.zeros((1, 7, 67), dtype=torch.bfloat16)
+    assert gdn._heads(-1, "k", y[:, 3:4, :64], (1, 1, 64))[1:] == (0, 0)
+    z = torch.zeros((6, 131), dtype=torch.bfloat16).as_strided((3, 1, 64), (136, 67, 1))
+    assert gdn._heads(-1, "v", z, (3, 1, 64))[1:] == (136, 0)
+    assert gdn._heads(-1, "q", x[:, :128].view(5, 2, 64), (5, 2, 64))[1:] == (133, 64)     # five rows: it counts, and is refused
+
+
 def test_binding_imports_on_a_torch_without_raw_calls(L):
     """A torch built without a GPU lacks its private stream and device calls: what needs no device still works."""
     import subprocess

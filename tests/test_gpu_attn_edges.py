@@ -196,3 +196,22 @@ def test_e4m3_values_near_the_smallest(rows, hq):
     c = Case([1500], [rows], hq, 2, 128, 32, e4m3=True, seed=43, amp=3.0)
     c.vs = torch.where(torch.isnan(c.vs), c.vs, torch.full_like(c.vs, 2.0 ** -100 / 448))
     close(c.run(), *c.oracle())
+
+
+# ---- layouts ------------------------------------------------------------------------
+
+def test_one_row_of_a_tensor_with_odd_rows():
+    """One stream's step from a projection whose rows are no multiple of 16 bytes apart."""
+    announce("prep and attention of one row with an odd stride")
+    d, page = 64, 16
+    x = torch.randn((1, 8 * d + 5), device="cuda", generator=torch.Generator("cuda").manual_seed(3)).to(BF16)
+    views = [x[:, a * d:b * d].view(1, b - a, d) for a, b in ((0, 2), (2, 3), (3, 4), (4, 6))]
+    res = []
+    for q, k, v, gate in (views, [t.contiguous() for t in views]):
+        kc, vc = (torch.zeros((1, 1, page, d), dtype=BF16, device="cuda") for _ in range(2))
+        qo, out = (torch.zeros((1, 2, d), dtype=BF16, device="cuda") for _ in range(2))
+        gdn.attn_prep(q, k, v, None, None, torch.ones(8, device="cuda"), i32([4]), i32([4]), qo, kc, vc)
+        gdn.attn_window(i32([0, 1]), i32([4]), i32([[0]]), qo, kc, vc, out, None, max_kv=5, max_rows=1, gate=gate)
+        res.append((qo, kc, vc, out))
+    for a, b in zip(*res):
+        assert torch.equal(a, b) and a.any()

@@ -434,7 +434,8 @@ def _heads(dev, name, t, shape):
     row, head, one = t.stride()
     if one != 1 and t.numel():
         raise ValueError(f"{name}'s channels must be contiguous")
-    return t.data_ptr(), row, head
+    # a single row's or head's stride is never used, and may be anything
+    return t.data_ptr(), row if shape[0] > 1 else 0, head if shape[1] > 1 else 0
 
 
 def _query(q, d):
