@@ -10,6 +10,7 @@ from verify_causal_conv1d_amd import gdn
 
 from gpu_util import announce
 from test_gpu_attn import BF16, F8, I32, Case, Server, check_tables, close, f64, i32, tables_case, values
+from test_gpu_attn import test_prep_matches_oracle as prep_matches_oracle
 
 pytestmark = pytest.mark.gpu
 
@@ -215,3 +216,41 @@ def test_one_row_of_a_tensor_with_odd_rows():
         res.append((qo, kc, vc, out))
     for a, b in zip(*res):
         assert torch.equal(a, b) and a.any()
+
+
+# ---- prompts ------------------------------------------------------------------------
+
+# rows past those whose heads are spread over workgroups (512), where one workgroup goes through all of a row's heads:
+# fewer than it holds at once, one batch of loads, several, a last one that is not full
+@pytest.mark.parametrize("R,hq,hkv,d,rot,page,e4m3,inter,norm", [
+    (513, 24, 4, 256, 64, 64, False, False, True), (700, 24, 4, 256, 64, 64, True, False, True),
+    (530, 36, 9, 256, 256, 16, False, True, True), (530, 36, 9, 256, 256, 16, True, True, True),
+    (515, 64, 8, 128, 100, 32, True, False, True), (515, 63, 9, 128, 128, 32, False, True, False),
+    (600, 130, 10, 64, 64, 128, False, False, True), (600, 130, 10, 64, 22, 128, True, True, True),
+    (1025, 3, 1, 64, 64, 256, True, False, False)])
+def test_prep_of_prompts_matches_oracle(R, hq, hkv, d, rot, page, e4m3, inter, norm):
+    prep_matches_oracle(R, hq, hkv, d, rot, page, e4m3, inter, norm)
+
+
+def test_prep_of_prompts_equals_prep_in_pieces():
+    """The rows of a long call have the bits that they have in calls of few rows."""
+    announce("prep of 1,200 rows against pieces of 100")
+    g = torch.Generator("cuda").manual_seed(45)
+    R, hq, hkv, d, page = 1200, 30, 6, 128, 32
+    x = torch.randn((R, hq + 2 * hkv, d), device="cuda", generator=g).to(BF16)
+    w, freq = torch.rand((2, d), device="cuda", generator=g) + 0.5, 1e4 ** (-torch.arange(32, device="cuda") / 32)
+    pos = torch.randint(0, 1 << 20, (R,), device="cuda", generator=g).to(I32)
+    slots = torch.randperm(R + 80, device="cuda", generator=g)[:R].to(I32)
+    for e4m3 in (False, True):
+        res = []
+        for step in (R, 100):
+            kc, vc = (torch.zeros((40, hkv, page, d), device="cuda").to(F8 if e4m3 else BF16) for _ in range(2))
+            sc = [torch.zeros((40, hkv, page), device="cuda") for _ in range(2)] if e4m3 else [None, None]
+            qo = torch.zeros((R, hq, d), dtype=BF16, device="cuda")
+            for a in range(0, R, step):
+                p = x[a:a + step]
+                gdn.attn_prep(p[:, :hq], p[:, hq:hq + hkv], p[:, hq + hkv:], w[0], w[1], freq, pos[a:a + step], slots[a:a + step],
+                              qo[a:a + step], kc, vc, *sc)
+            res.append([qo, kc.view(torch.uint8), vc.view(torch.uint8)] + (sc if e4m3 else []))
+        for a, b in zip(*res):
+            assert torch.equal(a, b) and a.any()
