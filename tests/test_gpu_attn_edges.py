@@ -254,3 +254,17 @@ def test_prep_of_prompts_equals_prep_in_pieces():
             res.append([qo, kc.view(torch.uint8), vc.view(torch.uint8)] + (sc if e4m3 else []))
         for a, b in zip(*res):
             assert torch.equal(a, b) and a.any()
+
+
+# ---- long streams ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("n,rows,hq,d,e4m3,tree", [
+    (16384 - 8, 9, 2, 64, False, True), (16384 + 1, 12, 2, 64, True, False), (33000, 16, 2, 64, False, False),
+    (40003, 9, 2, 128, True, True), (65536 - 9, 9, 2, 64, False, False), (65536 + 5, 16, 2, 64, True, True), (70001, 3, 8, 64, False, True)])
+def test_wide_windows_over_long_streams(n, rows, hq, d, e4m3, tree):
+    """More than 16 columns over streams whose chunks are longer than the usual 512 keys, up to 64 of them, beside short ones."""
+    announce(f"{rows} rows of {hq} heads over {n} keys, d {d}, e4m3 {e4m3}, tree {tree}")
+    c = Case([40, n, 700], [rows, rows, 2], hq, 1, d, 256, e4m3=e4m3, tree=tree, seed=46)
+    out = c.run()
+    close(out, *c.oracle())
+    assert torch.equal(c.run(max_kv=1 << 18), out)
