@@ -313,6 +313,13 @@ int gdn_inproj_affine4(const gdn_shape *shape, int32_t rows, int32_t hidden, int
  * page_size + row.  page_size is 16, 32, 64, 128 or 256, d is 64, 128 or 256,
  * and n_pages * hkv * page_size < 2^31 (GDN_EUNSUPPORTED otherwise).  Query
  * head h reads kv head h / (hq / hkv).  A step is a window of one row.
+ *
+ * row_start must not fall.  Every stream is looked at by itself: one whose own
+ * two entries break the rules is skipped, the others are served as ever.  Where
+ * a fall makes the windows of two streams overlap instead, what their common
+ * rows get (slots, positions, results) is undefined, and with it what these
+ * streams' next rows see; streams without common rows are not touched by it,
+ * and no access leaves the arrays.  gdn_check_layout finds both on the host.
  */
 enum gdn_kv_format {
     GDN_KV_BF16 = 0,

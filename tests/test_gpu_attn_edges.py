@@ -9,7 +9,7 @@ from oracle import attn as ref
 from verify_causal_conv1d_amd import gdn
 
 from gpu_util import announce
-from test_gpu_attn import BF16, F8, I32, Case, Server, check_tables, close, f64, i32, tables_case, values
+from test_gpu_attn import BF16, F8, I32, Case, Server, check_tables, close, f64, i32, run_tables, tables_case, values
 from test_gpu_attn import test_prep_matches_oracle as prep_matches_oracle
 
 pytestmark = pytest.mark.gpu
@@ -216,6 +216,37 @@ def test_one_row_of_a_tensor_with_odd_rows():
         res.append((qo, kc, vc, out))
     for a, b in zip(*res):
         assert torch.equal(a, b) and a.any()
+
+
+@pytest.mark.parametrize("by", [-3, -4, 3, 4])
+def test_windows_that_overlap_touch_no_other_stream(by):
+    """A small fall of row_start, after which two windows share rows: streams without shared rows get their pages and slots as ever."""
+    announce(f"tables, overlapping windows, an entry off by {by}")
+    n, at = 70, 33
+    kv = np.arange(300, 300 + 7 * n, 7).astype(np.int32)
+    rs = np.arange(0, 2 * n + 1, 2).astype(np.int32)
+    rs[at] += by
+    start = rs.tolist()
+    window = {s: set(range(start[s], start[s + 1])) for s in range(n)}
+    alone = [s for s in range(n) if s not in (at - 1, at) and not window[s] & (window[at - 1] | window[at])]
+    assert n - 5 <= len(alone) < n - 2
+    for tree in (False, True):
+        d = tables_case(n, 16, 48, tree=False, free=300)
+        d["kv_len"], d["slots"], d["positions"] = kv, np.full(2 * n, -9, np.int32), np.full(2 * n, -9, np.int32)
+        d["block_table"] = np.concatenate([d["block_table"], np.full((n, 60), -7, np.int32)], 1)
+        d["free_pages"] = np.concatenate([d["free_pages"], np.arange(d["free_pages"].shape[0], 5000)]).astype(np.int32)
+        d["free_pages"][300:4000] = np.arange(1300, 5000)
+        d["free_count"][:] = 4000
+        d["row_start"], d["parent"] = rs, np.full(2 * n, -1, np.int32) if tree else None
+        before = sorted(p for s in range(n) for p in d["block_table"][s, :d["page_count"][s]]) + sorted(d["free_pages"][:4000])
+        out = {k: v.cpu().numpy() for k, v in run_tables(d, 16, False).items()}
+        table, held = out["block_table"], out["page_count"]
+        after = [p for s in range(n) for p in table[s, :held[s]]] + list(out["free_pages"][:out["free_count"][0]])
+        assert sorted(after) == sorted(before)              # no page is lost or held twice
+        for s in alone:
+            for t in range(2):
+                j = int(kv[s]) + t
+                assert held[s] * 16 > j and out["slots"][2 * s + t] == table[s, j // 16] * 16 + j % 16, (s, t)
 
 
 # ---- prompts ------------------------------------------------------------------------
