@@ -360,6 +360,11 @@ typedef struct gdn_kv_cache {
  * another stream's by now) become -1.  gdn_attn_window and gdn_attn_commit then
  * skip the stream, and its kv_len stays.  The mixer's commits do not look at
  * pages: give them accept_row -1 for a stream whose slots are -1.
+ * Pages are not counted: each is on the stack or one stream's.  A page that the
+ * tables of two streams hold (gdn_attn_window reads such pages like any other)
+ * would go to the stack with the first stream that lets it go, while the other
+ * still reads it; streams that share pages need a caller that takes them out of
+ * this call's hands.
  * n <= 4096, total_rows and n * max_blocks <= 2^30.
  */
 int gdn_kv_tables(int32_t n_streams, int32_t total_rows, int32_t page_size, int32_t n_pages,
