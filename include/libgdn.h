@@ -302,7 +302,8 @@ int gdn_inproj_affine4(const gdn_shape *shape, int32_t rows, int32_t hidden, int
  * A hybrid model's other layers are gated full attention over a growing
  * key-value cache.  The calls below run them beside the mixer's: the same
  * packed rows, windows, trees and accepted rows, every count read on the
- * device.  (The engine on the pages keeps its gated attention in qwen35.cu,
+ * device.  gdn_kv_tables and gdn_attn_prep take prompts, too; attention of whole
+ * prompts is not among these calls.  (The engine on the pages keeps its gated attention in qwen35.cu,
  * cuts decode attention into key chunks at logical positions, and stores e4m3
  * cache rows with an fp32 scale of amax / 448.)
  *
@@ -417,7 +418,8 @@ int gdn_attn_prep(const gdn_kv_cache *cache, int32_t rows, int32_t hq, const uin
  *   q, out [total_rows][hq][d] bf16;  gate bf16 with row and head strides in
  *     elements (multiples of 4; 8-byte aligned), or NULL
  *   max_rows 1..16 and max_kv (at most 2^21): bounds on every window's rows and
- *     on kv_len[s] + its rows
+ *     on kv_len[s] + its rows; they size the launch, and total_rows is at most
+ *     n_streams * max_rows (a max_kv far above all lengths costs some time)
  *   workspace: gdn_attn_workspace_bytes() of device memory, 16-byte aligned
  *     (NULL where that is 0); its contents need not be kept between calls, and
  *     calls that may overlap need their own.  A size serves every call with the

@@ -24,8 +24,9 @@
 //  - more, attn_wide_kernel: each wave has a column tile of its own, and K and
 //    V pass through LDS once for all of them.
 // (16 streams of 700 to 8,191 keys, 24 query and 4 kv heads of 256: with 24
-// columns the wide kernel takes 57 us and the other one, reading K and V once a
-// tile, 69; with 48 columns 61 and 97.  One stream of 500 keys: 16 and 17.)
+// columns the wide kernel takes 53 us and the other one, reading K and V once a
+// tile, 69; with 48 columns 59 and 97.  One stream of 500 keys and 18 columns:
+// 15.7 and 14.4.)
 #include "gdn_attn.h"
 #include "gdn_device.h"
 #include "gdn_internal.h"
@@ -60,10 +61,10 @@ __host__ __device__ inline int at_most(int a, int b) { return a < b ? a : b; }
 // kChunkLeast; more once there are 4 of them, up to chunk_usual; more again once
 // there are 32, up to chunk_long; and more than that once there are kMaxChunks.
 // Short chunks spread a lone stream over the chip, long ones write fewer parts
-// and begin less often: 64 steps of 2,000 to 4,096 keys take 157 us in chunks of
-// 256 and 181 in chunks of 128, one step of 500 keys 14.6 and 13.1; 16 steps of
-// up to 16,384 keys 100 us in chunks of 256 and 87 of 512; a tree over 500 keys
-// 28 us in one wide chunk and 17 in chunks of 128.
+// and begin less often: 64 steps of 2,000 to 4,096 keys take 164 us in chunks of
+// 256 and 186 in chunks of 128, one step of 500 keys 15.5 and 13.4; 16 steps of
+// up to 16,384 keys 82 us in chunks of 256 and 77 of 512; a tree of 8 rows over
+// 500 keys 27 us in one wide chunk and 17 in chunks of 128.
 constexpr int kChunkLeast = 128;
 __host__ __device__ inline int chunk_usual(bool wide) { return wide ? 512 : 256; }
 __host__ __device__ inline int chunk_long(bool wide) { return wide ? 1024 : 512; }
@@ -75,9 +76,11 @@ __host__ __device__ inline int chunk_most(int len, bool wide)
     return at_least(b, ceil_div(len, kMaxChunks));
 }
 
-// Its keys: equal chunks, in whole units.  A sixteenth more than the most is
-// allowed (in whole units, too), so that a few rows past a round number do not
-// make another chunk.
+// Its keys: equal chunks, in whole units.  Up to a sixteenth more than the most is
+// allowed, so that a few rows past a round number do not make another chunk; but
+// in whole units, too, which is nothing before the most is sixteen units (wide:
+// from 32,737 keys, else from 131,009).  Below that they do make one: 8,200 keys
+// are 16 wide chunks of 512 and one of 8.
 __host__ __device__ inline int chunk_unit(bool wide) { return wide ? 64 : 128; }
 __host__ __device__ inline int chunk_keys(int len, bool wide)
 {
@@ -420,8 +423,8 @@ struct Column {
     }
 
     // O brought up to date, after weights: by the caller for e4m3, once for tiles
-    // with and without TAIL (16 trees of 16 e4m3 rows 80 us, in weights 84), in
-    // weights for bf16 (69.7 us, by the caller 71.5)
+    // with and without TAIL (16 trees of 16 e4m3 rows 75.7 us, in weights 80.4), in
+    // weights for bf16 (70.1 us, by the caller 71.6)
     __device__ __forceinline__ void rescale()
     {
         if (moved) {
@@ -490,9 +493,12 @@ struct Chunk {
 
 // The pieces of all streams, in stream order.  How many there are follows from
 // the lengths, which only the device knows.  Every wave finds its pieces by
-// itself, with no workgroup for a piece that is not there before those that
-// are: lane l holds stream first + l of a block of 64 streams, and the pieces of
-// the block up to and including that stream's.
+// itself: lane l holds stream first + l of a block of 64 streams, and the pieces
+// of the block up to and including that stream's.  Within a block no workgroup
+// for a piece that is not there comes before those that are.  attn_kernel's grid
+// has room for max_kv keys of every stream, a row of workgroups a block, and those
+// that find nothing end at once, but are not free: 512 steps of 500 keys take 264
+// us under a max_kv of 501 and 423 under 262,144, 16 such steps 15.7 and 18.1.
 struct Pieces {
     int first = -64, before = 0, incl = 0;    // of the block: first stream, pieces before it, running sum
     int r0 = 0, m = 0, kv = 0;
@@ -596,7 +602,7 @@ constexpr int kAttnThreads = 256, kAttnWaves = 4;
 // transposition (its rows are rows of the A operand); V's 8 x 8 blocks of a lane
 // are turned by byte permutes as they are used.  Bounded by memory: 16 streams
 // of 1,000 to 16,384 keys (374 MB) take 76 us with the join, 4.9 TB/s; one of
-// 262,143 keys in e4m3 (545 MB) 104 us, 5.3 TB/s.  A short stream is bounded by
+// 262,143 keys in e4m3 (545 MB) 105 us, 5.2 TB/s.  A short stream is bounded by
 // the chain of layout, page numbers, first tile and join: 8 us for 100 keys.
 template <int D, bool F8>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
@@ -773,7 +779,7 @@ __device__ __forceinline__ void wait_and_meet()
 //
 // One workgroup of 8 waves stays on each CU and goes through its pieces.  16
 // draft trees of up to 16 rows over 700 to 8,191 keys (96 columns, 212 MB): 70 us
-// with the join, which has 27 MB of parts to read (11 us).  A tile of 32 keys
+// with the join (11 us, what bounds it is said there).  A tile of 32 keys
 // takes a CU about 1.2 us when nothing else runs there (each wave reads the
 // tile's 32 KB from LDS, and two of the waves with columns share a SIMD); how
 // evenly the pieces fall on the CUs costs the rest.  Over e4m3 rows (110 MB) they
@@ -934,8 +940,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
             const int first = K.k0 + tile * S::KEYS + sub * kTile;
             if (sub > 0 && first >= K.k1) break;
             const int key0 = first + 4 * g;
-            // all reads of the keys first, then the products as they arrive, then
-            // the reads of the first values, to be there when the weights are
+            // all reads of the keys first (the products wait for the last of them),
+            // then the products, and under them the reads of the first values, to be
+            // there when the weights are; over e4m3 rows the weights wait for the
+            // scales, and so for the values, whose reads are asked for beside them
             Run16<F8> kk[2][KS];
 #pragma unroll
             for (int k = 0; k < KS; ++k)
@@ -1122,7 +1130,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
 // reads does not wait for the stream to be found: the first parts, the sums and
 // the gates are asked for at once, by the row alone (a stream has at most
 // A.chunks chunks; what lies past its own is not used), and the streams' windows
-// are looked at 64 at a time.
+// are looked at 64 at a time.  The price: a (row, head) of a short stream asks for
+// more parts than it has.  The 16 trees above, the longest of which has 17 chunks
+// and ten of which have 4 to 6, ask for 58 MB where their chunks wrote 25, and the
+// kernel's 11 us are the time of those bytes.
 constexpr int kJoinWaves = 4, kJoinBatch = 16;      // loads in flight
 
 template <int D>

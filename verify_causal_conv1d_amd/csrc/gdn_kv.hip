@@ -341,7 +341,7 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, co
 
 // ---- commit of accepted paths ----------------------------------------------
 //
-// One workgroup a stream, 16 trees in 5 us on the GPU, one in 2.6: two dependent
+// One workgroup a stream, 16 trees in 4.6 us on the GPU, one in 2.7: two dependent
 // loads (layout, then page numbers), then the rows.  The path's rows i_0 < i_1 < ... move from cache
 // rows kv_len + i_j to kv_len + j.  A thread owns 16-byte columns (or one
 // scale) of the rows and holds every source in registers before it stores the
@@ -418,10 +418,10 @@ __global__ __launch_bounds__(256) void attn_commit_kernel(const AttnCommitArgs A
 
 hipError_t launch_tables(const TablesArgs &A, hipStream_t stream)
 {
-    // A single workgroup for a small call (16 streams of 16 rows: 8.5 us a call
-    // from Python, 8.8 with 32 workgroups, and one launch where the counts are
-    // updated in place); 500 streams with 12,163 rows take it 44 us, and 32
-    // workgroups 8.3.
+    // A single workgroup for a small call (16 streams of 16 rows: 6.8 us on the GPU,
+    // 6.5 with 32 workgroups, but one launch also where the counts are updated in
+    // place); 500 streams with 12,163 rows take it 44 us, and 32 workgroups 7.3
+    // (8.6 us a call from Python; with the counts in place, in two launches, 12.1).
     const size_t lds = sizeof(int) * (6 * (size_t)A.n_streams + 1);
     if (A.n_streams <= 32 && A.total_rows <= kTablesThreads) {
         tables_kernel<<<1, kTablesThreads, lds, stream>>>(A, 1, 1);
@@ -438,10 +438,10 @@ template <int D>
 static void launch_prep_d(const PrepArgs &A, hipStream_t stream)
 {
     // A workgroup has all of a row's heads, or where the rows are few, as many as
-    // its lanes hold at once (32 heads of 256: one row 3.9 us on the GPU instead
-    // of 8.7, 249 rows 4.6 instead of 7.2; from about 500 rows on the angles that
-    // every workgroup works out again cost more: 1,024 rows 12.8 us instead of
-    // 10.9, 8,306 rows 88 instead of 68)
+    // its lanes hold at once (on the GPU, 32 heads of 256: one row 3.7 us instead of
+    // 6.8, 249 rows of 48 heads of 128 4.5 instead of 5.3; from about 500 rows on the
+    // angles that every workgroup works out again cost more: 1,024 rows 12.5 us
+    // instead of 11.0, 8,306 rows 86 instead of 62)
     const int heads = A.hq + 2 * A.kv.hkv, at_once = kPrepThreads / (D / 8);
     const int span = A.rows <= kPrepFewRows && heads > at_once ? at_once : heads;
     prep_kernel<D><<<dim3(A.rows, (heads + span - 1) / span), kPrepThreads, 0, stream>>>(A, span);
