@@ -303,9 +303,9 @@ int gdn_inproj_affine4(const gdn_shape *shape, int32_t rows, int32_t hidden, int
  * key-value cache.  The calls below run them beside the mixer's: the same
  * packed rows, windows, trees and accepted rows, every count read on the
  * device.  gdn_kv_tables and gdn_attn_prep take prompts, too; attention of whole
- * prompts is not among these calls.  (The engine on the pages keeps its gated attention in qwen35.cu,
- * cuts decode attention into key chunks at logical positions, and stores e4m3
- * cache rows with an fp32 scale of amax / 448.)
+ * prompts is not among these calls.  (The engine on the pages keeps its gated
+ * attention in qwen35.cu, cuts decode attention into key chunks at logical
+ * positions, and stores e4m3 cache rows with an fp32 scale of amax / 448.)
  *
  * The cache is paged.  K and V are [n_pages][hkv][page_size][d] (bf16, or
  * e4m3 codes with one fp32 scale a row in [n_pages][hkv][page_size]); a

@@ -190,6 +190,30 @@ def test_values_near_the_largest(rows, hq, d, e4m3):
     close(c.run(scale=scale), *c.oracle(scale=scale))
 
 
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("rows", [1, 2, 9])
+def test_infinite_values_under_small_weights(rows, d):
+    """An infinite value makes its channel infinite as long as its weight is a number above 0, a power of two among them."""
+    announce(f"infinite values under small weights, {rows} rows, d {d}")
+    n = 700
+    c = Case([n], [rows], 4, 2, d, 64, seed=49)
+    at = torch.arange(n + rows)
+    page, off = c.table[0, at // 64].long(), at % 64
+    c.k[page, :, off] = 0
+    c.q = torch.zeros_like(c.q)
+    c.q[:, :, 0] = 8
+    scale = float(np.log(2.0) / 8)
+    for key, score in ((130, -1.0), (131, -60.0), (400, -98.0), (401, -110.0)):
+        for sign in (1.0, -1.0):
+            k, v = c.k.clone(), c.v.clone()
+            c.k[page[key], :, off[key], 0] = score
+            c.v[page[key], :, off[key], 5] = sign * float("inf")
+            got = f64(c.run(scale=scale))
+            c.k, c.v = k, v
+            assert np.all(got[:, :, 5] == sign * np.inf), (key, sign)
+            assert np.all(np.isfinite(np.delete(got, 5, axis=2))), (key, sign)
+
+
 @pytest.mark.parametrize("rows,hq", [(1, 2), (9, 4)])
 def test_e4m3_values_near_the_smallest(rows, hq):
     """Rows with the least scale: weights times scales lie near the least normal number."""
