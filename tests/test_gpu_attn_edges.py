@@ -242,6 +242,23 @@ def test_one_row_of_a_tensor_with_odd_rows():
         assert torch.equal(a, b) and a.any()
 
 
+def test_two_broken_entries_of_row_start_skip_their_streams_only():
+    """The start of a block of 64 streams and the last entry at once."""
+    announce("attention of 70 streams, two broken entries of row_start")
+    c = Case([300 + 7 * s for s in range(70)], [2] * 70, 4, 2, 64, 32, seed=50)
+    good = c.run()
+    for first in (10 ** 6, -5):
+        for last in (-5, 3, 10 ** 6):
+            rs = c.row_start.clone()
+            rs[64], rs[70] = first, last
+            got = c.run(row_start=rs)
+            for s in range(70):
+                if s in (63, 64, 69):
+                    assert torch.isnan(got[2 * s:2 * s + 2]).all(), (first, last, s)
+                else:
+                    assert torch.equal(got[2 * s:2 * s + 2], good[2 * s:2 * s + 2]), (first, last, s)
+
+
 @pytest.mark.parametrize("by", [-3, -4, 3, 4])
 def test_windows_that_overlap_touch_no_other_stream(by):
     """A small fall of row_start, after which two windows share rows: streams without shared rows get their pages and slots as ever."""

@@ -1173,9 +1173,15 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const AttnArgs A,
         return __ballot(s < A.n_streams && stream_window(A, s, r0, m, kv) && r >= r0 && r < r0 + m);
     };
     uint64_t found = holder(block);
-    // not where it should be: a row of no stream, or row_start decreases somewhere
-    if (!found && A.n_streams > 64 && r < A.row_start[A.n_streams])
-        for (block = 0; !found && 64 * block < A.n_streams; ++block) found = holder(block);
+    // not where it should be: a row of no stream, past the last one in the last
+    // block, or an entry of row_start is broken and leads elsewhere
+    if (!found && A.n_streams > 64) {
+        const int s = 64 * block + lane;
+        const bool past = block == (A.n_streams - 1) / 64 && r >= A.row_start[A.n_streams]
+                          && !__ballot(s < A.n_streams && A.row_start[s + 1] < A.row_start[s]);
+        if (!past)
+            for (block = 0; !found && 64 * block < A.n_streams; ++block) found = holder(block);
+    }
     if (!found) return;
     const int l = __builtin_ctzll(found);
     const int nch = chunk_count(__builtin_amdgcn_readlane(kv, l) + __builtin_amdgcn_readlane(m, l), is_wide);
