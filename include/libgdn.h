@@ -392,8 +392,8 @@ int gdn_kv_tables(int32_t n_streams, int32_t total_rows, int32_t page_size, int3
  *   positions, slots [rows] int32 (gdn_kv_tables); a row whose slot is outside
  *     the cache stores no key and value
  *   q_out [rows][hq][d] bf16
- * GDN_KV_E4M3 rows get scale = max(max|y|, 2^-100) / 448 and codes y / scale
- * rounded to nearest.  No two rows may have the same slot.  rows < 2^24.
+ * GDN_KV_E4M3 rows get scale = max(max|y|, 2^-100) / 448 and codes y / scale,
+ * an fp32 quotient, rounded to nearest.  No two rows may have the same slot.  rows < 2^24.
  */
 typedef struct gdn_rope {
     const float *inv_freq;   /* [rot_dim / 2], device */
