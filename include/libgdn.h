@@ -319,8 +319,9 @@ int gdn_inproj_affine4(const gdn_shape *shape, int32_t rows, int32_t hidden, int
  * two entries break the rules is skipped, the others are served as ever.  Where
  * a fall makes the windows of two streams overlap instead, what their common
  * rows get (slots, positions, results) is undefined, and with it what these
- * streams' next rows see; streams without common rows are not touched by it,
- * and no access leaves the arrays.  gdn_check_layout finds both on the host.
+ * streams' next rows see; streams without common rows are not touched by it
+ * (but gdn_kv_tables takes pages for every window as it stands), and no access
+ * leaves the arrays.  gdn_check_layout finds both on the host.
  */
 enum gdn_kv_format {
     GDN_KV_BF16 = 0,
