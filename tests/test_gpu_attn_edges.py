@@ -214,6 +214,21 @@ def test_infinite_values_under_small_weights(rows, d):
             assert np.all(np.isfinite(np.delete(got, 5, axis=2))), (key, sign)
 
 
+@pytest.mark.parametrize("rows", [1, 2, 9])
+def test_an_infinite_scale_makes_its_row_infinite(rows):
+    """A cached e4m3 row of codes other than 0 under an infinite scale: infinities of the codes' signs."""
+    announce(f"an infinite scale, {rows} rows")
+    c = Case([300, 40], [rows, rows], 4, 2, 64, 16, e4m3=True, seed=51)
+    clean = c.run()
+    page, off = int(c.table[0, 70 // 16]), 70 % 16
+    c.vs[page, :, off] = float("inf")
+    codes = c.v.view(torch.uint8)
+    codes[page, :, off] = torch.where(torch.arange(64) % 2 == 0, 0x38, 0xB8).to(torch.uint8)      # 1 and -1
+    got = f64(c.run())
+    assert np.all(got[:rows, :, 0::2] == np.inf) and np.all(got[:rows, :, 1::2] == -np.inf)
+    assert np.array_equal(got[rows:], f64(clean)[rows:])
+
+
 @pytest.mark.parametrize("rows,hq", [(1, 2), (9, 4)])
 def test_e4m3_values_near_the_smallest(rows, hq):
     """Rows with the least scale: weights times scales lie near the least normal number."""

@@ -403,16 +403,15 @@ struct Column {
             w[i] = SPLIT && !F8 ? __builtin_amdgcn_perm(hi, lo, 0x07060302u) : pack2(p[2 * i], p[2 * i + 1]);
         }
         if constexpr (SPLIT) {
-            // bf16 values may be infinite, which times a rest of 0 or less is not the
-            // infinity that the weight makes of them: the weight is cut there, not
-            // rounded (its rest is less than 2^-7 of it), and where it is not 0 the
-            // rest is at least the least normal number.  e4m3 codes have no infinities.
-            const uint32_t top = 0xffff0000u;
+            // What is infinite has to stay so.  bf16 values times a rest of 0 or less do
+            // not: the weight is cut there, not rounded (its rest is less than 2^-7 of
+            // it), and where it is not 0 the rest is at least the least normal number.
+            // e4m3 codes have no infinities, but their weights may be infinite with
+            // their scale; their rest is that then, not NaN.
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float lo = p[2 * i] - __uint_as_float(w[i] << 16), hi = p[2 * i + 1] - __uint_as_float(w[i] & top);
-                p[2 * i] = F8 ? lo : fmaxf(lo, fminf(p[2 * i], 0x1p-126f));
-                p[2 * i + 1] = F8 ? hi : fmaxf(hi, fminf(p[2 * i + 1], 0x1p-126f));
+            for (int i = 0; i < 8; ++i) {
+                const float left = p[i] - __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+                p[i] = F8 ? fminf(left, fabsf(p[i])) : fmaxf(left, fminf(p[i], 0x1p-126f));
             }
             const uint4 x = {pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
             rest = __builtin_bit_cast(bf8v, x);
