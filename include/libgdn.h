@@ -302,13 +302,14 @@ int gdn_inproj_affine4(const gdn_shape *shape, int32_t rows, int32_t hidden, int
  * A hybrid model's other layers are gated full attention over a growing
  * key-value cache.  The calls below run them beside the mixer's: the same
  * packed rows, windows, trees and accepted rows, every count read on the
- * device.  gdn_kv_tables and gdn_attn_prep take prompts, too; attention of whole
- * prompts is not among these calls.  (The engine on the pages keeps its gated
+ * device.  gdn_kv_tables and gdn_attn_prep take prompts, too, and
+ * gdn_attn_prompt attends over them.  (The engine on the pages keeps its gated
  * attention in qwen35.cu, cuts decode attention into key chunks at logical
  * positions, and stores e4m3 cache rows with an fp32 scale of amax / 448.)
  *
  * The cache is paged.  K and V are [n_pages][hkv][page_size][d] (bf16, or
- * e4m3 codes with one fp32 scale a row in [n_pages][hkv][page_size]); a
+ * e4m3 codes with one fp32 scale a row in [n_pages][hkv][page_size], or 4-bit
+ * codes with an exponent byte for every 32 channels of a row); a
  * stream's cache row i is row i % page_size of page block_table[s][i /
  * page_size], block_table [n][max_blocks] int32.  Slot numbers are page *
  * page_size + row.  page_size is 16, 32, 64, 128 or 256, d is 64, 128 or 256,
@@ -325,12 +326,23 @@ int gdn_inproj_affine4(const gdn_shape *shape, int32_t rows, int32_t hidden, int
  */
 enum gdn_kv_format {
     GDN_KV_BF16 = 0,
-    GDN_KV_E4M3 = 1   /* OCP e4m3, value = code * scale of its row */
+    GDN_KV_E4M3 = 1,  /* OCP e4m3, value = code * scale of its row */
+    GDN_KV_MXFP4 = 4  /* OCP MXFP4, value = code * 2^(e - 127) of its block */
 };
 
+/*
+ * GDN_KV_MXFP4 rows are those of the OCP Microscaling Formats 1.0: e2m1 codes
+ * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two a byte with the even
+ * channel in the low half, and exponent bytes e in [n_pages][hkv][page_size]
+ * [d / 32], whose addresses go into k_scale and v_scale.  e is 1..252, or 255
+ * where the block's values are all NaN (253 and 254 are read as 255); so every
+ * value is a bf16 number, and the calls that read it round nothing.  4.25 bits a
+ * value: 136 bytes for a key of 256 channels instead of 512.
+ */
 typedef struct gdn_kv_cache {
     void *k, *v;                /* [n_pages][hkv][page_size][d], 16-byte aligned  */
-    float *k_scale, *v_scale;   /* [n_pages][hkv][page_size], 16-byte aligned, GDN_KV_E4M3 only */
+    float *k_scale, *v_scale;   /* [n_pages][hkv][page_size], 16-byte aligned, GDN_KV_E4M3 only;
+                                   GDN_KV_MXFP4: exponent bytes (cast) */
     int32_t n_pages, page_size;
     int32_t hkv, d;
     int32_t format;             /* enum gdn_kv_format */
@@ -394,7 +406,14 @@ int gdn_kv_tables(int32_t n_streams, int32_t total_rows, int32_t page_size, int3
  *     the cache stores no key and value
  *   q_out [rows][hq][d] bf16
  * GDN_KV_E4M3 rows get scale = max(max|y|, 2^-100) / 448 and codes y / scale,
- * an fp32 quotient, rounded to nearest.  No two rows may have the same slot.  rows < 2^24.
+ * an fp32 quotient, rounded to nearest.  GDN_KV_MXFP4 blocks get, from the bits
+ * of amax = max|y| over their 32 channels in fp32,
+ *     e = min(max(((bits(amax) + 2^21) >> 23) - 2, 25), 252)
+ * (so that amax / 2^(e - 127) is in [3.5, 7), what rounds to 4 or 6) and codes
+ * y / 2^(e - 127) rounded to nearest, ties to even, at most 6; a block with an
+ * infinite or NaN value gets e = 255 and codes 0.  There y is a key's norm and
+ * rotation in fp64 from the bf16 inputs, with one rounding to fp32.  No two rows
+ * may have the same slot.  rows < 2^24.
  */
 typedef struct gdn_rope {
     const float *inv_freq;   /* [rot_dim / 2], device */
@@ -445,6 +464,55 @@ int gdn_attn_window(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_
                     const int32_t *block_table, const uint16_t *q, const uint16_t *gate,
                     int64_t gate_row_stride, int64_t gate_head_stride, float scale, uint16_t *out,
                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Attention of whole prompts, fresh (kv_len[s] 0), resumed, or in pieces, packed
+ * rows of any lengths whose keys and values are already stored (gdn_attn_prep):
+ * row t of stream s sees cache rows 0 .. kv_len[s] + t,
+ *     out = sigmoid(gate) * softmax(scale q K^T) V.
+ *   q, out [total_rows][hq][d] bf16;  gate as in gdn_attn_window
+ *   max_kv (at most 2^21): a bound on kv_len[s] + the stream's rows
+ *   workspace: gdn_attn_prompt_workspace_bytes() of device memory, 16-byte
+ *     aligned (NULL where that is 0); its contents need not be kept between
+ *     calls, and calls that may overlap need their own.  A size serves every call
+ *     with the same hq, hkv and d whose total_rows and max_kv are no larger; 0
+ *     also for what is refused
+ * A stream without rows has nothing to do; one that breaks a rule (its window,
+ * lengths over max_kv or max_blocks, a page outside the cache) is skipped: its
+ * rows of out are left as they were, and so are rows of no stream.  Scores,
+ * softmax statistics and sums are in fp32; the weights go into the product with
+ * the values in bf16, rounded to nearest (2^-8 at most, as the result's own
+ * rounding).  A call of few rows over long streams is cut along the keys, by
+ * total_rows, max_kv and the heads alone; given these, a stream's results depend
+ * on neither the other streams nor its place in the call, bit for bit.  A row
+ * takes nothing from rows that it does not see, whatever they hold.  Streams of a
+ * row or two are taken, but each fills its tile of 256 (row, head) pairs with
+ * nothing: steps belong into gdn_attn_window.  total_rows * hq <= 2^26 - 4.
+ */
+size_t gdn_attn_prompt_workspace_bytes(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,
+                                       int32_t max_kv, int32_t hq);
+
+int gdn_attn_prompt(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows, int32_t max_kv,
+                    int32_t max_blocks, int32_t hq, const int32_t *row_start, const int32_t *kv_len,
+                    const int32_t *block_table, const uint16_t *q, const uint16_t *gate,
+                    int64_t gate_row_stride, int64_t gate_head_stride, float scale, uint16_t *out,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Cached rows read back, in any format: packed row row_start[s] + t of k_out and
+ * v_out gets the values of cache row first[s] + t of stream s (a prompt's rows to
+ * be kept outside the pool, or a working copy).  Written again by gdn_attn_prep
+ * without norms and rotation, rows of a bf16 cache come back bit for bit.
+ *   row_start [n+1], first [n] int32;  k_out, v_out [total_rows][hkv][d] bf16
+ * E4M3 values are rounded to bf16 from the fp32 product of code and scale; the
+ * other formats' are exact.  A stream whose rows would end past total_rows or its
+ * block table, or with first[s] < 0, and a row whose page is outside the cache,
+ * are left out: their rows of k_out and v_out stay as they were, and so do rows
+ * of no stream.  total_rows < 2^24.
+ */
+int gdn_kv_read(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows, int32_t max_blocks,
+                const int32_t *row_start, const int32_t *first, const int32_t *block_table, uint16_t *k_out,
+                uint16_t *v_out, void *stream);
 
 /*
  * Commit of the accepted rows in the cache, beside gdn_commit or

@@ -608,7 +608,7 @@ int check_cache_sizes(const gdn_kv_cache *c, gdn::KvArgs &K)
     if (c->n_pages <= 0 || c->hkv <= 0 || c->d <= 0 || c->page_size <= 0)
         return fail(GDN_EINVAL, "cache sizes must be positive (n_pages=%d hkv=%d page_size=%d d=%d)", c->n_pages,
                     c->hkv, c->page_size, c->d);
-    if (c->format != GDN_KV_BF16 && c->format != GDN_KV_E4M3) return fail(GDN_EINVAL, "unknown cache format %d", c->format);
+    if (c->format != GDN_KV_BF16 && c->format != GDN_KV_E4M3 && c->format != GDN_KV_MXFP4) return fail(GDN_EINVAL, "unknown cache format %d", c->format);
     if (c->d != 64 && c->d != 128 && c->d != 256)
         return fail(GDN_EUNSUPPORTED, "d %d: only 64, 128 and 256 are supported", c->d);
     K.page_shift = page_shift(c->page_size);
@@ -635,6 +635,11 @@ int check_cache_pointers(const gdn_kv_cache *c, gdn::KvArgs &K)
         REQUIRE_PTR(v_scale);
         K.k_scale = c->k_scale;
         K.v_scale = c->v_scale;
+    } else if (c->format == GDN_KV_MXFP4) {
+        REQUIRE_PTR(k_scale);
+        REQUIRE_PTR(v_scale);
+        K.k_exp = reinterpret_cast<uint8_t *>(c->k_scale);
+        K.v_exp = reinterpret_cast<uint8_t *>(c->v_scale);
     }
     return GDN_OK;
 }
@@ -843,6 +848,98 @@ int gdn_attn_window(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_
     A.out = out;
     if (!gdn::attn_fits(A)) return fail(GDN_EUNSUPPORTED, "too many streams and chunks for one launch");
     return launched(gdn::launch_attn(A, workspace, static_cast<hipStream_t>(stream)));
+}
+
+size_t gdn_attn_prompt_workspace_bytes(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,
+                                       int32_t max_kv, int32_t hq)
+{
+    gdn::KvArgs K;
+    if (check_cache_sizes(cache, K) != GDN_OK || check_heads(cache, hq, max_kv) != GDN_OK
+        || check_counts(n_streams, total_rows, 1, 1, cache->page_size) != GDN_OK)
+        return 0;
+    return gdn::prompt_workspace_bytes(hq, cache->hkv, cache->d, total_rows, max_kv, true);
+}
+
+int gdn_attn_prompt(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows, int32_t max_kv,
+                    int32_t max_blocks, int32_t hq, const int32_t *row_start, const int32_t *kv_len,
+                    const int32_t *block_table, const uint16_t *q, const uint16_t *gate,
+                    int64_t gate_row_stride, int64_t gate_head_stride, float scale, uint16_t *out,
+                    void *workspace, size_t workspace_bytes, void *stream)
+{
+    gdn::AttnArgs A = {};
+    int rc = check_cache_sizes(cache, A.kv);
+    if (!rc) rc = check_heads(cache, hq, max_kv);
+    if (!rc) rc = check_counts(n_streams, total_rows, 1, max_blocks, cache->page_size);
+    if (!rc && gate) rc = check_strides("gate", gate_row_stride, gate_head_stride, 4);
+    if (rc) return rc;
+    const float scale2 = scale * 1.44269504088896340736f;       // for exponentials to base 2
+    if (!isfinite(scale2)) return fail(GDN_EINVAL, "scale must be finite, also times log2(e)");
+    if (n_streams == 0 || total_rows == 0) {
+        g_err[0] = '\0';
+        return GDN_OK;
+    }
+    rc = check_cache_pointers(cache, A.kv);
+    if (rc) return rc;
+    if (!row_start) return fail(GDN_EINVAL, "row_start is NULL");
+    if (!kv_len) return fail(GDN_EINVAL, "kv_len is NULL");
+    if (!block_table) return fail(GDN_EINVAL, "block_table is NULL");
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(out);
+    if (reinterpret_cast<uintptr_t>(gate) & 7u) return fail(GDN_EINVAL, "gate must be 8-byte aligned");
+    A.n_streams = n_streams;
+    A.total_rows = total_rows;
+    A.max_kv = max_kv;
+    A.max_blocks = max_blocks;
+    A.hq = hq;
+    A.group = hq / cache->hkv;
+    if (!gdn::prompt_fits(A)) return fail(GDN_EUNSUPPORTED, "too many rows, streams or chunks for one launch");
+    const size_t need = gdn::prompt_workspace_bytes(hq, cache->hkv, cache->d, total_rows, max_kv, false);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return fail(GDN_EWORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+        if (!aligned16(workspace)) return fail(GDN_EINVAL, "workspace must be 16-byte aligned");
+    }
+    A.row_start = row_start;
+    A.kv_len = kv_len;
+    A.table = block_table;
+    A.q = q;
+    A.gate = gate;
+    A.gate_row = gate_row_stride;
+    A.gate_head = gate_head_stride;
+    A.scale = scale2;
+    A.out = out;
+    return launched(gdn::launch_prompt(A, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int gdn_kv_read(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows, int32_t max_blocks,
+                const int32_t *row_start, const int32_t *first, const int32_t *block_table, uint16_t *k_out,
+                uint16_t *v_out, void *stream)
+{
+    gdn::ReadArgs A = {};
+    int rc = check_cache_sizes(cache, A.kv);
+    if (!rc) rc = check_counts(n_streams, total_rows, 1, max_blocks, cache->page_size);
+    if (rc) return rc;
+    if (total_rows > gdn::kMaxGroups) return fail(GDN_EUNSUPPORTED, "total_rows %d: at most %d", total_rows, gdn::kMaxGroups);
+    if (n_streams == 0 || total_rows == 0) {
+        g_err[0] = '\0';
+        return GDN_OK;
+    }
+    rc = check_cache_pointers(cache, A.kv);
+    if (rc) return rc;
+    if (!row_start) return fail(GDN_EINVAL, "row_start is NULL");
+    if (!first) return fail(GDN_EINVAL, "first is NULL");
+    if (!block_table) return fail(GDN_EINVAL, "block_table is NULL");
+    REQUIRE_PTR(k_out);
+    REQUIRE_PTR(v_out);
+    A.n_streams = n_streams;
+    A.total_rows = total_rows;
+    A.max_blocks = max_blocks;
+    A.row_start = row_start;
+    A.first = first;
+    A.table = block_table;
+    A.k_out = k_out;
+    A.v_out = v_out;
+    return launched(gdn::launch_read(A, static_cast<hipStream_t>(stream)));
 }
 
 int gdn_attn_commit(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,

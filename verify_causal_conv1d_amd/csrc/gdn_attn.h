@@ -8,13 +8,17 @@
 
 namespace gdn {
 
-// A paged cache: K and V of [pages][hkv][page_size][d], bf16 or e4m3 with one
-// fp32 scale a row in [pages][hkv][page_size].
+// A paged cache: K and V of [pages][hkv][page_size][d], bf16, e4m3 with one fp32
+// scale a row in [pages][hkv][page_size], or e2m1 (two codes a byte) with an
+// exponent byte for every 32 channels in [pages][hkv][page_size][d / 32].
 struct KvArgs {
     uint8_t *k, *v;
-    float *k_scale, *v_scale;   // NULL: bf16
+    float *k_scale, *v_scale;   // e4m3 only
     int32_t n_pages, page_shift, hkv, d;
+    uint8_t *k_exp, *v_exp;     // e2m1 only
 };
+enum { FMT_BF16 = 0, FMT_E4M3 = 1, FMT_MXFP4 = 2 };
+inline int format_of(const KvArgs &K) { return K.k_exp ? FMT_MXFP4 : K.k_scale ? FMT_E4M3 : FMT_BF16; }
 
 struct TablesArgs {
     int32_t n_streams, total_rows, page_shift, max_blocks, n_pages;
@@ -54,6 +58,13 @@ struct AttnCommitArgs {
     int32_t *kv_len_out;
 };
 
+struct ReadArgs {
+    KvArgs kv;
+    int32_t n_streams, total_rows, max_blocks;
+    const int32_t *row_start, *first, *table;
+    uint16_t *k_out, *v_out;     // [total_rows][hkv][d]
+};
+
 constexpr int kMaxAttnKeys = 1 << 21;    // of one stream: a workgroup lists its chunk's pages in LDS
 constexpr int kMaxGroups = (1 << 24) - 1;  // workgroups of 256 threads: a launch has less than 2^32 threads
 constexpr int kMaxTableStreams = 4096;   // a workgroup keeps six ints of each in LDS
@@ -66,6 +77,17 @@ bool attn_fits(const AttnArgs &A);   // the launch's workgroups can be numbered
 hipError_t launch_tables(const TablesArgs &A, hipStream_t stream);
 hipError_t launch_prep(const PrepArgs &A, hipStream_t stream);
 hipError_t launch_attn(AttnArgs A, void *workspace, hipStream_t stream);
+
+// Attention of whole prompts: max_rows is not looked at.  The workspace of a call
+// with just these bounds, or (or_less) of any with no larger ones.
+size_t prompt_workspace_bytes(int hq, int hkv, int d, int total_rows, int max_kv, bool or_less);
+bool prompt_fits(const AttnArgs &A);
+hipError_t launch_prompt(AttnArgs A, void *workspace, hipStream_t stream);
+// Windows of more than 16 columns over a 4-bit cache, in the chunks of the others
+hipError_t launch_wide4(const AttnArgs &A, long long pieces, hipStream_t stream);
+// Merges the chunks of every (row, head); split_keys 0: chunks of windows
+hipError_t launch_join(const AttnArgs &A, bool wide, int split_keys, hipStream_t stream);
+hipError_t launch_read(const ReadArgs &A, hipStream_t stream);
 hipError_t launch_attn_commit(const AttnCommitArgs &A, hipStream_t stream);
 
 }  // namespace gdn

@@ -27,114 +27,12 @@
 // columns the wide kernel takes 53 us and the other one, reading K and V once a
 // tile, 69; with 48 columns 59 and 97.  One stream of 500 keys and 18 columns:
 // 15.7 and 14.4.)
-#include "gdn_attn.h"
-#include "gdn_device.h"
-#include "gdn_internal.h"
+#include "gdn_attn_core.h"
+#include "gdn_mxfp4.h"
 #include "gdn_once.h"
 
 namespace gdn {
 namespace {
-
-constexpr int kTile = 32;                  // keys of a wave's step
-constexpr int kCols = 16;                  // (row, head) pairs of a column tile
-constexpr int kMaxChunks = 64;             // of one stream
-
-__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-// a / b for 0 <= a < 2^22 and 0 < b: on the device by a reciprocal, whose
-// quotient is off by one at most, and a correction (the integer sequence is four
-// times as long, and a short call is little else).
-__host__ __device__ inline int small_div(int a, int b)
-{
-#ifdef __HIP_DEVICE_COMPILE__
-    const int q = (int)((float)a * __builtin_amdgcn_rcpf((float)b)), r = a - q * b;
-    return q + (r >= b) - (r < 0);
-#else
-    return a / b;
-#endif
-}
-__host__ __device__ inline int small_ceil_div(int a, int b) { return small_div(a + b - 1, b); }
-__host__ __device__ inline int at_least(int a, int b) { return a > b ? a : b; }
-__host__ __device__ inline int at_most(int a, int b) { return a < b ? a : b; }
-
-// The most keys that a chunk of a stream with len keys is to have: at least
-// kChunkLeast; more once there are 4 of them, up to chunk_usual; more again once
-// there are 32, up to chunk_long; and more than that once there are kMaxChunks.
-// Short chunks spread a lone stream over the chip, long ones write fewer parts
-// and begin less often: 64 steps of 2,000 to 4,096 keys take 164 us in chunks of
-// 256 and 186 in chunks of 128, one step of 500 keys 15.5 and 13.4; 16 steps of
-// up to 16,384 keys 82 us in chunks of 256 and 77 of 512; a tree of 8 rows over
-// 500 keys 27 us in one wide chunk and 17 in chunks of 128.
-constexpr int kChunkLeast = 128;
-__host__ __device__ inline int chunk_usual(bool wide) { return wide ? 512 : 256; }
-__host__ __device__ inline int chunk_long(bool wide) { return wide ? 1024 : 512; }
-
-__host__ __device__ inline int chunk_most(int len, bool wide)
-{
-    const int a = at_least(kChunkLeast, at_most(chunk_usual(wide), ceil_div(len, 4)));
-    const int b = at_least(a, at_most(chunk_long(wide), ceil_div(len, 32)));
-    return at_least(b, ceil_div(len, kMaxChunks));
-}
-
-// Its keys: equal chunks, in whole units.  Up to a sixteenth more than the most is
-// allowed, so that a few rows past a round number do not make another chunk; but
-// in whole units, too, which is nothing before the most is sixteen units (wide:
-// from 32,737 keys, else from 131,009).  Below that they do make one: 8,200 keys
-// are 16 wide chunks of 512 and one of 8.
-__host__ __device__ inline int chunk_unit(bool wide) { return wide ? 64 : 128; }
-__host__ __device__ inline int chunk_keys(int len, bool wide)
-{
-    const int most = chunk_most(len, wide), unit = chunk_unit(wide);
-    return unit * ceil_div(small_ceil_div(len, small_ceil_div(len, most + most / 16 / unit * unit)), unit);
-}
-
-__host__ __device__ inline int chunk_count(int len, bool wide) { return len <= 0 ? 0 : small_ceil_div(len, chunk_keys(len, wide)); }
-
-// The most chunks that a stream of up to max_kv keys can have.
-inline int chunk_bound(int max_kv, bool wide)
-{
-    const int n = at_least(at_most(4, ceil_div(max_kv, kChunkLeast)), at_most(32, ceil_div(max_kv, chunk_usual(wide))));
-    return at_most(kMaxChunks, at_least(n, ceil_div(max_kv, chunk_long(wide))));
-}
-
-inline bool is_wide(int max_rows, int group) { return max_rows * group > kCols; }
-
-// A stream's window by the layout rules that need no parents: false skips it.
-__device__ __forceinline__ bool stream_window(const AttnArgs &A, int s, int &r0, int &m, int &kv)
-{
-    r0 = A.row_start[s];
-    const int r1 = A.row_start[s + 1];
-    kv = A.kv_len[s];
-    m = r1 - r0;
-    return r0 >= 0 && r1 > r0 && r1 <= A.total_rows && m <= A.max_rows && kv >= 0 && kv <= A.max_kv - m
-           && (long long)kv + m <= (long long)A.max_blocks << A.kv.page_shift;
-}
-
-// Bits of the window's rows that row t sees (itself and its ancestors);
-// ok = false if a parent breaks the rules.  Lane u < m holds row u.
-__device__ __forceinline__ uint32_t seen_rows(const AttnArgs &A, int r0, int m, int t, bool &ok)
-{
-    if (!A.parent) return (2u << t) - 1;
-    const int lane = threadIdx.x & 63;
-    const int up = lane < m ? A.parent[r0 + lane] : -1;
-    ok = ok && !__ballot(lane < m && (up < -1 || up >= lane));
-    uint32_t bits = 1u << t;
-    if (ok)
-        for (int u = m - 1; u >= 0; --u) {     // parents come before their rows
-            const int p = __builtin_amdgcn_readlane(up, u);
-            if (p >= 0 && (bits >> u & 1)) bits |= 1u << p;
-        }
-    return bits;
-}
-
-// The thread's number, as a value that the compiler cannot trace: what is worked
-// out from it inside a loop stays there, instead of taking registers from the
-// accumulators all through it.
-__device__ __forceinline__ int fresh(int x)
-{
-    asm volatile("" : "+v"(x));
-    return x;
-}
 
 // ---- operands in registers ---------------------------------------------------
 
@@ -170,6 +68,50 @@ struct Run16<true> {
     }
 };
 
+// A lane's share of a key row, in the order in which the steps of the product
+// take it: step s has 8 channels from channel(s, g) on.
+template <int D, int FMT>
+struct KeyRun {
+    static constexpr int STEPS = D / 32;
+    Run16<FMT == FMT_E4M3> r[D / 64];
+    static __device__ __forceinline__ int channel(int s, int g) { return 64 * (s / 2) + 16 * g + 8 * (s & 1); }
+    // from the 16 rows that begin with cache row `row`, its nth
+    __device__ __forceinline__ void load_from_cache(const KvArgs &kv, size_t row, int n, int g)
+    {
+        constexpr int ESZ = FMT == FMT_E4M3 ? 1 : 2;
+        const uint8_t *p = kv.k + row * (D * ESZ);
+        const uint32_t off = n * (D * ESZ) + 16 * g * ESZ;
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) r[k].load_from_cache(p + (off + 64 * k * ESZ));
+    }
+    __device__ __forceinline__ bf8v get(int s) const { return r[s / 2].get(s & 1); }
+};
+// 4 bits: a block of 32 channels a load (d = 64: half a block)
+template <int D>
+struct KeyRun<D, FMT_MXFP4> {
+    static constexpr int STEPS = D / 32, LOADS = D / 128 > 0 ? D / 128 : 1, W = D == 64 ? 2 : 4, ROW = D / 2, EXPS = D / 32;
+    typedef uint32_t vec_t __attribute__((ext_vector_type(W)));
+    vec_t w[LOADS];
+    uint2 e;
+    int shift;
+    static __device__ __forceinline__ int channel(int s, int g) { return D == 64 ? 16 * g + 8 * s : 128 * (s / 4) + 32 * g + 8 * (s & 3); }
+    __device__ __forceinline__ void load_from_cache(const KvArgs &kv, size_t row, int n, int g)
+    {
+        const uint8_t *p = kv.k + row * ROW, *x = kv.k_exp + row * EXPS;
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) w[j] = __builtin_nontemporal_load(reinterpret_cast<const vec_t *>(p + (n * ROW + 64 * j + 4 * W * g)));
+        if constexpr (EXPS == 8) e = *reinterpret_cast<const uint2 *>(x + n * 8);
+        else if constexpr (EXPS == 4) e.x = *reinterpret_cast<const uint32_t *>(x + n * 4);
+        else e.x = *reinterpret_cast<const uint16_t *>(x + n * 2);
+        shift = D == 64 ? 8 * (g >> 1) : 8 * g;
+    }
+    __device__ __forceinline__ bf8v get(int s) const
+    {
+        const float f = mx_scale((s < 4 ? e.x : e.y) >> shift & 255);
+        return __builtin_bit_cast(bf8v, mx_values8(w[s / 4][s & 3], f));
+    }
+};
+
 // A lane's share of one value row: NL loads of W dwords each.  Column i of
 // load h is channel h * 16 * EPL + (lane % 16) * EPL + i.
 template <int D, bool F8>
@@ -179,6 +121,12 @@ struct VLayout {
     static constexpr int W = BYTES / NL / 64;           // dwords of a load: 1, 2 or 4
     static constexpr int EPL = W * (F8 ? 4 : 2);
     static constexpr int NT = NL * EPL;                 // tiles of 16 channels of O^T
+};
+
+// 4 bits: one load, of at most two dwords
+template <int D>
+struct VLayout4 {
+    static constexpr int NL = 1, W = 1, EPL = D / 16, NT = D / 16;
 };
 
 template <bool F8, int W>
@@ -232,6 +180,37 @@ struct VPart {
     }
 };
 
+// 4 bits: a lane's D / 16 channels of a row lie in one block
+template <int D>
+struct VPart4 {
+    static constexpr int W = D == 256 ? 2 : 1;
+    uint32_t w[W], e;
+    __device__ __forceinline__ void load_from_cache(const KvArgs &kv, size_t row, int n)
+    {
+        const uint8_t *p = kv.v + row * (D / 2) + n * (D / 32);
+        if constexpr (D == 256) {
+            const auto x = __builtin_nontemporal_load(reinterpret_cast<const uint64_t *>(p));
+            w[0] = (uint32_t)x, w[1] = (uint32_t)(x >> 32);
+        } else if constexpr (D == 128) {
+            w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t *>(p));
+        } else {
+            w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t *>(p));
+        }
+        e = kv.v_exp[row * (D / 32) + n * (D / 32) / 16];
+    }
+    __device__ __forceinline__ bool finite() const { return e <= kMxMost; }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+        e = 127;
+    }
+    __device__ __forceinline__ void drop_bad()
+    {
+        if (!finite()) zero();
+    }
+};
+
 // The MFMA operand of column i of a load: that channel of the lane's 8 keys.
 template <bool F8, int W>
 __device__ __forceinline__ bf8v v_operand(const VPart<F8, W> (&v)[8], int i)
@@ -252,46 +231,19 @@ __device__ __forceinline__ bf8v v_operand(const VPart<F8, W> (&v)[8], int i)
 
 __device__ __forceinline__ f4v mfma(bf8v a, bf8v b, f4v c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 
-__device__ __forceinline__ float max_rows4(float x)     // over lanes l, l ^ 16, l ^ 32, l ^ 48
-{
-    const uint32_t xi = __float_as_uint(x);
-    const auto p = __builtin_amdgcn_permlane16_swap(xi, xi, false, false);
-    const float s = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
-    const uint32_t si = __float_as_uint(s);
-    const auto q = __builtin_amdgcn_permlane32_swap(si, si, false, false);
-    return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
-}
-
-// the gates of 4 channels (none: all ones, which finish4 does not look at)
-__device__ __forceinline__ uint2 gates4(const AttnArgs &A, int r, int head, int d)
-{
-    return A.gate ? *reinterpret_cast<const uint2 *>(A.gate + r * A.gate_row + head * A.gate_head + d) : make_uint2(0, 0);
-}
-
-// the result of one (row, head) column's 4 channels: o / l, gated, in bf16
-__device__ __forceinline__ uint2 finish4(const AttnArgs &A, float4 o, float inv, uint2 g)
-{
-    float x[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-    if (A.gate) {
-        x[0] *= sigmoid_f(__uint_as_float(g.x << 16));
-        x[1] *= sigmoid_f(__uint_as_float(g.x & 0xffff0000u));
-        x[2] *= sigmoid_f(__uint_as_float(g.y << 16));
-        x[3] *= sigmoid_f(__uint_as_float(g.y & 0xffff0000u));
-    }
-    return make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
-}
-
 // Adds the infinite and NaN values that the products of a chunk's keys [k0, k1)
 // left out to a column's channels d .. d + 3: those of the rows that it sees (of
 // the window, bits of seen) in the tiles that hold rows of the window.
-template <int D, bool F8>
+template <int D, int FMT>
 __device__ void add_bad(const AttnArgs &A, float4 &a, const int *rows16, uint32_t seen, int kv, int k0, int k1, int d)
 {
     for (int key = max(k0, kv & -kTile); key < k1; ++key) {
         if (key >= kv && !(seen >> (key - kv) & 1)) continue;
         const size_t row = (size_t)rows16[(key - k0) >> 4] + (key & 15);
         float v[4];
-        if constexpr (F8) {
+        if constexpr (FMT == FMT_MXFP4) {
+            v[0] = v[1] = v[2] = v[3] = A.kv.v_exp[row * (D / kMxBlock) + d / kMxBlock] > kMxMost ? NAN : 0.0f;
+        } else if constexpr (FMT == FMT_E4M3) {
             const uint32_t x = *reinterpret_cast<const uint32_t *>(A.kv.v + row * D + d);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = (x >> (8 * i) & 0x7fu) == 0x7fu ? NAN : 0.0f;
@@ -305,10 +257,6 @@ __device__ void add_bad(const AttnArgs &A, float4 &a, const int *rows16, uint32_
         a.x += v[0], a.y += v[1], a.z += v[2], a.w += v[3];
     }
 }
-
-// What a stream's skipped chunk leaves in the workspace for join_kernel: sums
-// are never negative.
-constexpr float kSkipped = -1.0f;
 
 // The running state of a wave's column tile.  Lane (n, g) = (lane % 16, lane /
 // 16) holds column n: of S^T the keys 16 u + 4 g + i of a tile of 32 (u < 2, i <
@@ -447,13 +395,37 @@ __device__ __forceinline__ void add_values(Column<D, F8> &C, int h, const VPart<
     }
 }
 
+// A byte's two channels are converted together, with their row's scale, and then
+// set beside the next row's.
+template <int D>
+__device__ __forceinline__ void add_values(Column<D, false> &C, int, const VPart4<D> (&v)[8], bf8v pb, bf8v rest)
+{
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = mx_scale(v[j].e);
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) {
+        uint32_t x[8], lo[4], hi[4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = mx_pair(v[j].w[b / 4], f[j], b & 3);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            lo[q] = __builtin_amdgcn_perm(x[2 * q + 1], x[2 * q], 0x05040100u);
+            hi[q] = __builtin_amdgcn_perm(x[2 * q + 1], x[2 * q], 0x07060302u);
+        }
+        const bf8v a = __builtin_bit_cast(bf8v, make_uint4(lo[0], lo[1], lo[2], lo[3])), c = __builtin_bit_cast(bf8v, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        C.o[2 * b] = mfma(a, rest, mfma(a, pb, C.o[2 * b]));
+        C.o[2 * b + 1] = mfma(c, rest, mfma(c, pb, C.o[2 * b + 1]));
+    }
+}
+
 // Values of a tile that holds keys of the window or past the end.  Rows past
 // the end hold anything: zeros instead.  And 0 * inf is NaN: an infinite or NaN
 // value of a window row must not reach the rows that do not see it, so such
 // values are left out of the product (true is returned), to be added at the
 // end to the results that they belong to (add_bad).
-template <bool F8, int W>
-__device__ __forceinline__ bool clean_values(VPart<F8, W> (&v)[8], int key0, int len, int m)
+template <class VP>
+__device__ __forceinline__ bool clean_values(VP (&v)[8], int key0, int len, int m)
 {
     bool fin = true;
 #pragma unroll
@@ -467,131 +439,6 @@ __device__ __forceinline__ bool clean_values(VPart<F8, W> (&v)[8], int key0, int
     return true;
 }
 
-// Sum over the lanes up to and including this one: row_shr within the 16-lane
-// rows, then row_bcast of a row's last lane to the rows after it.
-__device__ __forceinline__ int wave_running_sum(int x)
-{
-    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
-    return x;
-}
-
-// One piece of work: a chunk of a stream's keys, for one kv head and one tile of
-// columns.
-struct Chunk {
-    int h, rt, c;             // kv head, tile of columns, chunk
-    int s, r0, m, kv, len;    // the stream, its window, cached rows, keys in all
-    int k0, k1, nch;          // the chunk's keys, and chunks of the stream
-    int size;                 // keys of a full chunk
-    int cols;                 // (row, head) pairs of the stream
-};
-
-// The pieces of all streams, in stream order.  How many there are follows from
-// the lengths, which only the device knows.  Every wave finds its pieces by
-// itself: lane l holds stream first + l of a block of 64 streams, and the pieces
-// of the block up to and including that stream's.  Within a block no workgroup
-// for a piece that is not there comes before those that are.  attn_kernel's grid
-// has room for max_kv keys of every stream, a row of workgroups a block, and those
-// that find nothing end at once, but are not free: 512 steps of 500 keys take 264
-// us under a max_kv of 501 and 423 under 262,144, 16 such steps 15.7 and 18.1.
-struct Pieces {
-    int first = -64, before = 0, incl = 0;    // of the block: first stream, pieces before it, running sum
-    int r0 = 0, m = 0, kv = 0;
-
-    __device__ __forceinline__ void load(const AttnArgs &A, bool wide, int tile_cols, int block)
-    {
-        const int lane = threadIdx.x & 63, s = block + lane;
-        first = block;
-        int count = 0;
-        if (s < A.n_streams && stream_window(A, s, r0, m, kv))
-            count = chunk_count(kv + m, wide) * A.kv.hkv * ceil_div(m * A.group, tile_cols);
-        incl = wave_running_sum(count);
-    }
-
-    // piece `at` of the block's
-    __device__ __forceinline__ void get(const AttnArgs &A, bool wide, int at, Chunk &K) const
-    {
-        const int l = __builtin_ctzll(__ballot(incl > at));
-        const int x = at - (l ? __builtin_amdgcn_readlane(incl, l - 1) : 0);
-        K.s = first + l;
-        K.r0 = __builtin_amdgcn_readlane(r0, l);
-        K.m = __builtin_amdgcn_readlane(m, l);
-        K.kv = __builtin_amdgcn_readlane(kv, l);
-        K.len = K.kv + K.m;
-        K.size = chunk_keys(K.len, wide);
-        K.nch = small_ceil_div(K.len, K.size);
-        K.cols = K.m * A.group;
-        // the stream's pieces: chunks innermost (at most 64 * 1024 * 128 of them)
-        const int y = x < 1 << 22 ? small_div(x, K.nch) : x / K.nch;
-        K.c = x - y * K.nch;
-        K.rt = small_div(y, A.kv.hkv);
-        K.h = y - K.rt * A.kv.hkv;
-        K.k0 = K.c * K.size;
-        K.k1 = min(K.k0 + K.size, K.len);
-    }
-
-    // piece `at` of the block of 64 streams from `block`; false if it has fewer
-    __device__ __forceinline__ bool find_in_block(const AttnArgs &A, bool wide, int tile_cols, int block, int at, Chunk &K)
-    {
-        load(A, wide, tile_cols, block);
-        if (at >= __builtin_amdgcn_readlane(incl, 63)) return false;
-        get(A, wide, at, K);
-        return true;
-    }
-
-    // piece `item` of all (not less than in the call before); false if there is none
-    __device__ __forceinline__ bool find(const AttnArgs &A, bool wide, int tile_cols, int item, Chunk &K)
-    {
-        while (item >= before + __builtin_amdgcn_readlane(incl, 63)) {
-            before += __builtin_amdgcn_readlane(incl, 63);
-            if (first + 64 >= A.n_streams) return false;
-            load(A, wide, tile_cols, first + 64);
-        }
-        get(A, wide, item - before, K);
-        return true;
-    }
-};
-
-// Cache rows of the chunk's keys, 16 at a time (pages hold multiples of 16) up
-// to the chunk's full size: past the stream's end those of its last keys, so
-// that every load stays in its pages.  false if a page is not in the cache.
-// (For the caller's wave: whether its share of them is.)
-__device__ __forceinline__ bool chunk_rows(const AttnArgs &A, const Chunk &K, int *rows16, int threads)
-{
-    bool ok = true;
-    for (int i = threadIdx.x; i < K.size / 16; i += threads) {
-        const int key = min(K.k0 + 16 * i, (K.len - 1) & ~15);
-        const int id = A.table[(size_t)K.s * A.max_blocks + (key >> A.kv.page_shift)];
-        const bool good = id >= 0 && id < A.kv.n_pages;
-        ok = ok && good;
-        rows16[i] = good ? ((id * A.kv.hkv + K.h) << A.kv.page_shift) + (key & ((1 << A.kv.page_shift) - 1)) : 0;
-    }
-    return !__ballot(!ok);
-}
-
-// Packed row and query head of a stream's column.
-__device__ __forceinline__ int col_row(const AttnArgs &A, const Chunk &K, int col) { return K.r0 + small_div(col, A.group); }
-__device__ __forceinline__ int col_head(const AttnArgs &A, const Chunk &K, int col) { return K.h * A.group + col - small_div(col, A.group) * A.group; }
-// and its place in the workspace
-__device__ __forceinline__ size_t col_part(const AttnArgs &A, const Chunk &K, int col)
-{
-    return ((size_t)col_row(A, K, col) * A.hq + col_head(A, K, col)) * A.chunks + K.c;
-}
-
-// A column's 4 channels from d: the result where the chunk is the stream's only
-// one, else its part in the workspace.
-template <int D>
-__device__ __forceinline__ void put4(const AttnArgs &A, const Chunk &K, int col, float4 a, float l, int d)
-{
-    const int r = col_row(A, K, col), hd = col_head(A, K, col);
-    if (K.nch == 1) *reinterpret_cast<uint2 *>(A.out + ((size_t)r * A.hq + hd) * D + d) = finish4(A, a, 1.0f / l, gates4(A, r, hd, d));
-    else *reinterpret_cast<float4 *>(A.part + col_part(A, K, col) * D + d) = a;
-}
-
 // ---- up to 16 columns -----------------------------------------------------------
 
 constexpr int kAttnThreads = 256, kAttnWaves = 4;
@@ -603,11 +450,13 @@ constexpr int kAttnThreads = 256, kAttnWaves = 4;
 // of 1,000 to 16,384 keys (374 MB) take 76 us with the join, 4.9 TB/s; one of
 // 262,143 keys in e4m3 (545 MB) 105 us, 5.2 TB/s.  A short stream is bounded by
 // the chain of layout, page numbers, first tile and join: 8 us for 100 keys.
-template <int D, bool F8>
+template <int D, int FMT>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
 {
+    constexpr bool F8 = FMT == FMT_E4M3, MX = FMT == FMT_MXFP4;
     constexpr int ESZ = F8 ? 1 : 2, ROW = D * ESZ, KS = D / 64;
-    using V = VLayout<D, F8>;
+    using KR = KeyRun<D, FMT>;
+    using V = typename std::conditional<MX, VLayout4<D>, VLayout<D, F8>>::type;
     constexpr int OP = D + 4;                      // padded LDS row of a column's channels
     extern __shared__ __align__(16) uint8_t smem[];
     float *o_lds = reinterpret_cast<float *>(smem);                    // [waves][kCols][OP]
@@ -625,14 +474,14 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
     const int col0 = K.rt * kCols, ncol = min(K.cols - col0, kCols);
     bool ok = chunk_rows(A, K, rows16, kAttnThreads);
     const uint32_t seen = seen_rows(A, K.r0, K.m, min(small_div(col0 + n, A.group), K.m - 1), ok);
-    // the queries, in the order of the lanes' operands: [k-step][half][lane] of
-    // 16 bytes (column n, channels 64 k + 16 g + 8 half; zero past the last column)
+    // the queries, in the order of the lanes' operands: [step][lane] of 16 bytes
+    // (column n, 8 channels from KeyRun's on; zero past the last column)
     for (int i = tid; i < KS * 2 * 64; i += kAttnThreads) {
-        const int qc = i & 15, qg = i >> 4 & 3, hh = i >> 6 & 1, k = i >> 7;
+        const int qc = i & 15, qg = i >> 4 & 3, step = i >> 6;
         uint4 x = {0, 0, 0, 0};
         if (qc < ncol)
             x = *reinterpret_cast<const uint4 *>(A.q + ((size_t)col_row(A, K, col0 + qc) * A.hq + col_head(A, K, col0 + qc)) * D
-                                                 + 64 * k + 16 * qg + 8 * hh);
+                                                 + KR::channel(step, qg));
         q_lds[i] = x;
     }
     static_assert(kAttnWaves == 4, "");
@@ -647,25 +496,24 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
 
     Column<D, F8> C;
     C.clear();
-    Run16<F8> kk[2][KS];
-    VPart<F8, V::W> vv[V::NL][8];
-    const uint32_t k_off = n * ROW + 16 * g * ESZ, v_off = 4 * g * ROW + n * V::W * 4;
+    KR kk[2];
+    typename std::conditional<MX, VPart4<D>, VPart<F8, V::W>>::type vv[V::NL][8];
+    const uint32_t v_off = 4 * g * ROW + n * V::W * 4;
     auto load_k = [&](int tile) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint8_t *p = A.kv.k + (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]) * ROW;
-#pragma unroll
-            for (int k = 0; k < KS; ++k) kk[u][k].load_from_cache(p + (k_off + 64 * k * ESZ));
-        }
+        for (int u = 0; u < 2; ++u) kk[u].load_from_cache(A.kv, (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]), n, g);
     };
     auto load_v = [&](int tile) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const uint8_t *p = A.kv.v + (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]) * ROW;
+            const size_t row = (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]);
+            const uint8_t *p = A.kv.v + row * ROW;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int hh = 0; hh < V::NL; ++hh) vv[hh][4 * u + j].load_from_cache(p + (v_off + j * ROW + hh * 16 * V::W * 4));
+                for (int hh = 0; hh < V::NL; ++hh)
+                    if constexpr (MX) vv[hh][4 * u + j].load_from_cache(A.kv, row + 4 * g + j, n);
+                    else vv[hh][4 * u + j].load_from_cache(p + (v_off + j * ROW + hh * 16 * V::W * 4));
         }
     };
     const int tiles = ceil_div(K.k1 - K.k0, kTile);
@@ -678,13 +526,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
         const int key0 = K.k0 + tile * kTile + 4 * g;
         f4v acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const bf8v q = __builtin_bit_cast(bf8v, q_lds[(2 * k + hh) * 64 + lane]);
-                acc[0] = mfma(kk[0][k].get(hh), q, acc[0]);
-                acc[1] = mfma(kk[1][k].get(hh), q, acc[1]);
-            }
+        for (int s = 0; s < KR::STEPS; ++s) {
+            const bf8v q = __builtin_bit_cast(bf8v, q_lds[s * 64 + lane]);
+            acc[0] = mfma(kk[0].get(s), q, acc[0]);
+            acc[1] = mfma(kk[1].get(s), q, acc[1]);
+        }
         if (more) load_k(tile + kAttnWaves);
         float4 ks[2] = {}, vs[2] = {};
         if constexpr (F8)
@@ -746,28 +592,13 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
             l += l_lds[w * kCols + cc];
             mm = fmaxf(mm, m_lds[w * kCols + cc]);
         }
-        if (*bad_lds) add_bad<D, F8>(A, a, rows16, seen_lds[cc], K.kv, K.k0, K.k1, d);
+        if (*bad_lds) add_bad<D, FMT>(A, a, rows16, seen_lds[cc], K.kv, K.k0, K.k1, d);
         put4<D>(A, K, col0 + cc, a, l, d);
         if (K.nch > 1 && d == 0) A.stat[col_part(A, K, col0 + cc)] = make_float2(mm, l);
     }
 }
 
 // ---- more columns ----------------------------------------------------------------
-
-typedef const __attribute__((address_space(1))) void global_void;
-typedef __attribute__((address_space(3))) void lds_void;
-constexpr int kOnce = 2;        // the nontemporal bit of a load's cache policy
-
-// Waits until all but the newest N vector memory operations of the wave and all
-// of its LDS reads are done, then for the workgroup's other waves.
-template <int N>
-__device__ __forceinline__ void wait_and_meet()
-{
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | (N >> 4) << 14);     // vmcnt(N) lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
 
 // Four stages of keys and values in LDS, filled by direct loads (16 bytes a
 // lane, 1 KB an instruction): while a stage is multiplied the next three are
@@ -804,25 +635,6 @@ struct Stage {
         return 2 * (ROW >= 256 ? key & 7 : key >> 1 & 3);
     }
 };
-
-typedef short s4v __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s4v lds_s4v;
-
-// Transposing LDS read: each group of 16 lanes brings four 16-element rows, lane
-// 4 r + c elements 4 c .. 4 c + 3 of row r; lane i gets element i of the four.
-__device__ __forceinline__ s4v read_transposed(const uint8_t *p)
-{
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(s4v *)p);
-}
-
-// The same of bytes: eight 16-byte rows, lane 2 r + c bytes 8 c .. 8 c + 7 of row
-// r; lane i gets byte i of the eight.
-typedef int v2i __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(3))) v2i lds_v2i;
-__device__ __forceinline__ v2i read_transposed_codes(const uint8_t *p)
-{
-    return __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)(v2i *)p);
-}
 
 // clean_values of one operand in e4m3 codes (byte j: key key0 + 16 (j / 4) + j %
 // 4) or in bf16 (element j likewise);
@@ -1105,7 +917,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
             if (K.nch > 1 && eg == 0) A.stat[col_part(A, K, col)] = ok ? make_float2(C[c].mx, l) : make_float2(0.0f, kSkipped);
             if (!ok) continue;
             auto put = [&](float4 a, int d) {
-                if (bad) add_bad<D, F8>(A, a, rows16 + list, seen[c], K.kv, K.k0, K.k1, d);
+                if (bad) add_bad<D, F8 ? FMT_E4M3 : FMT_BF16>(A, a, rows16 + list, seen[c], K.kv, K.k0, K.k1, d);
                 put4<D>(A, K, col, a, l, d);
             };
 #pragma unroll
@@ -1135,8 +947,8 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
 // kernel's 11 us are the time of those bytes.
 constexpr int kJoinWaves = 4, kJoinBatch = 16;      // loads in flight
 
-template <int D>
-__global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const AttnArgs A, const int is_wide)
+template <int D, bool PROMPT>
+__global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const AttnArgs A, const int is_wide, const int split_keys)
 {
     constexpr int VEC = D / 64;
     typedef float part_t __attribute__((ext_vector_type(VEC)));
@@ -1183,8 +995,15 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const AttnArgs A,
     }
     if (!found) return;
     const int l = __builtin_ctzll(found);
-    const int nch = chunk_count(__builtin_amdgcn_readlane(kv, l) + __builtin_amdgcn_readlane(m, l), is_wide);
-    if (nch <= 1) return;
+    const int len = __builtin_amdgcn_readlane(kv, l) + __builtin_amdgcn_readlane(m, l);
+    int nch;
+    if constexpr (PROMPT) {         // of the stream; then those that the row sees
+        if (len <= split_keys) return;
+        nch = (__builtin_amdgcn_readlane(kv, l) + r - __builtin_amdgcn_readlane(r0, l)) / split_keys + 1;
+    } else {
+        nch = chunk_count(len, is_wide);
+        if (nch <= 1) return;
+    }
     if (lane >= nch) st = {-INFINITY, 0.0f};
     if (__ballot(st.y < 0.0f)) return;                      // a chunk was skipped: so is the stream
     float top = st.x;
@@ -1223,7 +1042,7 @@ int longest_chunk(int max_kv, bool wide)
 
 constexpr int kCUs = 256;
 
-template <int D, bool F8>
+template <int D, int FMT>
 hipError_t launch_d(const AttnArgs &A, bool wide, long long pieces, hipStream_t stream)
 {
     const int list = longest_chunk(A.max_kv, wide) / 16;
@@ -1232,14 +1051,26 @@ hipError_t launch_d(const AttnArgs &A, bool wide, long long pieces, hipStream_t 
         constexpr size_t lds = sizeof(float) * kAttnWaves * kCols * (D + 4 + 2) + D * 2 * kCols + sizeof(int) * (4 + kCols);
         // 64 streams a grid row
         const unsigned per_row = (unsigned)(pieces / A.n_streams * (A.n_streams < 64 ? A.n_streams : 64));
-        hipLaunchKernelGGL((attn_kernel<D, F8>), dim3(per_row, ceil_div(A.n_streams, 64)), dim3(kAttnThreads), lds + list_bytes, stream, A);
+        hipLaunchKernelGGL((attn_kernel<D, FMT>), dim3(per_row, ceil_div(A.n_streams, 64)), dim3(kAttnThreads), lds + list_bytes, stream, A);
+    } else if constexpr (FMT == FMT_MXFP4) {
+        const hipError_t rc = launch_wide4(A, pieces, stream);
+        if (rc != hipSuccess) return rc;
     } else {
         const unsigned blocks = (unsigned)(pieces < kCUs ? pieces : kCUs);
-        hipLaunchKernelGGL((attn_wide_kernel<D, F8>), dim3(blocks), dim3(kWideThreads), 2 * list_bytes, stream, A, list);
+        hipLaunchKernelGGL((attn_wide_kernel<D, FMT == FMT_E4M3>), dim3(blocks), dim3(kWideThreads), 2 * list_bytes, stream, A, list);
     }
-    if (A.chunks > 1)
-        hipLaunchKernelGGL((join_kernel<D>), dim3(ceil_div(A.total_rows * A.hq, kJoinWaves)), dim3(64 * kJoinWaves), 0, stream, A, wide ? 1 : 0);
+    if (A.chunks > 1) return launch_join(A, wide, 0, stream);
     return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_fmt(const AttnArgs &A, bool wide, long long pieces, hipStream_t stream)
+{
+    switch (format_of(A.kv)) {
+    case FMT_BF16: return launch_d<D, FMT_BF16>(A, wide, pieces, stream);
+    case FMT_E4M3: return launch_d<D, FMT_E4M3>(A, wide, pieces, stream);
+    default: return launch_d<D, FMT_MXFP4>(A, wide, pieces, stream);
+    }
 }
 
 int column_tiles(int max_rows, int group)
@@ -1248,6 +1079,27 @@ int column_tiles(int max_rows, int group)
 }
 
 }  // namespace
+
+hipError_t launch_join(const AttnArgs &A, bool wide, int split_keys, hipStream_t stream)
+{
+    const dim3 grid(ceil_div(A.total_rows * A.hq, kJoinWaves)), block(64 * kJoinWaves);
+    const int w = wide ? 1 : 0;
+    switch (A.kv.d) {
+    case 64:
+        if (split_keys) join_kernel<64, true><<<grid, block, 0, stream>>>(A, w, split_keys);
+        else join_kernel<64, false><<<grid, block, 0, stream>>>(A, w, 0);
+        break;
+    case 128:
+        if (split_keys) join_kernel<128, true><<<grid, block, 0, stream>>>(A, w, split_keys);
+        else join_kernel<128, false><<<grid, block, 0, stream>>>(A, w, 0);
+        break;
+    default:
+        if (split_keys) join_kernel<256, true><<<grid, block, 0, stream>>>(A, w, split_keys);
+        else join_kernel<256, false><<<grid, block, 0, stream>>>(A, w, 0);
+        break;
+    }
+    return hipGetLastError();
+}
 
 size_t attn_workspace_bytes(int hq, int hkv, int d, int total_rows, int max_rows, int max_kv)
 {
@@ -1270,15 +1122,15 @@ bool attn_fits(const AttnArgs &A)
 
 hipError_t launch_attn(AttnArgs A, void *workspace, hipStream_t stream)
 {
-    const bool wide = is_wide(A.max_rows, A.group), f8 = A.kv.k_scale != nullptr;
+    const bool wide = is_wide(A.max_rows, A.group);
     const long long pieces = most_pieces(A, wide);
     A.chunks = chunk_bound(A.max_kv, wide);
     A.part = static_cast<float *>(workspace);
     A.stat = reinterpret_cast<float2 *>(A.part + (size_t)A.total_rows * A.hq * A.chunks * A.kv.d);
     switch (A.kv.d) {
-    case 64: return f8 ? launch_d<64, true>(A, wide, pieces, stream) : launch_d<64, false>(A, wide, pieces, stream);
-    case 128: return f8 ? launch_d<128, true>(A, wide, pieces, stream) : launch_d<128, false>(A, wide, pieces, stream);
-    default: return f8 ? launch_d<256, true>(A, wide, pieces, stream) : launch_d<256, false>(A, wide, pieces, stream);
+    case 64: return launch_fmt<64>(A, wide, pieces, stream);
+    case 128: return launch_fmt<128>(A, wide, pieces, stream);
+    default: return launch_fmt<256>(A, wide, pieces, stream);
     }
 }
 

@@ -5,6 +5,7 @@
 #include "gdn_attn.h"
 #include "gdn_device.h"
 #include "gdn_internal.h"
+#include "gdn_mxfp4.h"
 #include "gdn_once.h"
 
 namespace gdn {
@@ -217,10 +218,65 @@ __device__ __forceinline__ float max_group(float x)
     return x;
 }
 
+// A key head's values once more, in fp64 from its bf16 channels up to the last
+// rounding: norm, then rotation.  For all lanes of a wave; those of other heads
+// keep what they have.
+template <int LANES>
+__device__ __forceinline__ double sum_group(double x)
+{
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) x += __shfl_xor(x, o);
+    return x;
+}
+template <int D, int LANES>
+__device__ __forceinline__ void exact_key(const PrepArgs &A, uint4 raw, int lane, bool is_k, float *row, const double *cs, const double *sn,
+                                          float (&x)[8])
+{
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[2 * i] = __uint_as_float(w[i] << 16);
+        y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    double inv = 1.0;
+    if (A.k_norm) {
+        double ss = 0.0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fma((double)y[i], (double)y[i], ss);
+        inv = 1.0 / sqrt(sum_group<LANES>(ss) * (1.0 / D) + (double)A.eps);
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) row[8 * lane + i] = y[i];
+    __builtin_amdgcn_wave_barrier();
+    const int half = A.rot / 2;
+    if (is_k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = 8 * lane + i;
+            auto normed = [&](int c) { return (double)row[c] * inv * (A.k_norm ? (double)A.k_norm[c] : 1.0); };
+            double z = normed(e);
+            if (e < 2 * half) {
+                const bool second = A.interleaved ? e & 1 : e >= half;
+                const int p = A.interleaved ? e >> 1 : second ? e - half : e;
+                const double other = normed(A.interleaved ? e ^ 1 : second ? e - half : e + half);
+                z = second ? fma(z, cs[p], other * sn[p]) : fma(z, cs[p], -(other * sn[p]));
+            }
+            x[i] = (float)z;
+        }
+    __builtin_amdgcn_wave_barrier();
+}
+
 // The rows pass through once, and what is stored is read by other kernels on
 // whichever XCD: load_once and store_once (the prompt pass of 8,306 rows takes
 // 62 us with them and 68 us without).
-template <int D>
+//
+// Into a 4-bit cache (MX) a key's norm and rotation are taken in fp64 up to the
+// fp32 value that is quantised: that close to a border between two codes or two
+// scales fp32 sums would decide by the order of their terms.  Only the key heads
+// need it, and memory stays the bound.
+template <int D, bool MX>
 __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, const int span)
 {
     constexpr int LANES = D / 8, HEADS = kPrepThreads / LANES;   // heads a workgroup handles at once
@@ -228,6 +284,7 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, co
     // this workgroup's heads: span of them from span * blockIdx.y
     __shared__ float cs[kPrepMaxHalf], sn[kPrepMaxHalf];
     __shared__ __align__(16) float swap[HEADS][D];
+    __shared__ double cs64[MX ? kPrepMaxHalf : 1], sn64[MX ? kPrepMaxHalf : 1];
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid % LANES, grp = tid / LANES;
     const int half = A.rot / 2, hkv = A.kv.hkv, first = span * blockIdx.y, heads = min(A.hq + 2 * hkv, first + span);
     const int64_t q_row = r * A.q_row, k_row = r * A.k_row, v_row = r * A.v_row;
@@ -252,6 +309,12 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, co
         sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
         cs[tid] = c * A.rot_scale;
         sn[tid] = s * A.rot_scale;
+        if constexpr (MX) {
+            double s64, c64;
+            sincos((double)pos * (double)A.inv_freq[tid], &s64, &c64);      // the product is exact
+            cs64[tid] = c64 * (double)A.rot_scale;
+            sn64[tid] = s64 * (double)A.rot_scale;
+        }
     }
     const int page = slot >> A.kv.page_shift, off = slot & ((1 << A.kv.page_shift) - 1);
     const bool cached = slot >= 0 && page < A.kv.n_pages;
@@ -316,7 +379,28 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, co
                 store_once(A.q_out + ((size_t)r * A.hq + h) * D + 8 * lane, o);
             }
             const size_t at = (((size_t)page * hkv + kvh) << A.kv.page_shift) + off;
-            if (A.kv.k_scale) {
+            if constexpr (MX) {
+                if (__ballot(is_k)) exact_key<D, LANES>(A, raw[b], lane, is_k, swap[grp], cs64, sn64, x);
+                uint32_t top = 0;               // of the bits: a NaN is above infinity
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+                top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, false));
+                top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, false));
+                if (there && !is_q && cached) {
+                    const bool fin = top < 0x7f800000u;
+                    const int e = fin ? min(max((int)((top + (1u << 21)) >> 23) - 2, kMxLeast), kMxMost) : kMxNan;
+                    const float to = __uint_as_float((uint32_t)(254 - e) << 23);         // 2^(127 - e)
+                    uint32_t codes = 0;
+                    if (fin) {
+                        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, x[0] * to, x[1] * to, 1.0f, 0);
+                        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, x[2] * to, x[3] * to, 1.0f, 1);
+                        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, x[4] * to, x[5] * to, 1.0f, 2);
+                        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, x[6] * to, x[7] * to, 1.0f, 3);
+                    }
+                    *reinterpret_cast<uint32_t *>((is_k ? A.kv.k : A.kv.v) + at * (D / 2) + 4 * lane) = codes;
+                    if (lane % 4 == 0) (is_k ? A.kv.k_exp : A.kv.v_exp)[at * (D / kMxBlock) + lane / 4] = (uint8_t)e;
+                }
+            } else if (A.kv.k_scale) {
                 float m = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
@@ -411,6 +495,90 @@ __global__ __launch_bounds__(256) void attn_commit_kernel(const AttnCommitArgs A
             for (int t = 0; t < kMaxWindowRows; ++t)
                 if (t >= first && t < n) pool[dst[t]] = x[t];
         }
+    } else if (A.kv.k_exp) {
+        const int exps = A.kv.d / kMxBlock;             // bytes of a row
+        for (int i = tid; i < 2 * A.kv.hkv * exps; i += 256) {
+            const int j = i % (A.kv.hkv * exps), h = j / exps;
+            uint8_t *pool = (i == j ? A.kv.k_exp : A.kv.v_exp) + (((size_t)h << A.kv.page_shift) * exps + j % exps);
+            uint8_t x[kMaxWindowRows];
+#pragma unroll
+            for (int t = 0; t < kMaxWindowRows; ++t)
+                x[t] = pool[(size_t)src[min(t, n - 1)] * exps];
+#pragma unroll
+            for (int t = 0; t < kMaxWindowRows; ++t)
+                if (t >= first && t < n) pool[(size_t)dst[t] * exps] = x[t];
+        }
+    }
+}
+
+// ---- cached rows read back ---------------------------------------------------
+//
+// Bounded by memory: 16 packed rows a workgroup, all their kv heads, 16 bytes of
+// bf16 a lane and step, so that every wave writes runs of 1 KB.
+constexpr int kReadRows = 16, kReadThreads = 256;
+
+template <int FMT>
+__global__ __launch_bounds__(kReadThreads) void read_kernel(const ReadArgs A)
+{
+    __shared__ int at[kReadRows];                   // a row's place in the cache (of kv head 0), or -1
+    const int tid = threadIdx.x, first = blockIdx.x * kReadRows, rows = min(kReadRows, A.total_rows - first);
+    if (tid < 64) {
+        // lane i: row first + i of the stream whose rows hold it
+        const int r = first + min(tid, rows - 1);
+        int stream = -1, t = 0;
+        auto look = [&](int block) {
+            const int s = block + tid;
+            int r0 = 0, r1 = 0;
+            if (s < A.n_streams) {
+                r0 = A.row_start[s], r1 = A.row_start[s + 1];
+                const int f = A.first[s];
+                const bool ok = r0 >= 0 && r1 >= r0 && r1 <= A.total_rows && f >= 0 && (long long)f + (r1 - r0) <= (long long)A.max_blocks << A.kv.page_shift;
+                if (!ok) r0 = r1 = 0;
+            }
+            uint64_t some = __ballot(r1 > first && r0 < first + rows);
+            while (some) {
+                const int l = __builtin_ctzll(some);
+                some &= some - 1;
+                const int a = __builtin_amdgcn_readlane(r0, l), b = __builtin_amdgcn_readlane(r1, l);
+                if (stream < 0 && r >= a && r < b) stream = block + l, t = r - a;
+            }
+        };
+        for (int block = 0; block < A.n_streams && __ballot(stream < 0); block += 64) look(block);
+        int row = -1;
+        if (stream >= 0) {
+            const int key = A.first[stream] + t;
+            const int id = A.table[(size_t)stream * A.max_blocks + (key >> A.kv.page_shift)];
+            if (id >= 0 && id < A.kv.n_pages) row = ((id * A.kv.hkv) << A.kv.page_shift) + (key & ((1 << A.kv.page_shift) - 1));
+        }
+        if (tid < rows) at[tid] = row;
+    }
+    __syncthreads();
+    const int d = A.kv.d, per = d / 8, per_row = A.kv.hkv * per;        // 16-byte pieces of a head, and of a row
+    for (int i = tid; i < 2 * rows * per_row; i += kReadThreads) {
+        const bool is_v = i >= rows * per_row;
+        const int j = i - is_v * rows * per_row, r = j / per_row, x = j - r * per_row, h = x / per, p = x - h * per;
+        if (at[r] < 0) continue;
+        const size_t row = (size_t)at[r] + ((size_t)h << A.kv.page_shift);
+        const uint8_t *pool = is_v ? A.kv.v : A.kv.k;
+        uint4 y;
+        if constexpr (FMT == FMT_BF16) {
+            y = load_once(pool + (row * d + 8 * p) * 2);
+        } else if constexpr (FMT == FMT_E4M3) {
+            const uint2 c = *reinterpret_cast<const uint2 *>(pool + row * d + 8 * p);
+            const float f = (is_v ? A.kv.v_scale : A.kv.k_scale)[row];
+            float z[8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t w = k ? c.y : c.x;
+                z[4 * k] = __builtin_amdgcn_cvt_f32_fp8(w, 0) * f, z[4 * k + 1] = __builtin_amdgcn_cvt_f32_fp8(w, 1) * f;
+                z[4 * k + 2] = __builtin_amdgcn_cvt_f32_fp8(w, 2) * f, z[4 * k + 3] = __builtin_amdgcn_cvt_f32_fp8(w, 3) * f;
+            }
+            y = make_uint4(pack2(z[0], z[1]), pack2(z[2], z[3]), pack2(z[4], z[5]), pack2(z[6], z[7]));
+        } else {
+            const uint32_t c = *reinterpret_cast<const uint32_t *>(pool + row * (d / 2) + 4 * p);
+            y = mx_values8(c, mx_scale((is_v ? A.kv.v_exp : A.kv.k_exp)[row * (d / kMxBlock) + p / 4]));
+        }
+        store_once((is_v ? A.v_out : A.k_out) + ((size_t)(first + r) * per_row + x) * 8, y);
     }
 }
 
@@ -444,7 +612,9 @@ static void launch_prep_d(const PrepArgs &A, hipStream_t stream)
     // instead of 11.0, 8,306 rows 86 instead of 62)
     const int heads = A.hq + 2 * A.kv.hkv, at_once = kPrepThreads / (D / 8);
     const int span = A.rows <= kPrepFewRows && heads > at_once ? at_once : heads;
-    prep_kernel<D><<<dim3(A.rows, (heads + span - 1) / span), kPrepThreads, 0, stream>>>(A, span);
+    const dim3 grid(A.rows, (heads + span - 1) / span);
+    if (A.kv.k_exp) prep_kernel<D, true><<<grid, kPrepThreads, 0, stream>>>(A, span);
+    else prep_kernel<D, false><<<grid, kPrepThreads, 0, stream>>>(A, span);
 }
 
 hipError_t launch_prep(const PrepArgs &A, hipStream_t stream)
@@ -459,7 +629,18 @@ hipError_t launch_prep(const PrepArgs &A, hipStream_t stream)
 
 hipError_t launch_attn_commit(const AttnCommitArgs &A, hipStream_t stream)
 {
-    attn_commit_kernel<<<A.n_streams, 256, 0, stream>>>(A, A.kv.d * (A.kv.k_scale ? 1 : 2));
+    attn_commit_kernel<<<A.n_streams, 256, 0, stream>>>(A, A.kv.k_exp ? A.kv.d / 2 : A.kv.d * (A.kv.k_scale ? 1 : 2));
+    return hipGetLastError();
+}
+
+hipError_t launch_read(const ReadArgs &A, hipStream_t stream)
+{
+    const int blocks = (A.total_rows + kReadRows - 1) / kReadRows;
+    switch (format_of(A.kv)) {
+    case FMT_BF16: read_kernel<FMT_BF16><<<blocks, kReadThreads, 0, stream>>>(A); break;
+    case FMT_E4M3: read_kernel<FMT_E4M3><<<blocks, kReadThreads, 0, stream>>>(A); break;
+    default: read_kernel<FMT_MXFP4><<<blocks, kReadThreads, 0, stream>>>(A); break;
+    }
     return hipGetLastError();
 }
 

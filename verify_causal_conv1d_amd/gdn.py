@@ -31,6 +31,7 @@ EXPORTED = (
     "gdn_check_layout",
     "gdn_inproj_affine4", "gdn_inproj_pack_affine4", "gdn_inproj_padded_features",
     "gdn_kv_tables", "gdn_attn_prep", "gdn_attn_workspace_bytes", "gdn_attn_window", "gdn_attn_commit",
+    "gdn_attn_prompt_workspace_bytes", "gdn_attn_prompt", "gdn_kv_read",
 )
 
 
@@ -90,11 +91,15 @@ def lib():
             L.gdn_attn_workspace_bytes.argtypes = [P, i32, i32, i32, i32, i32]
             L.gdn_attn_window.argtypes = [P] + [i32] * 6 + [P] * 6 + [i64, i64, f32, P, P, C.c_size_t, P]
             L.gdn_attn_commit.argtypes = [P] + [i32] * 4 + [P] * 7
+            L.gdn_attn_prompt_workspace_bytes.restype = C.c_size_t
+            L.gdn_attn_prompt_workspace_bytes.argtypes = [P, i32, i32, i32, i32]
+            L.gdn_attn_prompt.argtypes = [P] + [i32] * 5 + [P] * 5 + [i64, i64, f32, P, P, C.c_size_t, P]
+            L.gdn_kv_read.argtypes = [P] + [i32] * 3 + [P] * 6
             for name in ("gdn_conv_step", "gdn_recur_window", "gdn_recur_tree", "gdn_commit",
                          "gdn_recur_log", "gdn_commit_replay", "gdn_prefill_chunked",
                          "gdn_prefill_chunked_noalloc",
                          "gdn_check_layout", "gdn_inproj_affine4", "gdn_inproj_pack_affine4", "gdn_kv_tables",
-                         "gdn_attn_prep", "gdn_attn_window", "gdn_attn_commit"):
+                         "gdn_attn_prep", "gdn_attn_window", "gdn_attn_commit", "gdn_attn_prompt", "gdn_kv_read"):
                 getattr(L, name).restype = C.c_int
             _lib = L
     return _lib
@@ -326,7 +331,7 @@ def inproj_affine4(shape, x, wq, scales, biases, qkv, a, b, group: int):
 # (what is wrong is worked out only when one fails), structs are packed bytes,
 # and the stream comes from torch as its raw handle.
 
-_BF16, _F32, _I32, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+_BF16, _F32, _I32, _F8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn, torch.uint8
 _pack_cache = struct.Struct("PPPPiiiii4x").pack     # gdn_kv_cache
 _pack_rope = struct.Struct("Piif4x").pack           # gdn_rope
 # the current stream's handle and the current device, of a process that holds device
@@ -360,6 +365,12 @@ def _f32s(name, t, dev, size):
     return t.data_ptr()
 
 
+def _u8s(name, t, dev, size):
+    if t.dtype is not _U8 or t.get_device() != dev or t.numel() != size or not t.is_contiguous():
+        _wrong(name, t, _U8, dev, size)
+    return t.data_ptr()
+
+
 def _on(t: torch.Tensor, name: str) -> int:
     dev = t.get_device()
     if dev < 0:
@@ -386,8 +397,8 @@ def _cache(dev, k, v, k_scale, v_scale):
     shape = k.shape
     pages, hkv, page, d = shape
     dtype = k.dtype
-    if dtype is not _BF16 and dtype is not _F8:
-        raise TypeError(f"k_cache must be {_BF16} or {_F8}, got {dtype}")
+    if dtype is not _BF16 and dtype is not _F8 and dtype is not _U8:
+        raise TypeError(f"k_cache must be {_BF16}, {_F8} or {_U8} (two 4-bit codes), got {dtype}")
     if k.get_device() != dev or not k.is_contiguous():
         _wrong("k_cache", k, dtype, dev, tuple(shape))
     if v.dtype is not dtype or v.get_device() != dev or v.shape != shape or not v.is_contiguous():
@@ -397,8 +408,13 @@ def _cache(dev, k, v, k_scale, v_scale):
             raise ValueError("a bfloat16 cache has no scales")
         return _pack_cache(k.data_ptr(), v.data_ptr(), 0, 0, pages, page, hkv, d, 0), hkv, d
     if k_scale is None or v_scale is None:
-        raise ValueError("a float8_e4m3fn cache needs k_scale and v_scale")
+        raise ValueError(f"a {str(dtype)[6:]} cache needs k_scale and v_scale")
     rows = pages * hkv * page
+    if dtype is _U8:        # MXFP4
+        d *= 2
+        exps = rows * (d // 32)
+        return _pack_cache(k.data_ptr(), v.data_ptr(), _u8s("k_scale", k_scale, dev, exps), _u8s("v_scale", v_scale, dev, exps),
+                           pages, page, hkv, d, 4), hkv, d
     return _pack_cache(k.data_ptr(), v.data_ptr(), _f32s("k_scale", k_scale, dev, rows), _f32s("v_scale", v_scale, dev, rows),
                        pages, page, hkv, d, 1), hkv, d
 
@@ -501,6 +517,59 @@ def attn_window(row_start, kv_len, block_table, q, k_cache, v_cache, out, worksp
             None if parent is None else _i32s("parent", parent, dev, total), _i32s("kv_len", kv_len, dev, n),
             _i32s("block_table", block_table, dev, n * blocks), q.data_ptr(), gp, gr, gh,
             d ** -0.5 if scale is None else scale, out.data_ptr(), ws, size)
+
+
+def attn_prompt_workspace_bytes(hq: int, hkv: int, d: int, n_streams: int, total_rows: int, max_kv: int) -> int:
+    """Bytes of workspace that serve every ``attn_prompt`` call with these heads and
+    up to these sizes: any total_rows and max_kv that are no larger."""
+    return int(lib().gdn_attn_prompt_workspace_bytes(_pack_cache(0, 0, 0, 0, 1, 16, hkv, d, 0), int(n_streams), int(total_rows),
+                                                     int(max_kv), int(hq)))
+
+
+def attn_prompt(row_start, kv_len, block_table, q, k_cache, v_cache, out, workspace, max_kv: int, gate=None, k_scale=None,
+                v_scale=None, scale=None):
+    """Causal attention of packed prompts of any lengths over the cache, which holds
+    this pass's rows already: row t of stream s sees cache rows up to kv_len[s] + t.
+    ``scale`` of the scores d ** -0.5 unless given, ``gate`` (bf16 [R][hq][d], may
+    be a view) applied as sigmoid(gate)."""
+    dev = _on(q, "q")
+    cache, _, d = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    shape = _query(q, d)
+    total, hq, _ = shape
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [streams][blocks]")
+    n, blocks = block_table.shape
+    if q.dtype is not _BF16 or not q.is_contiguous():
+        _wrong("q", q, _BF16, dev, tuple(shape))
+    if out.dtype is not _BF16 or out.get_device() != dev or out.shape != shape or not out.is_contiguous():
+        _wrong("out", out, _BF16, dev, tuple(shape))
+    gp, gr, gh = (None, 0, 0) if gate is None else _heads(dev, "gate", gate, shape)
+    ws, size = None, 0
+    if workspace is not None:
+        size = workspace.numel()
+        ws = _u8s("workspace", workspace, dev, size)
+    _launch(dev, "gdn_attn_prompt", cache, n, total, max_kv, blocks, hq, _i32s("row_start", row_start, dev, n + 1),
+            _i32s("kv_len", kv_len, dev, n), _i32s("block_table", block_table, dev, n * blocks), q.data_ptr(), gp, gr, gh,
+            d ** -0.5 if scale is None else scale, out.data_ptr(), ws, size)
+
+
+def kv_read(row_start, first, block_table, k_cache, v_cache, k_out, v_out, k_scale=None, v_scale=None):
+    """Cached rows read back: packed row ``row_start[s] + t`` of k_out and v_out
+    (bf16 [R][hkv][d], written) is cache row ``first[s] + t`` of stream s."""
+    dev = _on(row_start, "row_start")
+    cache, hkv, d = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [streams][blocks]")
+    n, blocks = block_table.shape
+    if k_out.dim() != 3:
+        raise ValueError(f"k_out must be [rows][kv heads][d], got {tuple(k_out.shape)}")
+    total = k_out.shape[0]
+    shape = (total, hkv, d)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t.dtype is not _BF16 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+            _wrong(name, t, _BF16, dev, shape)
+    _launch(dev, "gdn_kv_read", cache, n, total, blocks, _i32s("row_start", row_start, dev, n + 1), _i32s("first", first, dev, n),
+            _i32s("block_table", block_table, dev, n * blocks), k_out.data_ptr(), v_out.data_ptr())
 
 
 def attn_commit(row_start, accept_row, kv_len, block_table, k_cache, v_cache, k_scale=None, v_scale=None, parent=None,
