@@ -133,6 +133,70 @@ def window_bound(ref, mag, reach, d):
     return 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -18 + 2.0 * (d + 8) * 2.0 ** -24 * reach[..., None]) * 1.01 * mag + 1e-37
 
 
+def prompt(page, row_start, kv_len, block_table, q, k, v, scale, gate=None):
+    """As ``window`` for chains of any length, a stream and head at a time."""
+    R, hq, d = q.shape
+    G = hq // k.shape[1]
+    out, mag, reach = np.zeros((R, hq, d)), np.zeros((R, hq, d)), np.zeros((R, hq))
+    for s in range(len(kv_len)):
+        a, b, c = int(row_start[s]), int(row_start[s + 1]), int(kv_len[s])
+        if a == b:
+            continue
+        at = np.arange(c + b - a)
+        pages, offs = np.asarray(block_table)[s][at // page], at % page
+        hidden = at[None, :] > c + np.arange(b - a)[:, None]
+        for h in range(hq):
+            kk, vv = k[pages, h // G, offs], v[pages, h // G, offs]
+            x = np.where(hidden, -np.inf, q[a:b, h] @ kk.T * scale)
+            p = np.exp(x - x.max(1, keepdims=True))
+            p /= p.sum(1, keepdims=True)
+            g = 1.0 if gate is None else 1.0 / (1.0 + np.exp(-gate[a:b, h]))
+            out[a:b, h], mag[a:b, h] = p @ vv * g, p @ np.abs(vv) * g
+            reach[a:b, h] = np.where(hidden, 0.0, np.abs(q[a:b, h]) @ np.abs(kk).T).max(1) * abs(scale)
+    return out, mag, reach
+
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def mx_values(codes, exps):
+    """The values of MXFP4 rows: codes [..][d / 2] (even channels in the low halves), exps [..][d / 32]."""
+    c = np.stack([codes & 15, codes >> 4], -1).reshape(*codes.shape[:-1], -1)
+    y = np.where(c >= 8, -1.0, 1.0) * E2M1[c & 7]
+    e = np.repeat(exps.astype(np.int64), 32, -1)
+    return np.where(e > 252, np.nan, np.ldexp(y, np.where(e > 252, 127, e) - 127))
+
+
+def mx_quantise(y):
+    """fp32 rows [..][d] in MXFP4: the exponent that puts a block's largest
+    magnitude into [3.5, 7) (within 25 .. 252; 255 if a value is not finite), and
+    of the 8 magnitudes the nearest, of two as near the one with the even code."""
+    y = np.asarray(y, np.float32).astype(np.float64)
+    b = y.reshape(*y.shape[:-1], -1, 32)
+    fin = np.isfinite(b).all(-1)
+    top = np.where(fin, np.abs(np.where(np.isfinite(b), b, 0.0)).max(-1), 1.0)
+    e = np.full(top.shape, 25)
+    for x in range(25, 252):                       # the least exponent that the rule allows
+        e = np.where(top >= 7.0 * 2.0 ** (x - 127), x + 1, e)
+    a = np.where(fin[..., None], np.abs(np.where(np.isfinite(b), b, 0.0)) / np.ldexp(1.0, e - 127)[..., None], 0.0)
+    far = np.abs(a[..., None] - E2M1)
+    near = far == far.min(-1, keepdims=True)
+    order = np.array([0, 2, 4, 6, 1, 3, 5, 7])
+    code = order[np.argmax(near[..., order], -1)]
+    code = np.where(fin[..., None], code + 8 * np.signbit(b), 0).astype(np.uint8).reshape(y.shape)
+    return code[..., 0::2] | code[..., 1::2] << 4, np.where(fin, e, 255).astype(np.uint8)
+
+
+def read(page, row_start, first, block_table, pool, out):
+    """The rows of ``out`` [R][hkv][d] after reading pool's values [pages][hkv][page][d] back."""
+    out = out.copy()
+    for s in range(len(first)):
+        for r in range(int(row_start[s]), int(row_start[s + 1])):
+            at = int(first[s]) + r - int(row_start[s])
+            out[r] = pool[block_table[s, at // page], :, at % page]
+    return out
+
+
 def commit(page, row_start, parent, accept, kv_len, block_table, *pools):
     """The pools ([pages][hkv][page] + ...) and lengths after the accepted paths moved."""
     pools = [p.copy() for p in pools]

@@ -885,7 +885,6 @@ int gdn_attn_prompt(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_
     if (!block_table) return fail(GDN_EINVAL, "block_table is NULL");
     REQUIRE_PTR(q);
     REQUIRE_PTR(out);
-    if (reinterpret_cast<uintptr_t>(gate) & 7u) return fail(GDN_EINVAL, "gate must be 8-byte aligned");
     A.n_streams = n_streams;
     A.total_rows = total_rows;
     A.max_kv = max_kv;
@@ -899,6 +898,7 @@ int gdn_attn_prompt(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_
             return fail(GDN_EWORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
         if (!aligned16(workspace)) return fail(GDN_EINVAL, "workspace must be 16-byte aligned");
     }
+    if (reinterpret_cast<uintptr_t>(gate) & 7u) return fail(GDN_EINVAL, "gate must be 8-byte aligned");
     A.row_start = row_start;
     A.kv_len = kv_len;
     A.table = block_table;
