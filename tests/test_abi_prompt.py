@@ -83,7 +83,7 @@ def test_a_workspace_serves_every_smaller_call(L, hq, hkv, d):  # noqa: F811
     c = cache(hkv=hkv, d=d, page=16, pages=100)
     lengths = (1, 511, 512, 1023, 1024, 5000, 40000, 262144, 1 << 21)
     rows = (1, 2, 3, 10, 42, 43, 64, 65, 100, 255, 256, 257, 1000, 2730, 2731, 8306, 30000)
-    assert gdn.attn_prompt_workspace_bytes(hq, hkv, d, 4, 100, 1000) == 0              # not cut
+    assert gdn.attn_prompt_workspace_bytes(hq, hkv, d, 4, 100, 500) == 0               # not cut
     cut = 0
     for most_rows in (1, 65, 1000, 8306, 30000):
         for most in lengths:
@@ -94,7 +94,7 @@ def test_a_workspace_serves_every_smaller_call(L, hq, hkv, d):  # noqa: F811
                     rc = prompt(L, c=c, n=16, total=total, max_kv=kv, blocks=1 << 18, hq=hq, ws=P8, wsb=size, gate=P4)
                     refused(L, rc, gdn.GDN_EINVAL, "must be")
                     cut += "workspace" in L.gdn_last_error().decode()
-    assert cut > 0 or hkv == 1024
+    assert cut > 0
 
 
 def test_binding_takes_a_4_bit_cache():

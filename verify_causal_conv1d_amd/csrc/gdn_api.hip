@@ -857,7 +857,7 @@ size_t gdn_attn_prompt_workspace_bytes(const gdn_kv_cache *cache, int32_t n_stre
     if (check_cache_sizes(cache, K) != GDN_OK || check_heads(cache, hq, max_kv) != GDN_OK
         || check_counts(n_streams, total_rows, 1, 1, cache->page_size) != GDN_OK)
         return 0;
-    return gdn::prompt_workspace_bytes(hq, cache->hkv, cache->d, total_rows, max_kv, true);
+    return gdn::prompt_workspace_most(hq, cache->d, total_rows, max_kv);
 }
 
 int gdn_attn_prompt(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows, int32_t max_kv,
@@ -892,7 +892,7 @@ int gdn_attn_prompt(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_
     A.hq = hq;
     A.group = hq / cache->hkv;
     if (!gdn::prompt_fits(A)) return fail(GDN_EUNSUPPORTED, "too many rows, streams or chunks for one launch");
-    const size_t need = gdn::prompt_workspace_bytes(hq, cache->hkv, cache->d, total_rows, max_kv, false);
+    const size_t need = gdn::prompt_workspace_bytes(hq, cache->hkv, cache->d, gdn::format_of(A.kv), n_streams, total_rows, max_kv);
     if (need > 0) {
         if (!workspace || workspace_bytes < need)
             return fail(GDN_EWORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);

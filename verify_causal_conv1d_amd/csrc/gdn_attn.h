@@ -78,9 +78,10 @@ hipError_t launch_tables(const TablesArgs &A, hipStream_t stream);
 hipError_t launch_prep(const PrepArgs &A, hipStream_t stream);
 hipError_t launch_attn(AttnArgs A, void *workspace, hipStream_t stream);
 
-// Attention of whole prompts: max_rows is not looked at.  The workspace of a call
-// with just these bounds, or (or_less) of any with no larger ones.
-size_t prompt_workspace_bytes(int hq, int hkv, int d, int total_rows, int max_kv, bool or_less);
+// Attention of whole prompts: max_rows is not looked at.  The workspace of a call,
+// and one that is enough for all calls with no larger sizes.
+size_t prompt_workspace_bytes(int hq, int hkv, int d, int fmt, int n_streams, int total_rows, int max_kv);
+size_t prompt_workspace_most(int hq, int d, int total_rows, int max_kv);
 bool prompt_fits(const AttnArgs &A);
 hipError_t launch_prompt(AttnArgs A, void *workspace, hipStream_t stream);
 // Windows of more than 16 columns over a 4-bit cache, in the chunks of the others

@@ -27,7 +27,35 @@ __device__ __forceinline__ float sum_halves(float x)
     return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
+// The lane's number, worked out anew where it is needed: no register holds it
+// through the loop.
+__device__ __forceinline__ int this_lane()
+{
+    int x;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(x));
+    return x;
+}
+
+// The kernel's arguments, loaded anew: none of them holds scalar registers through
+// the loop for the sake of what comes after it (registers that hold spilled scalars
+// went to memory, and every wait for one of them waited for all stores before it).
+typedef const __attribute__((address_space(4))) AttnArgs const_args;
+__device__ __forceinline__ const_args *fresh_args()
+{
+    auto p = reinterpret_cast<uintptr_t>(__builtin_amdgcn_kernarg_segment_ptr());
+    asm volatile("" : "+s"(p));
+    return (const_args *)p;
+}
+
+__device__ __forceinline__ float uniform(float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x))); }
+
+// Entries of the block table, which nothing writes while the kernel runs, through
+// the scalar cache: their addresses are the wave's.
+typedef const __attribute__((address_space(4))) int const_int;
+__device__ __forceinline__ int table_entry(const int *table, int i) { return ((const_int *)table)[i]; }
+
 constexpr int kSub = 32;       // keys of a matrix instruction's tile
+constexpr int kAhead = 3;      // operands on their way from LDS
 
 // A stage of keys and values in LDS, in bf16: KEYS rows of K, then of V.  The
 // 16-byte pieces of a row of K are exchanged by a function of the row, so that 16
@@ -54,9 +82,12 @@ struct PromptPiece {
     int k0, k1, nch, cols;
 };
 
-// The pieces of all streams, in stream order, 64 streams a step; of a stream the
-// last rows, which see the most keys, first, and the kv heads innermost, so that
-// the workgroups of a head meet in as few XCDs as can be.
+// The pieces of all streams.  Their kv heads are innermost, so that the workgroups
+// of a head meet in as few XCDs as can be, and the tiles that see the most keys
+// come first, since workgroups begin in their order: of a stream its last rows,
+// and where a wave holds all streams and they are not cut into chunks, over all of
+// them (a prompt of 4,722 rows packed after shorter ones began too late to end
+// with them: 451 us and 373 in order).
 template <int COLS, bool WINDOW>
 __device__ __forceinline__ bool find_piece(const AttnArgs &A, int split_keys, int item, PromptPiece &K)
 {
@@ -74,8 +105,31 @@ __device__ __forceinline__ bool find_piece(const AttnArgs &A, int split_keys, in
             item -= all;
             continue;
         }
-        const int l = __builtin_ctzll(__ballot(incl > item));
-        int x = item - (l ? __builtin_amdgcn_readlane(incl, l - 1) : 0);
+        int l, x;
+        if (!WINDOW && A.n_streams > 1 && A.n_streams <= 64 && A.chunks == 1) {
+            // A tile's level: the cache row of its first pair.  Tiles of the lane's stream
+            // above a level; the one looked for has the least level that no more than
+            // y tiles are above.
+            auto above = [&](int level) {
+                const long long from = level < kv ? 0 : ((long long)(level - kv + 1) * A.group + COLS - 1) / COLS;
+                return from < tiles ? tiles - (int)from : 0;
+            };
+            auto total = [&](int level) { return __builtin_amdgcn_readlane(wave_running_sum(above(level)), 63); };
+            const int y = item / A.kv.hkv;
+            int lo = -1, hi = A.max_kv;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (total(mid) > y) lo = mid;
+                else hi = mid;
+            }
+            const int here = wave_running_sum(above(lo) - above(hi)), nth = y - total(hi);
+            l = __builtin_ctzll(__ballot(here > nth));
+            const int z = __builtin_amdgcn_readlane(above(lo), l) - 1 - (nth - (l ? __builtin_amdgcn_readlane(here, l - 1) : 0));
+            x = z * A.kv.hkv + item - y * A.kv.hkv;
+        } else {
+            l = __builtin_ctzll(__ballot(incl > item));
+            x = item - (l ? __builtin_amdgcn_readlane(incl, l - 1) : 0);
+        }
         K.s = first + l;
         K.r0 = __builtin_amdgcn_readlane(r0, l);
         K.m = __builtin_amdgcn_readlane(m, l);
@@ -111,83 +165,82 @@ __device__ __forceinline__ bool pages_ok(const AttnArgs &A, const PromptPiece &K
 
 // Channels d .. d + 3 of the values of a cache row, in bf16 (e4m3: before the row's scale).
 template <int D, int FMT>
-__device__ __forceinline__ uint2 cached_values4(const KvArgs &kv, size_t row, int d)
+__device__ __forceinline__ uint2 cached_values4(const uint8_t *pool, const uint8_t *exps, size_t row, int d)
 {
     if constexpr (FMT == FMT_BF16) {
-        return *reinterpret_cast<const uint2 *>(kv.v + (row * D + d) * 2);
+        return *reinterpret_cast<const uint2 *>(pool + (row * D + d) * 2);
     } else if constexpr (FMT == FMT_E4M3) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(kv.v + row * D + d);
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(pool + row * D + d);
         return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false)),
                           __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)));
     } else {
-        const uint32_t w = *reinterpret_cast<const uint16_t *>(kv.v + (row * D + d) / 2);
-        const float f = mx_scale(kv.v_exp[row * (D / kMxBlock) + d / kMxBlock]);
+        const uint32_t w = *reinterpret_cast<const uint16_t *>(pool + (row * D + d) / 2);
+        const float f = mx_scale(exps[row * (D / kMxBlock) + d / kMxBlock]);
         return make_uint2(mx_pair<0>(w, f), mx_pair<1>(w, f));
     }
 }
+// 4 channels of a result in bf16, gated
+__device__ __forceinline__ uint2 gated4(float4 o, bool gated, uint2 g)
+{
+    float x[4] = {o.x, o.y, o.z, o.w};
+    if (gated) {
+        x[0] *= sigmoid_f(__uint_as_float(g.x << 16));
+        x[1] *= sigmoid_f(__uint_as_float(g.x & 0xffff0000u));
+        x[2] *= sigmoid_f(__uint_as_float(g.y << 16));
+        x[3] *= sigmoid_f(__uint_as_float(g.y & 0xffff0000u));
+    }
+    return make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+}
+__device__ __forceinline__ int wave_int(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ float not_finite(uint32_t bits) { return (bits & 0x7f800000u) == 0x7f800000u ? __uint_as_float(bits) : 0.0f; }
 
-template <int D, int FMT, int WAVES, int TILES, int KEYS, bool WINDOW>
-__global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(const AttnArgs A, const int split_keys)
+template <int D, int FMT, int WAVES, int TILES, int KEYS, int PER_SIMD, bool WINDOW>
+__global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const AttnArgs A, const int split_keys)
 {
     using S = PromptShape<D, FMT, WAVES, TILES, KEYS>;
     constexpr int KS = D / 16, NT = D / 32, T = TILES;
     constexpr int NK = S::HALF / 1024, PER = 2 * NK / WAVES;     // direct loads of a stage's keys; of a wave, in all
-    static_assert(NK % WAVES == 0, "");
+    
     // separate arrays, so that loads into one are known not to touch the other
     __shared__ __align__(1024) uint8_t st0[S::BYTES], st1[S::BYTES];
     __shared__ __align__(16) float sc0[S::SCALES], sc1[S::SCALES];
     __shared__ int wave_ok[WAVES], bad;
+    __shared__ int2 pairs[S::COLS];          // packed row and query head of each column
+    __shared__ PromptPiece kept;             // K, for the end
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 31, g = lane >> 5;
-    const float scale = A.scale == 0.0f ? 1.0f : fabsf(A.scale);
+    const float scale = uniform(A.scale == 0.0f ? 1.0f : fabsf(A.scale));
     PromptPiece K;
     for (int item = blockIdx.x; find_piece<S::COLS, WINDOW>(A, split_keys, item, K); item += gridDim.x) {
-        bool ok = pages_ok(A, K, S::THREADS);
+        if (K.k0 >= K.k1) continue;                 // a chunk past all that the tile sees
+        bool ok = true;
         const int col0 = K.rt * S::COLS + wave * 32 * T;            // the wave's first column
         const bool busy = col0 < K.cols;                            // waves without columns only load
         const int t_lo = min(col0, K.cols - 1) / A.group, t_hi = min(col0 + 32 * T, K.cols) - 1;   // rows of the wave
         const int see_lo = K.kv + t_lo, see_hi = K.kv + t_hi / A.group;      // the last key that the first and the last one see
-        int row[T], head[T];
+        int row[T];
         uint32_t seen[T];
 #pragma unroll
         for (int c = 0; c < T; ++c) {
             const int col = min(col0 + 32 * c + n, K.cols - 1);     // past the last one: that one again, not stored
             const int t = col / A.group;
             row[c] = t;
-            head[c] = K.h * A.group + col - t * A.group;
+            pairs[wave * 32 * T + 32 * c + n] = make_int2(K.r0 + t, K.h * A.group + col - t * A.group);     // (both halves the same)
             seen[c] = 0;
             if constexpr (WINDOW) seen[c] = seen_rows(A, K.r0, K.m, t, ok);
         }
-        if (lane == 0) wave_ok[wave] = ok;
-        if (threadIdx.x == 0) bad = 0;
-        __syncthreads();
-        ok = true;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) ok = ok && wave_ok[w];
-        __syncthreads();
-        auto part_at = [&](int c) { return ((size_t)(K.r0 + row[c]) * A.hq + head[c]) * A.chunks + K.c; };
-        if (!ok) {
-            if (K.nch > 1 && g == 0)
-#pragma unroll
-                for (int c = 0; c < T; ++c)
-                    if (col0 + 32 * c + n < K.cols) A.stat[part_at(c)] = make_float2(0.0f, kSkipped);
-            continue;
-        }
-        if (K.k0 >= K.k1) continue;                 // a chunk past all that the tile sees
+        // place of a column's (row, head) in q and out
+        auto pair_of = [&](int c, int hq) {
+            const int2 p = pairs[wave * 32 * T + 32 * c + (this_lane() & 31)];
+            return (size_t)p.x * hq + p.y;
+        };
+        __builtin_amdgcn_wave_barrier();
         bf8v q[T][KS];
 #pragma unroll
         for (int c = 0; c < T; ++c) {
-            const uint16_t *p = A.q + ((size_t)(K.r0 + row[c]) * A.hq + head[c]) * D + 8 * g;
+            const uint16_t *p = A.q + pair_of(c, A.hq) * D + 8 * (this_lane() >> 5);
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                uint4 x = *reinterpret_cast<const uint4 *>(p + 16 * k);
-                if (A.scale <= 0.0f) {      // scores are multiplied by a positive scale: a negative one changes the queries' signs, 0 makes them 0
-                    const uint32_t sign = A.scale < 0.0f ? 0x80008000u : 0u, keep = A.scale < 0.0f ? ~0u : 0u;
-                    x = make_uint4((x.x & keep) ^ sign, (x.y & keep) ^ sign, (x.z & keep) ^ sign, (x.w & keep) ^ sign);
-                }
-                q[c][k] = __builtin_bit_cast(bf8v, x);
-            }
+            for (int k = 0; k < KS; ++k) q[c][k] = *reinterpret_cast<const bf8v *>(p + 16 * k);
         }
         f16v o[T][NT];
         float mx[T], sum[T];
@@ -203,64 +256,69 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(const AttnArgs A,
         // keys that every column of the workgroup sees
         const int all_see = WINDOW ? K.kv : K.kv + K.rt * S::COLS / A.group + 1;
 
-        // cache row of a key's group of 16 (past the stream's end: of its last keys)
         const int *table = A.table + (size_t)K.s * A.max_blocks;
-        auto cache_row = [&](int key) {
-            key = min(key, (K.len - 1) & ~15);
-            return ((table[key >> A.kv.page_shift] * A.kv.hkv + K.h) << A.kv.page_shift) + (key & ((1 << A.kv.page_shift) - 1));
-        };
         const int tiles = ceil_div(K.k1 - K.k0, S::KEYS);
-        constexpr int GROUPS = FMT == FMT_BF16 ? PER / 2 : S::LOADS;
-        int ahead[GROUPS], ahead_scale = 0;
+        // Pages of the groups of 16 keys of a stage, asked for a step before they are
+        // used; then the cache row of the nth group.
+        constexpr int GROUPS = S::KEYS / 16;
+        int pages[GROUPS], pages_key = 0;
+        auto look = [&](int tile) {
+            pages_key = K.k0 + min(tile, tiles - 1) * S::KEYS;
+#pragma unroll
+            for (int i = 0; i < GROUPS; ++i) pages[i] = table_entry(table, min(pages_key + 16 * i, (K.len - 1) & ~15) >> A.kv.page_shift);
+        };
+        auto group_row = [&](int i) {
+            int page = pages[0];
+#pragma unroll
+            for (int x = 1; x < GROUPS; ++x) page = i == x ? pages[x] : page;
+            page = (uint32_t)page < (uint32_t)A.kv.n_pages ? page : 0;
+            return ((page * A.kv.hkv + K.h) << A.kv.page_shift) + (min(pages_key + 16 * i, (K.len - 1) & ~15) & ((1 << A.kv.page_shift) - 1));
+        };
         uint4 raw[FMT == FMT_BF16 ? 1 : S::LOADS];
         uint32_t raw_scale[FMT == FMT_BF16 ? 1 : S::LOADS];
         float row_scale = 0.0f;
-        // unit x of a thread: keys and then values, whole rows in order
-        auto unit = [&](int x, int &is_v, int &r, int &p) {
-            const int u = x * S::THREADS + threadIdx.x;
-            is_v = u >= S::UNITS;
-            r = (u - is_v * S::UNITS) / S::PER_ROW;
-            p = u % S::PER_ROW;
-            return u < 2 * S::UNITS;
+        // unit x of a lane: the wave's are keys or values, whole rows in order
+        static_assert(S::UNITS % 64 == 0, "");
+        struct Unit {
+            bool there, is_v;
+            int first, r, p;        // the wave's first row; the lane's, and its piece there
         };
-        auto look = [&](int tile) {
-            const int key = K.k0 + min(tile, tiles - 1) * S::KEYS;
-            if constexpr (FMT == FMT_BF16) {
-#pragma unroll
-                for (int x = 0; x < GROUPS; ++x) ahead[x] = cache_row(key + ((x * WAVES + wave) * S::ROWS & ~15));
-            } else {
-#pragma unroll
-                for (int x = 0; x < GROUPS; ++x) {
-                    int is_v, r, p;
-                    unit(x, is_v, r, p);
-                    ahead[x] = cache_row(key + (r & ~15)) + (r & 15);
-                }
-                if constexpr (FMT == FMT_E4M3) ahead_scale = cache_row(key + (threadIdx.x % S::KEYS & ~15)) + (threadIdx.x & 15);
-            }
+        auto unit = [&](int x) {
+            constexpr bool SAME = S::UNITS % S::THREADS == 0, ALL = 2 * S::UNITS % S::THREADS == 0;
+            const int u = (x * WAVES + wave) * 64;
+            const bool is_v = SAME ? x >= S::LOADS / 2 : u >= S::UNITS;
+            const int at = is_v ? u - S::UNITS : u, in = this_lane();
+            return Unit{ALL || u < 2 * S::UNITS, is_v, at / S::PER_ROW, at / S::PER_ROW + in / S::PER_ROW, in % S::PER_ROW};
         };
         // bf16: straight to a stage; else to registers, for put
         auto load = [&](uint8_t *stage) {
             if constexpr (FMT == FMT_BF16) {
-                const int in = wave * S::ROWS % 16 + lane / S::PIECES;         // row in its group
-                const uint32_t k_off = in * S::ROW + (lane % S::PIECES ^ S::k_swizzle(in)) * 16, v_off = in * S::ROW + (lane % S::PIECES ^ S::v_swizzle(in)) * 16;
+                const int ln = this_lane();
 #pragma unroll
                 for (int j = 0; j < PER; ++j) {
                     const bool is_k = j < PER / 2;
                     const int x = j % (PER / 2);
-                    const uint8_t *p = (is_k ? A.kv.k : A.kv.v) + (size_t)__builtin_amdgcn_readfirstlane(ahead[x]) * S::ROW;
-                    __builtin_amdgcn_global_load_lds((global_void *)(p + (is_k ? k_off : v_off)),
+                    const int first = (x * WAVES + wave) * S::ROWS, in = first % 16 + ln / S::PIECES;      // rows of the stage; of its group
+                    const uint32_t off = in * S::ROW + (ln % S::PIECES ^ (is_k ? S::k_swizzle(in) : S::v_swizzle(in))) * 16;
+                    const uint8_t *p = (is_k ? A.kv.k : A.kv.v) + (size_t)group_row(first / 16) * S::ROW;
+                    __builtin_amdgcn_global_load_lds((global_void *)(p + off),
                                                      (lds_void *)(stage + (j * WAVES + wave) * 1024), 16, 0, 0);
                 }
             } else {
 #pragma unroll
                 for (int x = 0; x < S::LOADS; ++x) {
-                    int is_v, r, p;
-                    if (!unit(x, is_v, r, p)) continue;
-                    raw[x] = *reinterpret_cast<const uint4 *>((is_v ? A.kv.v : A.kv.k) + ((size_t)ahead[x] * S::CODES + 16 * p));
-                    if constexpr (FMT == FMT_MXFP4) raw_scale[x] = (is_v ? A.kv.v_exp : A.kv.k_exp)[(size_t)ahead[x] * (D / kMxBlock) + p];
+                    const Unit u = unit(x);
+                    if (!u.there) continue;
+                    // rows of a wave's unit: one group of 16, or two
+                    int row = group_row(u.first / 16);
+                    if constexpr (S::PER_ROW < 4) row = u.r / 16 == u.first / 16 ? row : group_row(u.first / 16 + 1);
+                    const size_t at = row + (u.r & 15);
+                    raw[x] = *reinterpret_cast<const uint4 *>((u.is_v ? A.kv.v : A.kv.k) + (at * S::CODES + 16 * u.p));
+                    if constexpr (FMT == FMT_MXFP4) raw_scale[x] = (u.is_v ? A.kv.v_exp : A.kv.k_exp)[at * (D / kMxBlock) + u.p];
                 }
-                if constexpr (FMT == FMT_E4M3)
-                    if (threadIdx.x < 2 * S::KEYS) row_scale = (threadIdx.x < S::KEYS ? A.kv.k_scale : A.kv.v_scale)[(size_t)ahead_scale];
+                if constexpr (FMT == FMT_E4M3) {        // the first waves: a scale a lane, of the keys and then of the values
+                    if (wave < 2) row_scale = (wave == 0 ? A.kv.k_scale : A.kv.v_scale)[(size_t)group_row(this_lane() % S::KEYS / 16) + (this_lane() & 15)];
+                }
             }
         };
         // rows in registers, to bf16, to a stage
@@ -268,10 +326,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(const AttnArgs A,
             if constexpr (FMT != FMT_BF16) {
 #pragma unroll
                 for (int x = 0; x < S::LOADS; ++x) {
-                    int is_v, r, p;
-                    if (!unit(x, is_v, r, p)) continue;
-                    uint8_t *to = stage + is_v * S::HALF + r * S::ROW;
-                    const int sw = is_v ? S::v_swizzle(r) : S::k_swizzle(r);
+                    __builtin_amdgcn_sched_barrier(0);
+                    const Unit u = unit(x);
+                    if (!u.there) continue;
+                    const int p = u.p;
+                    uint8_t *to = stage + u.is_v * S::HALF + u.r * S::ROW;
+                    const int sw = u.is_v ? S::v_swizzle(u.r) : S::k_swizzle(u.r);
                     const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
                     if constexpr (FMT == FMT_MXFP4) {
                         const float f = mx_scale(raw_scale[x]);
@@ -291,7 +351,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(const AttnArgs A,
                     }
                 }
                 if constexpr (FMT == FMT_E4M3)
-                    if (threadIdx.x < 2 * S::KEYS) scales[threadIdx.x] = row_scale;
+                    if (wave < 2 && this_lane() < S::KEYS) scales[wave * S::KEYS + this_lane()] = row_scale;
             }
         };
 
@@ -302,14 +362,49 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(const AttnArgs A,
             for (int c = 0; c < T; ++c)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[c][e] = 0.0f;
-            const uint8_t *kr = stage + (sub * kSub + n) * S::ROW;
+
+            // Operands are read kAhead steps before the products that take them; the
+            // first ones of the values before the weights are worked out.
+            // piece 2 k + g of row n: 2 k is even, so that it changes bits of its own
+            const int ln = this_lane(), kn = ln & 31;
+            const uint8_t *kr = stage + sub * kSub * S::ROW;
+            const int k_at = kn * S::ROW + ((ln >> 5) ^ S::k_swizzle(kn)) * 16;
+            auto key = [&](int k) { return *reinterpret_cast<const bf8v *>(kr + ((k_at ^ (k & 7) * 32) + (k >> 3) * 256)); };
+            // the operand of channels 32 i .. and keys 16 t + 8 a + 4 g .. + 3 (a < 2),
+            // transposed by the reads: this lane brings 4 channels of one of those keys
+            const int l16 = ln & 15, vr = 4 * (ln >> 5) + (l16 >> 2), cb = ln >> 4 & 1;
+            const uint8_t *vp = stage + S::HALF + sub * kSub * S::ROW;
+            const int v_at = vr * S::ROW + (l16 & 3) * 8 + ((2 * cb) ^ S::v_swizzle(vr)) * 16;
+            auto value = [&](int x) {
+                const int i = x >> 1, t = x & 1, at = (v_at ^ (i & 3) * 64) + (i >> 2) * 256 + 16 * t * S::ROW;
+                const s4v lo = read_transposed(vp + at), hi = read_transposed(vp + (at + 8 * S::ROW));
+                return __builtin_bit_cast(bf8v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            };
+            // (e4m3 rows' scales: asked for ahead where registers are left)
+            constexpr bool EARLY = FMT == FMT_E4M3 && D < 256;
+            float4 ks[4], vs[4];
+            const float *scale_at = scales + sub * kSub + 4 * (ln >> 5);
+            bf8v ring[kAhead + 1];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) ring[k] = key(k);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                if (k % 4 == 0) __builtin_amdgcn_sched_barrier(0);
-                const bf8v a = *reinterpret_cast<const bf8v *>(kr + ((2 * k + g) ^ S::k_swizzle(n)) * 16);
+                if (k + kAhead < KS) ring[(k + kAhead) % (kAhead + 1)] = key(k + kAhead);
+                if constexpr (EARLY)
+                    if (k == KS - kAhead)
 #pragma unroll
-                for (int c = 0; c < T; ++c) acc[c] = mfma32(a, q[c][k], acc[c]);
+                        for (int a = 0; a < 4; ++a) ks[a] = *reinterpret_cast<const float4 *>(scale_at + 8 * a);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int c = 0; c < T; ++c) acc[c] = mfma32(ring[k % (kAhead + 1)], q[c][k], acc[c]);
+                __builtin_amdgcn_sched_barrier(0);
             }
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) ring[x] = value(x);
+            if constexpr (EARLY)
+#pragma unroll
+                for (int a = 0; a < 4; ++a) vs[a] = *reinterpret_cast<const float4 *>(scale_at + S::KEYS + 8 * a);
+            __builtin_amdgcn_sched_barrier(0);
             // lane (n, g) has of column n the keys 8 a + 4 g + b (a, b < 4) of the 32
             bf8v pb[T][2];
 #pragma unroll
@@ -318,20 +413,24 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(const AttnArgs A,
                 if constexpr (FMT == FMT_E4M3) {
 #pragma unroll
                     for (int a = 0; a < 4; ++a) {
-                        const float4 f = *reinterpret_cast<const float4 *>(scales + sub * kSub + 8 * a + 4 * g);
+                        float4 f;
+                        if constexpr (EARLY) {
+                            f = ks[a];
+                        } else {
+                            __builtin_amdgcn_sched_barrier(0);
+                            f = *reinterpret_cast<const float4 *>(scale_at + 8 * a);
+                        }
                         s[4 * a] *= f.x, s[4 * a + 1] *= f.y, s[4 * a + 2] *= f.z, s[4 * a + 3] *= f.w;
                     }
                 }
-                uint32_t vis = 0xffffu;
-                if (tail) {
+                const int from = first + (this_lane() >> 5) * 4 - K.kv;          // the lane's first key's place in the pass
+                auto sees = [&](int e) {
+                    const int at = 8 * (e / 4) + (e & 3), j = from + at;
+                    return WINDOW ? (j < 0) | ((j < kMaxWindowRows) & (seen[c] >> (j & 31))) : at <= row[c] - from;
+                };
+                if (tail)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int j = first + 8 * (e / 4) + 4 * g + (e & 3) - K.kv;      // place in the pass
-                        const bool sees = WINDOW ? (j < 0) | ((j < kMaxWindowRows) & (seen[c] >> (j & 31))) : j <= row[c];
-                        s[e] = sees ? s[e] : -INFINITY;
-                        if constexpr (FMT == FMT_E4M3) vis &= ~((uint32_t)!sees << e);
-                    }
-                }
+                    for (int e = 0; e < 16; ++e) s[e] = sees(e) ? s[e] : -INFINITY;
                 float tm = fmaxf(s[0], s[1]);
 #pragma unroll
                 for (int e = 2; e < 16; ++e) tm = fmaxf(tm, s[e]);
@@ -353,12 +452,18 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(const AttnArgs A,
                 if constexpr (FMT == FMT_E4M3) {
 #pragma unroll
                     for (int a = 0; a < 4; ++a) {
-                        const float4 f = *reinterpret_cast<const float4 *>(scales + S::KEYS + sub * kSub + 8 * a + 4 * g);
+                        float4 f;
+                        if constexpr (EARLY) {
+                            f = vs[a];
+                        } else {
+                            __builtin_amdgcn_sched_barrier(0);
+                            f = *reinterpret_cast<const float4 *>(scale_at + S::KEYS + 8 * a);
+                        }
                         s[4 * a] *= f.x, s[4 * a + 1] *= f.y, s[4 * a + 2] *= f.z, s[4 * a + 3] *= f.w;
                     }
                     if (tail)                  // a masked row's scale may be anything
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) s[e] = vis >> e & 1 ? s[e] : 0.0f;
+                        for (int e = 0; e < 16; ++e) s[e] = sees(e) ? s[e] : 0.0f;
                 }
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -373,21 +478,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(const AttnArgs A,
                         for (int e = 0; e < 16; ++e) o[c][i][e] *= back;
                 }
             }
-            // the operand of channels 32 i .. and keys 16 t + 8 a + 4 g .. + 3 (a < 2),
-            // transposed by the reads: this lane brings 4 channels of one of those keys
-            const int l16 = lane & 15, vr = 4 * g + (l16 >> 2), cb = lane >> 4 & 1;
-            const uint8_t *vp = stage + S::HALF + (sub * kSub + vr) * S::ROW + (l16 & 3) * 8;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
+            for (int x = 0; x < 2 * NT; ++x) {
+                if (x + kAhead < 2 * NT) ring[(x + kAhead) % (kAhead + 1)] = value(x + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int at = ((4 * i + 2 * cb) ^ S::v_swizzle(vr)) * 16 + 16 * t * S::ROW;
-                    const s4v lo = read_transposed(vp + at), hi = read_transposed(vp + at + 8 * S::ROW);
-                    const bf8v v = __builtin_bit_cast(bf8v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-                    for (int c = 0; c < T; ++c) o[c][i] = mfma32(v, pb[c][t], o[c][i]);
-                }
+                for (int c = 0; c < T; ++c) o[c][x >> 1] = mfma32(ring[x % (kAhead + 1)], pb[c][x & 1], o[c][x >> 1]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         };
         auto compute = [&](int tile, const uint8_t *stage, const float *scales) {
@@ -400,13 +497,45 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(const AttnArgs A,
             }
         };
 
+        // The first stage is on its way while the stream's pages are checked: entries
+        // that name no page are taken for page 0 until then.
         look(0);
         load(st0);
         look(1);
+        ok = pages_ok(A, K, S::THREADS) && ok;
+        if (lane == 0) wave_ok[wave] = ok;
+        if (threadIdx.x == 0) {
+            bad = 0;
+            kept = K;
+        }
+        lds_barrier();
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) ok = ok && wave_ok[w];
+        if (!ok) {
+            if (K.nch > 1 && g == 0)
+#pragma unroll
+                for (int c = 0; c < T; ++c)
+                    if (col0 + 32 * c + n < K.cols) A.stat[pair_of(c, A.hq) * A.chunks + K.c] = make_float2(0.0f, kSkipped);
+            wait_vmem();
+            __syncthreads();
+            continue;
+        }
         if constexpr (FMT != FMT_BF16) {
             put(st0, sc0);
             load(nullptr);
             look(2);
+        }
+        // Scores are multiplied by a positive scale: a negative one changes the
+        // queries' signs, 0 makes them 0.
+        if (A.scale <= 0.0f) {
+            const uint32_t sign = A.scale < 0.0f ? 0x80008000u : 0u, keep = A.scale < 0.0f ? ~0u : 0u;
+#pragma unroll
+            for (int c = 0; c < T; ++c)
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const uint4 x = __builtin_bit_cast(uint4, q[c][k]);
+                    q[c][k] = __builtin_bit_cast(bf8v, make_uint4((x.x & keep) ^ sign, (x.y & keep) ^ sign, (x.z & keep) ^ sign, (x.w & keep) ^ sign));
+                }
         }
         auto step = [&](int tile, uint8_t *stage, float *scales, uint8_t *next, float *next_scales) {
             wait_and_meet<0>();
@@ -429,7 +558,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(const AttnArgs A,
                 bool found = false;
 #pragma unroll
                 for (int i = 0; i < S::HALF / 16 / S::THREADS; ++i) {
-                    uint4 *at = reinterpret_cast<uint4 *>(stage + S::HALF) + i * S::THREADS + threadIdx.x, x = *at;
+                    uint4 *at = reinterpret_cast<uint4 *>(stage + S::HALF) + i * S::THREADS + wave * 64 + this_lane(), x = *at;
                     const uint32_t m0 = ((x.x & 0x7f807f80u) + 0x00800080u) & 0x80008000u, m1 = ((x.y & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
                     const uint32_t m2 = ((x.z & 0x7f807f80u) + 0x00800080u) & 0x80008000u, m3 = ((x.w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
                     if (m0 | m1 | m2 | m3) {
@@ -449,67 +578,101 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(const AttnArgs A,
             if (tile + 1 < tiles) step(tile + 1, st1, sc1, st0, sc0);
         }
 
-        const int bad_from = K.k0 + max(0, (all_see - K.k0) / S::KEYS) * S::KEYS;       // the first stage that was looked at
+        // Results leave through LDS, up to 128 channels of a wave's 32 columns at a time, so that the gates' and the results' rows are read and written in runs.
+        // A column's 16-byte pieces are exchanged by its number.
+        __syncthreads();
+        const_args *B = fresh_args();
+        const PromptPiece E = {wave_int(kept.h), wave_int(kept.rt), wave_int(kept.c), wave_int(kept.s), wave_int(kept.r0), wave_int(kept.m),
+                               wave_int(kept.kv), wave_int(kept.len), wave_int(kept.k0), wave_int(kept.k1), wave_int(kept.nch), wave_int(kept.cols)};
+        const uint16_t *const gate_at = B->gate;
+        const int64_t gate_row = B->gate_row, gate_head = B->gate_head;
+        const int first_col = E.rt * S::COLS + wave * 32 * T, hq = B->hq, chunks = B->chunks;
+        constexpr int FIT = S::BYTES / (WAVES / 2 * 32 * 4), CH = FIT < D ? FIT : D, PC = CH / 4, LPC = CH / 8;    // channels; pieces of a column; lanes that read it
+        static_assert(CH >= 32 && D % CH == 0, "");
+        uint8_t *mine = wave < WAVES / 2 ? st0 + wave * (32 * CH * 4) : st1 + (wave - WAVES / 2) * (32 * CH * 4);
+        const int ln = this_lane(), en = ln & 31, eg = ln >> 5;
+        const int sees = WINDOW ? E.kv : E.kv + E.rt * S::COLS / B->group + 1, bad_from = E.k0 + max(0, (sees - E.k0) / S::KEYS) * S::KEYS;       // the first stage that was looked at
 #pragma unroll
         for (int c = 0; c < T; ++c) {
             const float l = sum_halves(sum[c]);
-            if (col0 + 32 * c + n >= K.cols) continue;
-            if (K.nch > 1 && g == 0) A.stat[part_at(c)] = make_float2(mx[c], l);
-            const int r = K.r0 + row[c];
+            if (E.nch > 1 && eg == 0 && first_col + 32 * c + en < E.cols) B->stat[pair_of(c, hq) * chunks + E.c] = make_float2(mx[c], l);
             if (bad) {
-                for (int key = bad_from; key < K.k1; ++key) {
-                    const int j = key - K.kv;
+                for (int key = bad_from; key < E.k1; ++key) {
+                    const int j = key - E.kv;
                     if (j >= 0 && !(WINDOW ? seen[c] >> j & 1 : j <= row[c])) continue;
-                    const size_t at = (size_t)cache_row(key & ~15) + (key & 15);
+                    const int id = B->table[(size_t)E.s * B->max_blocks + (key >> B->kv.page_shift)];
+                    const size_t at = (((size_t)id * B->kv.hkv + E.h) << B->kv.page_shift) + (key & ((1 << B->kv.page_shift) - 1));
 #pragma unroll
                     for (int i = 0; i < NT; ++i)
 #pragma unroll
                         for (int a = 0; a < 4; ++a) {
-                            const uint2 w = cached_values4<D, FMT>(A.kv, at, 32 * i + 8 * a + 4 * g);
+                            const uint2 w = cached_values4<D, FMT>(B->kv.v, B->kv.v_exp, at, 32 * i + 8 * a + 4 * eg);
                             o[c][i][4 * a] += not_finite(w.x << 16), o[c][i][4 * a + 1] += not_finite(w.x & 0xffff0000u);
                             o[c][i][4 * a + 2] += not_finite(w.y << 16), o[c][i][4 * a + 3] += not_finite(w.y & 0xffff0000u);
                             __builtin_amdgcn_sched_barrier(0);
                         }
                 }
             }
-            const float inv = 1.0f / l;
+            const float inv = E.nch == 1 ? 1.0f / l : 1.0f;
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int part = 0; part < D / CH; ++part) {
+                constexpr int RUNS = 32 * LPC / 64;
+                uint2 gate[RUNS][2];
+                if (c + part > 0) __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                    const int d = 32 * i + 8 * a + 4 * g;
-                    const float4 x = make_float4(o[c][i][4 * a], o[c][i][4 * a + 1], o[c][i][4 * a + 2], o[c][i][4 * a + 3]);
-                    if (K.nch == 1)
-                        *reinterpret_cast<uint2 *>(A.out + ((size_t)r * A.hq + head[c]) * D + d) = finish4(A, x, inv, gates4(A, r, head[c], d));
-                    else
-                        *reinterpret_cast<float4 *>(A.part + part_at(c) * D + d) = x;
+                for (int i = 0; i < CH / 32; ++i)
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) {
+                        const f16v &x = o[c][part * (CH / 32) + i];
+                        *reinterpret_cast<float4 *>(mine + (en * PC + ((8 * i + 2 * a + eg) ^ (en & (PC - 1)))) * 16) =
+                            make_float4(x[4 * a] * inv, x[4 * a + 1] * inv, x[4 * a + 2] * inv, x[4 * a + 3] * inv);
+                    }
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int y = 0; y < RUNS; ++y) gate[y][0] = gate[y][1] = make_uint2(0, 0);
+                if (E.nch == 1 && gate_at)
+#pragma unroll
+                    for (int y = 0; y < RUNS; ++y) {
+                        const int2 p = pairs[wave * 32 * T + 32 * c + y * (64 / LPC) + ln / LPC];
+                        const uint16_t *from = gate_at + p.x * gate_row + p.y * gate_head + (part * CH + 8 * (ln % LPC));
+                        gate[y][0] = reinterpret_cast<const uint2 *>(from)[0], gate[y][1] = reinterpret_cast<const uint2 *>(from)[1];
+                    }
+#pragma unroll
+                for (int y = 0; y < RUNS; ++y) {
+                    const int n = y * (64 / LPC) + ln / LPC, x = ln % LPC, d = part * CH + 8 * x;
+                    const float4 u = *reinterpret_cast<const float4 *>(mine + (n * PC + ((2 * x) ^ (n & (PC - 1)))) * 16);
+                    const float4 v = *reinterpret_cast<const float4 *>(mine + (n * PC + ((2 * x + 1) ^ (n & (PC - 1)))) * 16);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (first_col + 32 * c + n >= E.cols) continue;
+                    const int2 p = pairs[wave * 32 * T + 32 * c + n];
+                    const size_t pair = (size_t)p.x * hq + p.y;
+                    if (E.nch == 1) {
+                        const uint2 a = gated4(u, gate_at != nullptr, gate[y][0]), b = gated4(v, gate_at != nullptr, gate[y][1]);
+                        *reinterpret_cast<uint4 *>(B->out + pair * D + d) = make_uint4(a.x, a.y, b.x, b.y);
+                    } else {
+                        float *to = B->part + (pair * chunks + E.c) * D + d;
+                        *reinterpret_cast<float4 *>(to) = u;
+                        *reinterpret_cast<float4 *>(to + 4) = v;
+                    }
                 }
+            }
         }
         __syncthreads();
     }
 }
 
-constexpr int kPromptCols = 256;
-constexpr int kPromptPieces = 512;        // as many as a call is cut into where it has few tiles
-constexpr int kPromptLeastKeys = 512;     // but of no fewer keys
-
-// How many chunks the longest stream of a call with these bounds may have.
-int prompt_chunks(long long tiles, int max_kv)
-{
-    const long long want = tiles >= kPromptPieces / 2 ? 1 : kPromptPieces / at_least(1, (int)tiles);
-    return at_least(1, at_most((int)(want < kMaxChunks ? want : kMaxChunks), max_kv / kPromptLeastKeys));
-}
-
-long long prompt_tiles(int hq, int hkv, int total_rows)
-{
-    return ((long long)total_rows * (hq / hkv) + kPromptCols - 1) / kPromptCols * hkv;
-}
+template <int D, int FMT>
+struct PromptConfig {
+    static constexpr int WAVES = FMT == FMT_BF16 || D == 64 ? 4 : 8, KEYS = FMT == FMT_MXFP4 && D > 64 ? 64 : FMT == FMT_E4M3 && D == 128 ? 64 : 32;
+    static constexpr int PER_SIMD = D == 64 ? (FMT == FMT_E4M3 ? 3 : 4) : D == 128 && FMT == FMT_BF16 ? 3 : 2;
+};
 
 template <int D, int FMT>
 hipError_t launch_prompt_d(const AttnArgs &A, int split_keys, unsigned blocks, hipStream_t stream)
 {
-    if constexpr (D >= 128) prompt_kernel<D, FMT, 8, 1, 64, false><<<blocks, 512, 0, stream>>>(A, split_keys);
-    else prompt_kernel<D, FMT, 4, 2, 64, false><<<blocks, 256, 0, stream>>>(A, split_keys);
+    using P = PromptConfig<D, FMT>;
+    prompt_kernel<D, FMT, P::WAVES, 1, P::KEYS, P::PER_SIMD, false><<<blocks, 64 * P::WAVES, 0, stream>>>(A, split_keys);
     return hipGetLastError();
 }
 
@@ -523,11 +686,59 @@ hipError_t launch_prompt_fmt(const AttnArgs &A, int split_keys, unsigned blocks,
     }
 }
 
-// at most so many pieces
-long long prompt_pieces(const AttnArgs &A, int chunks)
+int prompt_waves(int d, int fmt) { return fmt == FMT_BF16 || d == 64 ? 4 : 8; }
+int prompt_cols(int d, int fmt) { return 32 * prompt_waves(d, fmt); }
+// workgroups that the chip holds at once
+int prompt_slots(int d, int fmt)
 {
-    const long long tiles = (long long)A.total_rows * A.group / kPromptCols + (A.n_streams < A.total_rows ? A.n_streams : A.total_rows);
-    return tiles * A.kv.hkv * chunks;
+    const int per_simd = d == 64 ? (fmt == FMT_E4M3 ? 3 : 4) : d == 128 && fmt == FMT_BF16 ? 3 : 2;
+    return 256 * 4 * per_simd / prompt_waves(d, fmt);
+}
+
+// Chunks of the longest stream: by the time that the call would take, in keys of a
+// workgroup, if its longest stream were the only one.  A workgroup's beginning and
+// end cost as much as 160 keys, a chunk's parts 400 more, and the join 600.  What
+// limits the call is its longest piece, or all of them spread over the chip with
+// half a piece to end on where the pieces are alike, less where the last ones are
+// short; workgroups that have their CU to themselves are faster.  (24 query and 4
+// kv heads of 256: a fresh prompt of 2,048 rows takes 109 us whole and 124 in two
+// chunks, 512 rows over 32,000 cached keys 526 in 12 chunks.)
+constexpr int kPromptRounds = 4;           // pieces of a call that is cut, in workgroups that the chip holds
+int most_chunks(int max_kv) { return at_most(kMaxChunks, max_kv / 256); }
+
+int prompt_chunks(long long tiles, int slots, int total_rows, int max_kv)
+{
+    const double cached = max_kv > total_rows ? max_kv - total_rows : 0, keys = max_kv, mean = (cached + keys) / 2;
+    int best = 1;
+    double least = 0;
+    for (int c = 1; c == 1 || (c <= most_chunks(max_kv) && tiles * c <= (long long)kPromptRounds * slots); ++c) {
+        const double parts = c > 1 ? 1 + (c - 1) * mean / keys : 0;       // of a mean tile
+        const double full = tiles * c < slots ? (double)(tiles * c) / slots : 1.0;
+        const double all = tiles * (mean + 160 + 400 * parts) / slots + (cached / 2 + (keys - cached) / 8) / c;
+        const double one = (keys / c + 160 + (c > 1 ? 400 : 0)) * (0.6 + 0.4 * full);
+        const double cost = (all > one ? all : one) + (c > 1 ? 600 : 0);
+        if (c == 1 || cost < least) best = c, least = cost;
+    }
+    return best;
+}
+
+struct PromptPlan {
+    int chunks, split_keys;
+    long long blocks;
+};
+long long prompt_tiles(int hq, int hkv, int cols, long long total_rows) { return (total_rows * (hq / hkv) + cols - 1) / cols * hkv; }
+PromptPlan prompt_plan(int hq, int hkv, int d, int fmt, int n_streams, int total_rows, int max_kv)
+{
+    const int cols = prompt_cols(d, fmt), rows = n_streams < total_rows ? n_streams : total_rows;
+    PromptPlan P;
+    P.chunks = prompt_chunks(prompt_tiles(hq, hkv, cols, total_rows), prompt_slots(d, fmt), total_rows, max_kv);
+    P.split_keys = ceil_div(ceil_div(max_kv, P.chunks), 64) * 64;
+    P.blocks = ((long long)total_rows * (hq / hkv) / cols + rows) * hkv * P.chunks;       // at most
+    return P;
+}
+size_t part_bytes(int hq, int d, int total_rows, int chunks)
+{
+    return chunks <= 1 ? 0 : (size_t)total_rows * hq * chunks * (sizeof(float) * d + sizeof(float2));
 }
 
 }  // namespace
@@ -536,49 +747,55 @@ hipError_t launch_wide4(const AttnArgs &A, long long pieces, hipStream_t stream)
 {
     const unsigned blocks = (unsigned)(pieces < 2048 ? pieces : 2048);
     switch (A.kv.d) {
-    case 64: prompt_kernel<64, FMT_MXFP4, 4, 1, 32, true><<<blocks, 256, 0, stream>>>(A, 0); break;
-    case 128: prompt_kernel<128, FMT_MXFP4, 4, 1, 32, true><<<blocks, 256, 0, stream>>>(A, 0); break;
-    default: prompt_kernel<256, FMT_MXFP4, 4, 1, 32, true><<<blocks, 256, 0, stream>>>(A, 0); break;
+    case 64: prompt_kernel<64, FMT_MXFP4, 4, 1, 32, 2, true><<<blocks, 256, 0, stream>>>(A, 0); break;
+    case 128: prompt_kernel<128, FMT_MXFP4, 4, 1, 32, 2, true><<<blocks, 256, 0, stream>>>(A, 0); break;
+    default: prompt_kernel<256, FMT_MXFP4, 4, 1, 32, 2, true><<<blocks, 256, 0, stream>>>(A, 0); break;
     }
     return hipGetLastError();
 }
 
-size_t prompt_workspace_bytes(int hq, int hkv, int d, int total_rows, int max_kv, bool or_less)
+size_t prompt_workspace_bytes(int hq, int hkv, int d, int fmt, int n_streams, int total_rows, int max_kv)
 {
-    auto bytes = [&](size_t rows, int chunks) { return chunks <= 1 ? 0 : rows * hq * chunks * (sizeof(float) * d + sizeof(float2)); };
-    const long long all = prompt_tiles(hq, hkv, total_rows);
-    size_t most = bytes(total_rows, prompt_chunks(all, max_kv));
-    if (or_less)        // fewer rows may be cut into more chunks: the most rows of each number of tiles
-        for (long long tiles = hkv; tiles < all && tiles < kPromptPieces / 2; tiles += hkv) {
-            const long long rows = tiles / hkv * kPromptCols / (hq / hkv);
-            const size_t b = bytes(rows < total_rows ? rows : total_rows, prompt_chunks(tiles, max_kv));
-            most = b > most ? b : most;
-        }
-    return most;
+    return part_bytes(hq, d, total_rows, prompt_plan(hq, hkv, d, fmt, n_streams, total_rows, max_kv).chunks);
+}
+
+// Of all calls up to these sizes, in any format: one with fewer rows may be cut into
+// more chunks, but what is cut has kPromptRounds * slots pieces of as many pairs as
+// a tile has columns at most.
+size_t prompt_workspace_most(int hq, int d, int total_rows, int max_kv)
+{
+    const int chunks = most_chunks(max_kv);
+    if (chunks <= 1) return 0;
+    size_t pairs = 0;
+    for (int fmt : {FMT_BF16, FMT_E4M3, FMT_MXFP4}) {
+        const size_t held = (size_t)kPromptRounds * prompt_slots(d, fmt) * prompt_cols(d, fmt);
+        pairs = held > pairs ? held : pairs;
+    }
+    const size_t all = (size_t)total_rows * hq * chunks;
+    return (all < pairs ? all : pairs) * (sizeof(float) * d + sizeof(float2));
 }
 
 bool prompt_fits(const AttnArgs &A)
 {
-    return prompt_pieces(A, prompt_chunks(prompt_tiles(A.hq, A.kv.hkv, A.total_rows), A.max_kv)) <= kMaxGroups / 2
+    return prompt_plan(A.hq, A.kv.hkv, A.kv.d, format_of(A.kv), A.n_streams, A.total_rows, A.max_kv).blocks <= kMaxGroups / 2
            && (long long)A.total_rows * A.hq <= (1 << 26) - 4;
 }
 
 hipError_t launch_prompt(AttnArgs A, void *workspace, hipStream_t stream)
 {
+    const PromptPlan P = prompt_plan(A.hq, A.kv.hkv, A.kv.d, format_of(A.kv), A.n_streams, A.total_rows, A.max_kv);
     A.max_rows = A.total_rows;
-    A.chunks = prompt_chunks(prompt_tiles(A.hq, A.kv.hkv, A.total_rows), A.max_kv);
+    A.chunks = P.chunks;
     A.part = static_cast<float *>(workspace);
     A.stat = reinterpret_cast<float2 *>(A.part + (size_t)A.total_rows * A.hq * A.chunks * A.kv.d);
-    const int split_keys = ceil_div(ceil_div(A.max_kv, A.chunks), 64) * 64;
-    const unsigned blocks = (unsigned)prompt_pieces(A, A.chunks);
     hipError_t rc;
     switch (A.kv.d) {
-    case 64: rc = launch_prompt_fmt<64>(A, split_keys, blocks, stream); break;
-    case 128: rc = launch_prompt_fmt<128>(A, split_keys, blocks, stream); break;
-    default: rc = launch_prompt_fmt<256>(A, split_keys, blocks, stream); break;
+    case 64: rc = launch_prompt_fmt<64>(A, P.split_keys, (unsigned)P.blocks, stream); break;
+    case 128: rc = launch_prompt_fmt<128>(A, P.split_keys, (unsigned)P.blocks, stream); break;
+    default: rc = launch_prompt_fmt<256>(A, P.split_keys, (unsigned)P.blocks, stream); break;
     }
     if (rc != hipSuccess || A.chunks == 1) return rc;
-    return launch_join(A, true, split_keys, stream);
+    return launch_join(A, true, P.split_keys, stream);
 }
 
 }  // namespace gdn
