@@ -68,50 +68,6 @@ struct Run16<true> {
     }
 };
 
-// A lane's share of a key row, in the order in which the steps of the product
-// take it: step s has 8 channels from channel(s, g) on.
-template <int D, int FMT>
-struct KeyRun {
-    static constexpr int STEPS = D / 32;
-    Run16<FMT == FMT_E4M3> r[D / 64];
-    static __device__ __forceinline__ int channel(int s, int g) { return 64 * (s / 2) + 16 * g + 8 * (s & 1); }
-    // from the 16 rows that begin with cache row `row`, its nth
-    __device__ __forceinline__ void load_from_cache(const KvArgs &kv, size_t row, int n, int g)
-    {
-        constexpr int ESZ = FMT == FMT_E4M3 ? 1 : 2;
-        const uint8_t *p = kv.k + row * (D * ESZ);
-        const uint32_t off = n * (D * ESZ) + 16 * g * ESZ;
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k) r[k].load_from_cache(p + (off + 64 * k * ESZ));
-    }
-    __device__ __forceinline__ bf8v get(int s) const { return r[s / 2].get(s & 1); }
-};
-// 4 bits: a block of 32 channels a load (d = 64: half a block)
-template <int D>
-struct KeyRun<D, FMT_MXFP4> {
-    static constexpr int STEPS = D / 32, LOADS = D / 128 > 0 ? D / 128 : 1, W = D == 64 ? 2 : 4, ROW = D / 2, EXPS = D / 32;
-    typedef uint32_t vec_t __attribute__((ext_vector_type(W)));
-    vec_t w[LOADS];
-    uint2 e;
-    int shift;
-    static __device__ __forceinline__ int channel(int s, int g) { return D == 64 ? 16 * g + 8 * s : 128 * (s / 4) + 32 * g + 8 * (s & 3); }
-    __device__ __forceinline__ void load_from_cache(const KvArgs &kv, size_t row, int n, int g)
-    {
-        const uint8_t *p = kv.k + row * ROW, *x = kv.k_exp + row * EXPS;
-#pragma unroll
-        for (int j = 0; j < LOADS; ++j) w[j] = __builtin_nontemporal_load(reinterpret_cast<const vec_t *>(p + (n * ROW + 64 * j + 4 * W * g)));
-        if constexpr (EXPS == 8) e = *reinterpret_cast<const uint2 *>(x + n * 8);
-        else if constexpr (EXPS == 4) e.x = *reinterpret_cast<const uint32_t *>(x + n * 4);
-        else e.x = *reinterpret_cast<const uint16_t *>(x + n * 2);
-        shift = D == 64 ? 8 * (g >> 1) : 8 * g;
-    }
-    __device__ __forceinline__ bf8v get(int s) const
-    {
-        const float f = mx_scale((s < 4 ? e.x : e.y) >> shift & 255);
-        return __builtin_bit_cast(bf8v, mx_values8(w[s / 4][s & 3], f));
-    }
-};
-
 // A lane's share of one value row: NL loads of W dwords each.  Column i of
 // load h is channel h * 16 * EPL + (lane % 16) * EPL + i.
 template <int D, bool F8>
@@ -121,12 +77,6 @@ struct VLayout {
     static constexpr int W = BYTES / NL / 64;           // dwords of a load: 1, 2 or 4
     static constexpr int EPL = W * (F8 ? 4 : 2);
     static constexpr int NT = NL * EPL;                 // tiles of 16 channels of O^T
-};
-
-// 4 bits: one load, of at most two dwords
-template <int D>
-struct VLayout4 {
-    static constexpr int NL = 1, W = 1, EPL = D / 16, NT = D / 16;
 };
 
 template <bool F8, int W>
@@ -180,37 +130,6 @@ struct VPart {
     }
 };
 
-// 4 bits: a lane's D / 16 channels of a row lie in one block
-template <int D>
-struct VPart4 {
-    static constexpr int W = D == 256 ? 2 : 1;
-    uint32_t w[W], e;
-    __device__ __forceinline__ void load_from_cache(const KvArgs &kv, size_t row, int n)
-    {
-        const uint8_t *p = kv.v + row * (D / 2) + n * (D / 32);
-        if constexpr (D == 256) {
-            const auto x = __builtin_nontemporal_load(reinterpret_cast<const uint64_t *>(p));
-            w[0] = (uint32_t)x, w[1] = (uint32_t)(x >> 32);
-        } else if constexpr (D == 128) {
-            w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t *>(p));
-        } else {
-            w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t *>(p));
-        }
-        e = kv.v_exp[row * (D / 32) + n * (D / 32) / 16];
-    }
-    __device__ __forceinline__ bool finite() const { return e <= kMxMost; }
-    __device__ __forceinline__ void zero()
-    {
-#pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = 0;
-        e = 127;
-    }
-    __device__ __forceinline__ void drop_bad()
-    {
-        if (!finite()) zero();
-    }
-};
-
 // The MFMA operand of column i of a load: that channel of the lane's 8 keys.
 template <bool F8, int W>
 __device__ __forceinline__ bf8v v_operand(const VPart<F8, W> (&v)[8], int i)
@@ -234,16 +153,14 @@ __device__ __forceinline__ f4v mfma(bf8v a, bf8v b, f4v c) { return __builtin_am
 // Adds the infinite and NaN values that the products of a chunk's keys [k0, k1)
 // left out to a column's channels d .. d + 3: those of the rows that it sees (of
 // the window, bits of seen) in the tiles that hold rows of the window.
-template <int D, int FMT>
+template <int D, bool F8>
 __device__ void add_bad(const AttnArgs &A, float4 &a, const int *rows16, uint32_t seen, int kv, int k0, int k1, int d)
 {
     for (int key = max(k0, kv & -kTile); key < k1; ++key) {
         if (key >= kv && !(seen >> (key - kv) & 1)) continue;
         const size_t row = (size_t)rows16[(key - k0) >> 4] + (key & 15);
         float v[4];
-        if constexpr (FMT == FMT_MXFP4) {
-            v[0] = v[1] = v[2] = v[3] = A.kv.v_exp[row * (D / kMxBlock) + d / kMxBlock] > kMxMost ? NAN : 0.0f;
-        } else if constexpr (FMT == FMT_E4M3) {
+        if constexpr (F8) {
             const uint32_t x = *reinterpret_cast<const uint32_t *>(A.kv.v + row * D + d);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = (x >> (8 * i) & 0x7fu) == 0x7fu ? NAN : 0.0f;
@@ -395,30 +312,6 @@ __device__ __forceinline__ void add_values(Column<D, F8> &C, int h, const VPart<
     }
 }
 
-// A byte's two channels are converted together, with their row's scale, and then
-// set beside the next row's.
-template <int D>
-__device__ __forceinline__ void add_values(Column<D, false> &C, int, const VPart4<D> (&v)[8], bf8v pb, bf8v rest)
-{
-    float f[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = mx_scale(v[j].e);
-#pragma unroll
-    for (int b = 0; b < D / 32; ++b) {
-        uint32_t x[8], lo[4], hi[4];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = mx_pair(v[j].w[b / 4], f[j], b & 3);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            lo[q] = __builtin_amdgcn_perm(x[2 * q + 1], x[2 * q], 0x05040100u);
-            hi[q] = __builtin_amdgcn_perm(x[2 * q + 1], x[2 * q], 0x07060302u);
-        }
-        const bf8v a = __builtin_bit_cast(bf8v, make_uint4(lo[0], lo[1], lo[2], lo[3])), c = __builtin_bit_cast(bf8v, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        C.o[2 * b] = mfma(a, rest, mfma(a, pb, C.o[2 * b]));
-        C.o[2 * b + 1] = mfma(c, rest, mfma(c, pb, C.o[2 * b + 1]));
-    }
-}
-
 // Values of a tile that holds keys of the window or past the end.  Rows past
 // the end hold anything: zeros instead.  And 0 * inf is NaN: an infinite or NaN
 // value of a window row must not reach the rows that do not see it, so such
@@ -450,13 +343,11 @@ constexpr int kAttnThreads = 256, kAttnWaves = 4;
 // of 1,000 to 16,384 keys (374 MB) take 76 us with the join, 4.9 TB/s; one of
 // 262,143 keys in e4m3 (545 MB) 105 us, 5.2 TB/s.  A short stream is bounded by
 // the chain of layout, page numbers, first tile and join: 8 us for 100 keys.
-template <int D, int FMT>
+template <int D, bool F8>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
 {
-    constexpr bool F8 = FMT == FMT_E4M3, MX = FMT == FMT_MXFP4;
     constexpr int ESZ = F8 ? 1 : 2, ROW = D * ESZ, KS = D / 64;
-    using KR = KeyRun<D, FMT>;
-    using V = typename std::conditional<MX, VLayout4<D>, VLayout<D, F8>>::type;
+    using V = VLayout<D, F8>;
     constexpr int OP = D + 4;                      // padded LDS row of a column's channels
     extern __shared__ __align__(16) uint8_t smem[];
     float *o_lds = reinterpret_cast<float *>(smem);                    // [waves][kCols][OP]
@@ -474,14 +365,14 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
     const int col0 = K.rt * kCols, ncol = min(K.cols - col0, kCols);
     bool ok = chunk_rows(A, K, rows16, kAttnThreads);
     const uint32_t seen = seen_rows(A, K.r0, K.m, min(small_div(col0 + n, A.group), K.m - 1), ok);
-    // the queries, in the order of the lanes' operands: [step][lane] of 16 bytes
-    // (column n, 8 channels from KeyRun's on; zero past the last column)
+    // the queries, in the order of the lanes' operands: [k-step][half][lane] of
+    // 16 bytes (column n, channels 64 k + 16 g + 8 half; zero past the last column)
     for (int i = tid; i < KS * 2 * 64; i += kAttnThreads) {
-        const int qc = i & 15, qg = i >> 4 & 3, step = i >> 6;
+        const int qc = i & 15, qg = i >> 4 & 3, hh = i >> 6 & 1, k = i >> 7;
         uint4 x = {0, 0, 0, 0};
         if (qc < ncol)
             x = *reinterpret_cast<const uint4 *>(A.q + ((size_t)col_row(A, K, col0 + qc) * A.hq + col_head(A, K, col0 + qc)) * D
-                                                 + KR::channel(step, qg));
+                                                 + 64 * k + 16 * qg + 8 * hh);
         q_lds[i] = x;
     }
     static_assert(kAttnWaves == 4, "");
@@ -496,24 +387,25 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
 
     Column<D, F8> C;
     C.clear();
-    KR kk[2];
-    typename std::conditional<MX, VPart4<D>, VPart<F8, V::W>>::type vv[V::NL][8];
-    const uint32_t v_off = 4 * g * ROW + n * V::W * 4;
+    Run16<F8> kk[2][KS];
+    VPart<F8, V::W> vv[V::NL][8];
+    const uint32_t k_off = n * ROW + 16 * g * ESZ, v_off = 4 * g * ROW + n * V::W * 4;
     auto load_k = [&](int tile) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) kk[u].load_from_cache(A.kv, (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]), n, g);
+        for (int u = 0; u < 2; ++u) {
+            const uint8_t *p = A.kv.k + (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]) * ROW;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) kk[u][k].load_from_cache(p + (k_off + 64 * k * ESZ));
+        }
     };
     auto load_v = [&](int tile) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const size_t row = (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]);
-            const uint8_t *p = A.kv.v + row * ROW;
+            const uint8_t *p = A.kv.v + (size_t)__builtin_amdgcn_readfirstlane(rows16[2 * tile + u]) * ROW;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int hh = 0; hh < V::NL; ++hh)
-                    if constexpr (MX) vv[hh][4 * u + j].load_from_cache(A.kv, row + 4 * g + j, n);
-                    else vv[hh][4 * u + j].load_from_cache(p + (v_off + j * ROW + hh * 16 * V::W * 4));
+                for (int hh = 0; hh < V::NL; ++hh) vv[hh][4 * u + j].load_from_cache(p + (v_off + j * ROW + hh * 16 * V::W * 4));
         }
     };
     const int tiles = ceil_div(K.k1 - K.k0, kTile);
@@ -526,11 +418,13 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
         const int key0 = K.k0 + tile * kTile + 4 * g;
         f4v acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-        for (int s = 0; s < KR::STEPS; ++s) {
-            const bf8v q = __builtin_bit_cast(bf8v, q_lds[s * 64 + lane]);
-            acc[0] = mfma(kk[0].get(s), q, acc[0]);
-            acc[1] = mfma(kk[1].get(s), q, acc[1]);
-        }
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const bf8v q = __builtin_bit_cast(bf8v, q_lds[(2 * k + hh) * 64 + lane]);
+                acc[0] = mfma(kk[0][k].get(hh), q, acc[0]);
+                acc[1] = mfma(kk[1][k].get(hh), q, acc[1]);
+            }
         if (more) load_k(tile + kAttnWaves);
         float4 ks[2] = {}, vs[2] = {};
         if constexpr (F8)
@@ -592,7 +486,296 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
             l += l_lds[w * kCols + cc];
             mm = fmaxf(mm, m_lds[w * kCols + cc]);
         }
-        if (*bad_lds) add_bad<D, FMT>(A, a, rows16, seen_lds[cc], K.kv, K.k0, K.k1, d);
+        if (*bad_lds) add_bad<D, F8>(A, a, rows16, seen_lds[cc], K.kv, K.k0, K.k1, d);
+        put4<D>(A, K, col0 + cc, a, l, d);
+        if (K.nch > 1 && d == 0) A.stat[col_part(A, K, col0 + cc)] = make_float2(mm, l);
+    }
+}
+
+// ---- up to 16 columns, 4-bit rows ------------------------------------------------
+
+// The same over 4-bit rows.  A tile of 32 keys is a quarter of the bytes, so a
+// chunk ends after a few of them, and what counts is how soon they are all on their
+// way: each wave keeps its next two tiles in flight, by direct loads into a ring of
+// its own in LDS (16 bytes a lane, no registers, no barriers).  Codes
+// are converted as they are used: K in blocks of 32 channels, whose exponent is the
+// conversion's scale; of V a byte's two channels at once, then set beside the next
+// key's.  Two workgroups a CU (LDS).
+// A direct load into LDS, 16 bytes a lane, lane after lane from byte `to` on (at is
+// the wave's, off the lane's).  The compiler is not told what it is: it would wait
+// for all of a ring's loads before the first read, where the kernel waits itself
+// (the counter that its own waits go by counts these loads, too, so that they come
+// no earlier).
+__device__ __forceinline__ uint32_t lds_at(const uint8_t *p) { return (uint32_t)(uintptr_t)(lds_void *)p; }
+__device__ __forceinline__ void load_to_lds(const uint8_t *at, uint32_t off, uint32_t to)
+{
+    const uint64_t a = reinterpret_cast<uint64_t>(at);
+    const uint64_t sa = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0 nt" ::"s"(sa), "v"(off), "s"(to) : "memory");
+}
+
+template <int D>
+struct Tile4 {
+    static constexpr int ROW = D / 2, EXPS = D / 32, CODES = 32 * ROW;       // bytes of a row, of its exponents, of the tile's keys
+    static constexpr int BYTES = 2 * CODES + 64 * EXPS, LOADS = 2 * (CODES / 1024) + 1;     // a tile in LDS: K, V, exponents of both
+    // 16-byte pieces of a row are exchanged, so that 16 rows lie in different banks
+    static __device__ __forceinline__ int swizzle(int r) { return D == 256 ? r >> 1 & 7 : D == 128 ? r >> 2 & 3 : r >> 3 & 1; }
+    static constexpr int VB = D / 32;                       // bytes of a lane's channels of a value row
+
+    // row0, row1: cache rows of the tile's two groups of 16 keys
+    static __device__ __forceinline__ void load(const KvArgs &kv, uint32_t to, size_t row0, size_t row1, int lane)
+    {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const uint8_t *pool = x ? kv.v : kv.k;
+#pragma unroll
+            for (int i = 0; i < CODES / 1024; ++i) {
+                const int b = i * 1024 + lane * 16, r = b / ROW, piece = b % ROW / 16 ^ swizzle(r), off = (r & 15) * ROW + piece * 16;
+                if constexpr (CODES == 1024) {              // both groups in one load: the second from the first one's address
+                    const int64_t apart = (int64_t)(row1 - row0) * ROW;
+                    const uint8_t *p = pool + row0 * ROW + (r < 16 ? 0 : apart) + off;
+                    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(p), "s"(to + x * CODES) : "memory");
+                } else {
+                    load_to_lds(pool + (i * 1024 / ROW < 16 ? row0 : row1) * ROW, off, to + x * CODES + i * 1024);
+                }
+            }
+        }
+        constexpr int LE = 2 * EXPS;                        // lanes that bring a pool's exponents
+        if (lane < 2 * LE) {
+            const int b = lane % LE * 16;
+            const uint8_t *p = (lane < LE ? kv.k_exp : kv.v_exp) + (b < 16 * EXPS ? row0 * EXPS + b : row1 * EXPS + (b - 16 * EXPS));
+            asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(to + 2 * CODES) : "memory");
+        }
+    }
+    // steps of the product S^T = K Q^T: step s has 8 channels from channel(s, g) on
+    static constexpr int STEPS = D / 32;
+    static __device__ __forceinline__ int channel(int s, int g) { return D == 64 ? 16 * g + 8 * s : 128 * (s / 4) + 32 * g + 8 * (s & 3); }
+};
+
+// The keys of a lane's row, and its channels' values of 8 rows, as they lie in LDS
+template <int D>
+struct Keys4 {
+    using S = Tile4<D>;
+    static constexpr int W = D == 64 ? 2 : 4, N = D == 256 ? 2 : 1;
+    uint32_t w[N][W];
+    float f[N];
+    __device__ __forceinline__ void read(const uint8_t *tile, int r, int g)
+    {
+        const uint8_t *p = tile + r * S::ROW, *x = tile + 2 * S::CODES + r * S::EXPS;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int piece = (D == 64 ? g >> 1 : 4 * j + g) ^ S::swizzle(r);
+            if constexpr (D == 64) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(p + piece * 16 + (g & 1) * 8);
+                w[j][0] = v.x, w[j][1] = v.y;
+            } else {
+                const uint4 v = *reinterpret_cast<const uint4 *>(p + piece * 16);
+                w[j][0] = v.x, w[j][1] = v.y, w[j][2] = v.z, w[j][3] = v.w;
+            }
+            f[j] = mx_scale(x[D == 64 ? g >> 1 : 4 * j + g]);
+        }
+    }
+    __device__ __forceinline__ bf8v get(int s) const { return __builtin_bit_cast(bf8v, mx_values8(w[s / 4][s % W], f[s / 4])); }
+};
+template <int D>
+struct Values4 {
+    using S = Tile4<D>;
+    static constexpr int W = D == 256 ? 2 : 1;
+    uint32_t w[W], e;
+    __device__ __forceinline__ void read(const uint8_t *tile, int r, int n)
+    {
+        const uint8_t *p = tile + S::CODES + r * S::ROW + (n * S::VB / 16 ^ S::swizzle(r)) * 16 + n * S::VB % 16;
+        if constexpr (D == 256) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x, w[1] = v.y;
+        } else if constexpr (D == 128) {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            w[0] = *reinterpret_cast<const uint16_t *>(p);
+        }
+        e = tile[2 * S::CODES + 32 * S::EXPS + r * S::EXPS + n * S::VB / 16];
+    }
+    __device__ __forceinline__ bool finite() const { return e <= kMxMost; }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+        e = 127;
+    }
+    __device__ __forceinline__ void drop_bad()
+    {
+        if (!finite()) zero();
+    }
+};
+
+// O^T += V^T P^T, P as the sum of its two parts: channel n * D / 16 + i is column i
+template <int D>
+__device__ __forceinline__ void add_values4(Column<D, false> &C, const Values4<D> (&v)[8], bf8v pb, bf8v rest)
+{
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = mx_scale(v[j].e);
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) {
+        uint32_t x[8], lo[4], hi[4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = mx_pair(v[j].w[b / 4], f[j], b & 3);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            lo[q] = __builtin_amdgcn_perm(x[2 * q + 1], x[2 * q], 0x05040100u);
+            hi[q] = __builtin_amdgcn_perm(x[2 * q + 1], x[2 * q], 0x07060302u);
+        }
+        const bf8v a = __builtin_bit_cast(bf8v, make_uint4(lo[0], lo[1], lo[2], lo[3])), c = __builtin_bit_cast(bf8v, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        C.o[2 * b] = mfma(a, rest, mfma(a, pb, C.o[2 * b]));
+        C.o[2 * b + 1] = mfma(c, rest, mfma(c, pb, C.o[2 * b + 1]));
+    }
+}
+
+
+constexpr int kWaves4 = 4, kThreads4 = 64 * kWaves4;
+
+template <int D>
+__global__ __launch_bounds__(kThreads4, 2) void attn4_kernel(const AttnArgs A)
+{
+    using S = Tile4<D>;
+    using C4 = Column<D, false>;
+    constexpr int OP = D + 4, EPL = D / 16;
+    // each wave's next tiles; afterwards their O
+    __shared__ __align__(1024) uint8_t ring0[kWaves4 * S::BYTES], ring1[kWaves4 * S::BYTES];
+    __shared__ __align__(16) uint4 q_lds[S::STEPS * 64];
+    __shared__ float m_lds[kWaves4 * kCols], l_lds[kWaves4 * kCols];
+    __shared__ uint32_t seen_lds[kCols];
+    __shared__ int ok_lds[kWaves4], bad_lds;
+    static_assert(2 * kCols * OP * 4 <= sizeof(ring0), "");
+
+    Pieces pieces;
+    Chunk K;
+    if (!pieces.find_in_block(A, false, kCols, 64 * blockIdx.y, blockIdx.x, K)) return;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, n = lane & 15, g = lane >> 4;
+    const int col0 = K.rt * kCols, ncol = min(K.cols - col0, kCols), tiles = ceil_div(K.k1 - K.k0, kTile);
+    const int *table = A.table + (size_t)K.s * A.max_blocks;
+    // cache row of a key's group of 16: past the stream's end that of its last keys,
+    // and in place of a page outside the cache page 0's
+    auto group_row = [&](int key) -> size_t {
+        key = min(key, (K.len - 1) & ~15);
+        const int id = table_entry(table, key >> A.kv.page_shift);
+        return ((((uint32_t)id < (uint32_t)A.kv.n_pages ? id : 0) * A.kv.hkv + K.h) << A.kv.page_shift) + (key & ((1 << A.kv.page_shift) - 1));
+    };
+    auto issue = [&](int tile, uint8_t *ring) {
+        const int key = K.k0 + tile * kTile;
+        S::load(A.kv, __builtin_amdgcn_readfirstlane(lds_at(ring)) + wave * S::BYTES, group_row(key), group_row(key + 16), lane);
+    };
+    // the chunk's pages
+    bool ok = true;
+    for (int i = (K.k0 >> A.kv.page_shift) + tid; i <= (K.k1 - 1) >> A.kv.page_shift; i += kThreads4) {
+        const int id = table[i];
+        ok = ok && id >= 0 && id < A.kv.n_pages;
+    }
+    ok = !__ballot(!ok);
+    const uint32_t seen = seen_rows(A, K.r0, K.m, min(small_div(col0 + n, A.group), K.m - 1), ok);
+    // the queries, in the order of the lanes' operands (zero past the last column)
+    for (int i = tid; i < S::STEPS * 64; i += kThreads4) {
+        const int qc = i & 15, qg = i >> 4 & 3, s = i >> 6;
+        uint4 x = {0, 0, 0, 0};
+        if (qc < ncol)
+            x = *reinterpret_cast<const uint4 *>(A.q + ((size_t)col_row(A, K, col0 + qc) * A.hq + col_head(A, K, col0 + qc)) * D + S::channel(s, qg));
+        q_lds[i] = x;
+    }
+    if (lane == 0) ok_lds[wave] = ok;
+    if (tid == 0) bad_lds = 0;
+    if (tid < kCols) seen_lds[tid] = seen;
+    // (the waits for what came before are over, and none of them waits for these)
+    if (wave < tiles) issue(wave, ring0);
+    if (wave + kWaves4 < tiles) issue(wave + kWaves4, ring1);
+    lds_barrier();
+
+    C4 C;
+    C.clear();
+    auto step = [&](int tile, uint8_t *ring) {
+        // this tile is there when no more than the next one's loads are left
+        asm volatile("" ::: "memory");
+        if (tile + kWaves4 < tiles) __builtin_amdgcn_s_waitcnt(0x0F70 | (S::LOADS & 15) | (S::LOADS >> 4) << 14);
+        else __builtin_amdgcn_s_waitcnt(0x0F70);
+        asm volatile("" ::: "memory");
+        const uint8_t *at = ring + wave * S::BYTES;
+        const int key0 = K.k0 + tile * kTile + 4 * g;
+        f4v acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        Keys4<D> kk[2];
+        kk[0].read(at, n, g);
+        kk[1].read(at, 16 + n, g);
+        Values4<D> v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i].read(at, 4 * g + (i & 3) + 16 * (i / 4), n);
+#pragma unroll
+        for (int s = 0; s < S::STEPS; ++s) {
+            const bf8v q = __builtin_bit_cast(bf8v, q_lds[s * 64 + lane]);
+            acc[0] = mfma(kk[0].get(s), q, acc[0]);
+            acc[1] = mfma(kk[1].get(s), q, acc[1]);
+        }
+        const float4 none[2] = {};
+        bf8v pb, rest;
+        if (K.k0 + tile * kTile + kTile <= K.kv) {
+            pb = C.template weights<false, true>(acc, A.scale, none, none, key0, K.kv, seen, rest);
+        } else {
+            pb = C.template weights<true, true>(acc, A.scale, none, none, key0, K.kv, seen, rest);
+            if (clean_values(v, key0, K.len, K.m) && lane == 0) bad_lds = 1;
+        }
+        // the tile's LDS has been read: the ring takes the tile after the next
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+        asm volatile("" ::: "memory");
+        if (tile + 2 * kWaves4 < tiles) issue(tile + 2 * kWaves4, ring);
+        add_values4(C, v, pb, rest);
+    };
+    for (int tile = wave; tile < tiles; tile += 2 * kWaves4) {
+        step(tile, ring0);
+        if (tile + kWaves4 < tiles) step(tile + kWaves4, ring1);
+    }
+
+    // join the waves: the column's maximum over them, each wave's O and l scaled to it
+    const float sum = sum_rows4(C.sum);
+    if (g == 0) m_lds[wave * kCols + n] = C.mx;
+    lds_barrier();
+    ok = ok_lds[0] && ok_lds[1] && ok_lds[2] && ok_lds[3];
+    static_assert(kWaves4 == 4, "");
+    if (!ok) {
+        if (K.nch > 1 && tid < ncol) A.stat[col_part(A, K, col0 + tid)] = make_float2(0.0f, kSkipped);
+        return;
+    }
+    auto o_at = [&](int w, int c) { return reinterpret_cast<float *>(w < 2 ? ring0 : ring1) + ((w & 1) * kCols + c) * OP; };
+    float top = m_lds[n];
+#pragma unroll
+    for (int w = 1; w < kWaves4; ++w) top = fmaxf(top, m_lds[w * kCols + n]);
+    const float f = __builtin_amdgcn_exp2f(C.mx - (top == -INFINITY ? 0.0f : top));
+    if (g == 0) l_lds[wave * kCols + n] = sum * f;
+    if (n < ncol) {
+        float *row = o_at(wave, n);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float *p = row + (4 * g + e) * EPL;
+#pragma unroll
+            for (int i = 0; i < EPL; i += 4)
+                *reinterpret_cast<float4 *>(p + i) = make_float4(C.o[i][e] * f, C.o[i + 1][e] * f, C.o[i + 2][e] * f, C.o[i + 3][e] * f);
+        }
+    }
+    lds_barrier();
+    for (int i = tid; i < ncol * (D / 4); i += kThreads4) {
+        const int cc = i / (D / 4), d = 4 * (i % (D / 4));
+        float4 a = *reinterpret_cast<const float4 *>(o_at(0, cc) + d);
+        float l = l_lds[cc], mm = m_lds[cc];
+#pragma unroll
+        for (int w = 1; w < kWaves4; ++w) {
+            const float4 b = *reinterpret_cast<const float4 *>(o_at(w, cc) + d);
+            a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+            l += l_lds[w * kCols + cc];
+            mm = fmaxf(mm, m_lds[w * kCols + cc]);
+        }
+        if (bad_lds)            // blocks of NaN that the products left out, to the columns that see them
+            for (int key = max(K.k0, K.kv & -kTile); key < K.k1; ++key) {
+                if (key >= K.kv && !(seen_lds[cc] >> (key - K.kv) & 1)) continue;
+                const size_t row = (((size_t)table[key >> A.kv.page_shift] * A.kv.hkv + K.h) << A.kv.page_shift) + (key & ((1 << A.kv.page_shift) - 1));
+                if (A.kv.v_exp[row * (D / kMxBlock) + d / kMxBlock] > kMxMost) a = make_float4(NAN, NAN, NAN, NAN);
+            }
         put4<D>(A, K, col0 + cc, a, l, d);
         if (K.nch > 1 && d == 0) A.stat[col_part(A, K, col0 + cc)] = make_float2(mm, l);
     }
@@ -917,7 +1100,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
             if (K.nch > 1 && eg == 0) A.stat[col_part(A, K, col)] = ok ? make_float2(C[c].mx, l) : make_float2(0.0f, kSkipped);
             if (!ok) continue;
             auto put = [&](float4 a, int d) {
-                if (bad) add_bad<D, F8 ? FMT_E4M3 : FMT_BF16>(A, a, rows16 + list, seen[c], K.kv, K.k0, K.k1, d);
+                if (bad) add_bad<D, F8>(A, a, rows16 + list, seen[c], K.kv, K.k0, K.k1, d);
                 put4<D>(A, K, col, a, l, d);
             };
 #pragma unroll
@@ -1051,7 +1234,9 @@ hipError_t launch_d(const AttnArgs &A, bool wide, long long pieces, hipStream_t 
         constexpr size_t lds = sizeof(float) * kAttnWaves * kCols * (D + 4 + 2) + D * 2 * kCols + sizeof(int) * (4 + kCols);
         // 64 streams a grid row
         const unsigned per_row = (unsigned)(pieces / A.n_streams * (A.n_streams < 64 ? A.n_streams : 64));
-        hipLaunchKernelGGL((attn_kernel<D, FMT>), dim3(per_row, ceil_div(A.n_streams, 64)), dim3(kAttnThreads), lds + list_bytes, stream, A);
+        const dim3 grid(per_row, ceil_div(A.n_streams, 64));
+        if constexpr (FMT == FMT_MXFP4) attn4_kernel<D><<<grid, kThreads4, 0, stream>>>(A);
+        else hipLaunchKernelGGL((attn_kernel<D, FMT == FMT_E4M3>), grid, dim3(kAttnThreads), lds + list_bytes, stream, A);
     } else if constexpr (FMT == FMT_MXFP4) {
         const hipError_t rc = launch_wide4(A, pieces, stream);
         if (rc != hipSuccess) return rc;

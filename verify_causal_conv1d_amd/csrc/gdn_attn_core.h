@@ -251,6 +251,11 @@ __device__ __forceinline__ bool chunk_rows(const AttnArgs &A, const Chunk &K, in
     return !__ballot(!ok);
 }
 
+// Entries of the block table, which nothing writes while the kernel runs, through
+// the scalar cache: their addresses are the wave's.
+typedef const __attribute__((address_space(4))) int const_int;
+__device__ __forceinline__ int table_entry(const int *table, int i) { return ((const_int *)table)[i]; }
+
 // Packed row and query head of a stream's column.
 __device__ __forceinline__ int col_row(const AttnArgs &A, const Chunk &K, int col) { return K.r0 + small_div(col, A.group); }
 __device__ __forceinline__ int col_head(const AttnArgs &A, const Chunk &K, int col) { return K.h * A.group + col - small_div(col, A.group) * A.group; }

@@ -221,78 +221,198 @@ __device__ __forceinline__ float max_group(float x)
 // A key head's values once more, in fp64 from its bf16 channels up to the last
 // rounding: norm, then rotation.  For all lanes of a wave; those of other heads
 // keep what they have.
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double x)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 template <int LANES>
 __device__ __forceinline__ double sum_group(double x)
 {
-#pragma unroll
-    for (int o = 1; o < LANES; o <<= 1) x += __shfl_xor(x, o);
+    x += dpp_f64<0xB1>(x);
+    x += dpp_f64<0x4E>(x);
+    x += dpp_f64<0x141>(x);
+    if (LANES > 8) x += dpp_f64<0x140>(x);
+    if (LANES > 16) x += __shfl_xor(x, 16);
     return x;
 }
+
+// 1 / sqrt(a), a > 0: the instruction's estimate (2^-22 or better) and two steps of
+// Newton's method; 0 of infinity
+__device__ __forceinline__ double rsqrt_f64(double a)
+{
+    const double r0 = __builtin_amdgcn_rsq(a);
+    double r = r0 * fma(-0.5 * a * r0, r0, 1.5);
+    r = r * fma(-0.5 * a * r, r, 1.5);
+    return a < INFINITY ? r : r0;
+}
+
+// cos and sin of 2 pi turns, |turns| <= 0.5, to 2^-45: quarter turns off, then the
+// Taylor series on [-pi / 4, pi / 4] (their next terms are below 2^-45)
+__device__ __forceinline__ void cos_sin_f64(double turns, double &c, double &s)
+{
+    const double q = rint(4.0 * turns), r = (turns - 0.25 * q) * 6.28318530717958647693, z = r * r;
+    const double sn = r * fma(z, fma(z, fma(z, fma(z, fma(z, fma(z, 1.0 / 6227020800.0, -1.0 / 39916800.0), 1.0 / 362880.0), -1.0 / 5040.0), 1.0 / 120.0), -1.0 / 6.0), 1.0);
+    const double cn = fma(z, fma(z, fma(z, fma(z, fma(z, fma(z, fma(z, -1.0 / 87178291200.0, 1.0 / 479001600.0), -1.0 / 3628800.0), 1.0 / 40320.0), -1.0 / 720.0), 1.0 / 24.0), -0.5), 1.0);
+    const int n = (int)q;
+    c = n & 1 ? (n & 2 ? sn : -sn) : (n & 2 ? -cn : cn);
+    s = n & 1 ? (n & 2 ? -cn : cn) : (n & 2 ? -sn : sn);
+}
+
+// cos and sin of a position's ith angle, times the rotation's scale.  The angle is
+// exact in fp64, and so, up to 2^-52 of a turn, is what whole turns leave of it.
+__device__ __forceinline__ void turn_f64(const PrepArgs &A, int pos, int i, double &c, double &s)
+{
+    const double angle = (double)pos * (double)A.inv_freq[i], n = rint(angle * 0.15915494309189533577);
+    const double rest = fma(-n, 2.4492935982947064e-16, fma(-n, 6.28318530717958647693, angle));
+    cos_sin_f64(rest * 0.15915494309189533577, c, s);
+    c *= (double)A.rot_scale;
+    s *= (double)A.rot_scale;
+}
+
+// A lane's 8 channels of a row, quantised with the other three lanes of their block
+// of 32 (all lanes of a wave call it), and stored
+template <int D>
+__device__ __forceinline__ void put_block(const float (&x)[8], int lane, bool store, uint8_t *pool, uint8_t *exps, size_t row)
+{
+    uint32_t top = 0;               // of the bits: a NaN is above infinity
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, false));
+    top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, false));
+    if (!store) return;
+    const bool fin = top < 0x7f800000u;
+    const int e = fin ? min(max((int)((top + (1u << 21)) >> 23) - 2, kMxLeast), kMxMost) : kMxNan;
+    const float to = __uint_as_float((uint32_t)(254 - e) << 23);         // 2^(127 - e)
+    uint32_t codes = 0;
+    if (fin) {
+        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, x[0] * to, x[1] * to, 1.0f, 0);
+        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, x[2] * to, x[3] * to, 1.0f, 1);
+        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, x[4] * to, x[5] * to, 1.0f, 2);
+        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, x[6] * to, x[7] * to, 1.0f, 3);
+    }
+    *reinterpret_cast<uint32_t *>(pool + row * (D / 2) + 4 * lane) = codes;
+    if (lane % 4 == 0) exps[row * (D / kMxBlock) + lane / 4] = (uint8_t)e;
+}
+
+// A key head's values in fp64 from its bf16 channels up to the last rounding: norm,
+// then rotation.  row: the head's LDS; weight: the norm's, there.
 template <int D, int LANES>
-__device__ __forceinline__ void exact_key(const PrepArgs &A, uint4 raw, int lane, bool is_k, float *row, const double *cs, const double *sn,
-                                          float (&x)[8])
+__device__ __forceinline__ void exact_key(const PrepArgs &A, uint4 raw, int lane, double *row, const double *weight, const double *cs,
+                                          const double *sn, float (&x)[8])
 {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        y[2 * i] = __uint_as_float(w[i] << 16);
-        y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
     double inv = 1.0;
     if (A.k_norm) {
         double ss = 0.0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fma((double)y[i], (double)y[i], ss);
-        inv = 1.0 / sqrt(sum_group<LANES>(ss) * (1.0 / D) + (double)A.eps);
+        for (int i = 0; i < 4; ++i) {
+            const double a = (double)__uint_as_float(w[i] << 16), b = (double)__uint_as_float(w[i] & 0xffff0000u);
+            ss = fma(b, b, fma(a, a, ss));
+        }
+        inv = rsqrt_f64(sum_group<LANES>(ss) * (1.0 / D) + (double)A.eps);
+    }
+    // the head's normed channels change lanes through LDS, within the wave
+    double z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        z[i] = (double)__uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) * (inv * weight[8 * lane + i]);
+        if (8 * lane < A.rot) row[8 * lane + i] = z[i];
     }
     __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) row[8 * lane + i] = y[i];
-    __builtin_amdgcn_wave_barrier();
-    const int half = A.rot / 2;
-    if (is_k)
+    if (8 * lane < A.rot) {
+        const int half = A.rot / 2;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int e = 8 * lane + i;
-            auto normed = [&](int c) { return (double)row[c] * inv * (A.k_norm ? (double)A.k_norm[c] : 1.0); };
-            double z = normed(e);
-            if (e < 2 * half) {
+            if (e < A.rot) {
                 const bool second = A.interleaved ? e & 1 : e >= half;
                 const int p = A.interleaved ? e >> 1 : second ? e - half : e;
-                const double other = normed(A.interleaved ? e ^ 1 : second ? e - half : e + half);
-                z = second ? fma(z, cs[p], other * sn[p]) : fma(z, cs[p], -(other * sn[p]));
+                const double other = row[A.interleaved ? e ^ 1 : second ? e - half : e + half] * sn[p];
+                z[i] = fma(z[i], cs[p], second ? other : -other);
             }
-            x[i] = (float)z;
         }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (float)z[i];
     __builtin_amdgcn_wave_barrier();
+}
+
+// A workgroup's keys of many rows into a 4-bit cache: (row, kv head) pairs in order,
+// as many as its lanes hold.
+// (rows that n pairs in order belong to, at most)
+__host__ __device__ inline int key_rows(int n, int hkv) { return (n - 1) / hkv + 2 < n ? (n - 1) / hkv + 2 : n; }
+
+template <int D>
+__device__ __forceinline__ void prep_keys(const PrepArgs &A, const int block, double *lds64)
+{
+    constexpr int LANES = D / 8, HEADS = kPrepThreads / LANES;
+    const int tid = threadIdx.x, lane = tid % LANES, grp = tid / LANES, hkv = A.kv.hkv, half = A.rot / 2;
+    double *weight = lds64, *swap = weight + D, *cs64 = swap + HEADS * A.rot, *sn64 = cs64 + key_rows(HEADS, hkv) * half;
+    const long long first = (long long)block * HEADS, pairs = (long long)A.rows * hkv, pair = first + grp;
+    const int row0 = (int)(first / hkv), r = (int)(min(pair, pairs - 1) / hkv), h = (int)(pair - (long long)r * hkv);
+    const bool there = pair < pairs;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (there) raw = load_once(A.k + (r * A.k_row + h * A.k_head + 8 * lane));
+    const int slot = there ? A.slots[r] : -1, page = slot >> A.kv.page_shift;
+    const int rows = (int)(min(first + HEADS, pairs) - 1) / hkv - row0 + 1;
+    for (int i = tid; i < rows * half; i += kPrepThreads) turn_f64(A, A.positions[row0 + i / half], i % half, cs64[i], sn64[i]);
+    if (tid < D) weight[tid] = A.k_norm ? (double)A.k_norm[tid] : 1.0;
+    lds_barrier();
+    float x[8];
+    exact_key<D, LANES>(A, raw, lane, swap + grp * A.rot, weight, cs64 + (r - row0) * half, sn64 + (r - row0) * half, x);
+    const size_t at = (((size_t)page * hkv + h) << A.kv.page_shift) + (slot & ((1 << A.kv.page_shift) - 1));
+    put_block<D>(x, lane, there && slot >= 0 && page < A.kv.n_pages, A.kv.k, A.kv.k_exp, at);
 }
 
 // The rows pass through once, and what is stored is read by other kernels on
 // whichever XCD: load_once and store_once (the prompt pass of 8,306 rows takes
 // 62 us with them and 68 us without).
 //
-// Into a 4-bit cache (MX) a key's norm and rotation are taken in fp64 up to the
-// fp32 value that is quantised: that close to a border between two codes or two
-// scales fp32 sums would decide by the order of their terms.  Only the key heads
-// need it, and memory stays the bound.
-template <int D, bool MX>
-__global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, const int span)
+// Into a 4-bit cache a key's norm and rotation are taken in fp64 up to the fp32 value
+// that is quantised: that close to a border between two codes or two scales fp32
+// sums would decide by the order of their terms.  Where the rows are few a
+// workgroup does its row's keys last (PREP_MX); else workgroups of their own, spread
+// among the others, do them (PREP_MX_APART: 8,306 rows 73 us, in the rows' own
+// workgroups 88, in a launch after theirs 75).
+enum { PREP_ROWS = 0, PREP_MX = 1, PREP_MX_APART = 2 };
+
+template <int D, int MODE>
+__global__ __launch_bounds__(kPrepThreads, MODE == PREP_MX_APART ? 8 : 1) void prep_kernel(const PrepArgs A, const int span)
 {
+    constexpr bool MX = MODE != PREP_ROWS, KEYS = MODE == PREP_MX;
     constexpr int LANES = D / 8, HEADS = kPrepThreads / LANES;   // heads a workgroup handles at once
     constexpr int BATCH = 4;                                     // and loads ahead
     // this workgroup's heads: span of them from span * blockIdx.y
     __shared__ float cs[kPrepMaxHalf], sn[kPrepMaxHalf];
     __shared__ __align__(16) float swap[HEADS][D];
-    __shared__ double cs64[MX ? kPrepMaxHalf : 1], sn64[MX ? kPrepMaxHalf : 1];
-    const int r = blockIdx.x, tid = threadIdx.x, lane = tid % LANES, grp = tid / LANES;
+    __shared__ double cs64[KEYS ? kPrepMaxHalf : 1], sn64[KEYS ? kPrepMaxHalf : 1];
+    __shared__ double weight[KEYS ? D : 1], swap64[KEYS ? HEADS : 1][D];     // of the keys' norm; their lanes' exchange
+    int r = blockIdx.x;
+    if constexpr (MODE == PREP_MX_APART) {
+        // of gridDim.x workgroups A.rows have a row, as evenly spread as can be
+        extern __shared__ double lds64[];
+        const long long all = gridDim.x, keys = all - A.rows, before = r * keys / all;
+        if ((r + 1) * keys / all > before) {
+            prep_keys<D>(A, (int)before, lds64);
+            return;
+        }
+        r -= (int)before;
+    }
+    const int tid = threadIdx.x, lane = tid % LANES, grp = tid / LANES;
     const int half = A.rot / 2, hkv = A.kv.hkv, first = span * blockIdx.y, heads = min(A.hq + 2 * hkv, first + span);
     const int64_t q_row = r * A.q_row, k_row = r * A.k_row, v_row = r * A.v_row;
     auto source = [&](int h) {
         return h < A.hq ? A.q + (q_row + h * A.q_head)
              : h < A.hq + hkv ? A.k + (k_row + (h - A.hq) * A.k_head) : A.v + (v_row + (h - A.hq - hkv) * A.v_head);
     };
-    uint4 raw[BATCH];
+    // into a 4-bit cache the keys come last, by themselves
+    const int k_first = max(first, A.hq), k_heads = min(heads, A.hq + hkv);
+    uint4 raw[BATCH], raw_k = make_uint4(0, 0, 0, 0);
+    if (KEYS && k_first + grp < k_heads) raw_k = load_once(source(k_first + grp) + 8 * lane);
     auto load = [&](int h0) {
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
@@ -309,13 +429,10 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, co
         sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
         cs[tid] = c * A.rot_scale;
         sn[tid] = s * A.rot_scale;
-        if constexpr (MX) {
-            double s64, c64;
-            sincos((double)pos * (double)A.inv_freq[tid], &s64, &c64);      // the product is exact
-            cs64[tid] = c64 * (double)A.rot_scale;
-            sn64[tid] = s64 * (double)A.rot_scale;
-        }
+        if constexpr (KEYS) turn_f64(A, pos, tid, cs64[tid], sn64[tid]);
     }
+    if constexpr (KEYS)
+        if (tid < D) weight[tid] = A.k_norm ? (double)A.k_norm[tid] : 1.0;
     const int page = slot >> A.kv.page_shift, off = slot & ((1 << A.kv.page_shift) - 1);
     const bool cached = slot >= 0 && page < A.kv.n_pages;
     lds_barrier();
@@ -380,26 +497,7 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, co
             }
             const size_t at = (((size_t)page * hkv + kvh) << A.kv.page_shift) + off;
             if constexpr (MX) {
-                if (__ballot(is_k)) exact_key<D, LANES>(A, raw[b], lane, is_k, swap[grp], cs64, sn64, x);
-                uint32_t top = 0;               // of the bits: a NaN is above infinity
-#pragma unroll
-                for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-                top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, false));
-                top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, false));
-                if (there && !is_q && cached) {
-                    const bool fin = top < 0x7f800000u;
-                    const int e = fin ? min(max((int)((top + (1u << 21)) >> 23) - 2, kMxLeast), kMxMost) : kMxNan;
-                    const float to = __uint_as_float((uint32_t)(254 - e) << 23);         // 2^(127 - e)
-                    uint32_t codes = 0;
-                    if (fin) {
-                        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, x[0] * to, x[1] * to, 1.0f, 0);
-                        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, x[2] * to, x[3] * to, 1.0f, 1);
-                        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, x[4] * to, x[5] * to, 1.0f, 2);
-                        codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, x[6] * to, x[7] * to, 1.0f, 3);
-                    }
-                    *reinterpret_cast<uint32_t *>((is_k ? A.kv.k : A.kv.v) + at * (D / 2) + 4 * lane) = codes;
-                    if (lane % 4 == 0) (is_k ? A.kv.k_exp : A.kv.v_exp)[at * (D / kMxBlock) + lane / 4] = (uint8_t)e;
-                }
+                put_block<D>(x, lane, there && !is_q && !is_k && cached, A.kv.v, A.kv.v_exp, at);
             } else if (A.kv.k_scale) {
                 float m = 0.0f;
 #pragma unroll
@@ -419,6 +517,20 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs A, co
                 const uint4 o = is_k ? make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])) : raw[b];
                 store_once((is_k ? A.kv.k : A.kv.v) + (at * D + 8 * lane) * 2, o);
             }
+        }
+    }
+    if constexpr (KEYS) {
+#pragma unroll 1
+        for (int h0 = k_first; h0 < k_heads; h0 += HEADS) {
+            const int h = h0 + grp;
+            if (h0 > k_first) {
+                raw_k = make_uint4(0, 0, 0, 0);
+                if (h < k_heads) raw_k = load_once(source(h) + 8 * lane);
+            }
+            float x[8];
+            exact_key<D, LANES>(A, raw_k, lane, swap64[grp], weight, cs64, sn64, x);
+            const size_t at = (((size_t)page * hkv + h - A.hq) << A.kv.page_shift) + off;
+            put_block<D>(x, lane, h < k_heads && cached, A.kv.k, A.kv.k_exp, at);
         }
     }
 }
@@ -613,8 +725,15 @@ static void launch_prep_d(const PrepArgs &A, hipStream_t stream)
     const int heads = A.hq + 2 * A.kv.hkv, at_once = kPrepThreads / (D / 8);
     const int span = A.rows <= kPrepFewRows && heads > at_once ? at_once : heads;
     const dim3 grid(A.rows, (heads + span - 1) / span);
-    if (A.kv.k_exp) prep_kernel<D, true><<<grid, kPrepThreads, 0, stream>>>(A, span);
-    else prep_kernel<D, false><<<grid, kPrepThreads, 0, stream>>>(A, span);
+    if (!A.kv.k_exp) {
+        prep_kernel<D, PREP_ROWS><<<grid, kPrepThreads, 0, stream>>>(A, span);
+    } else if (A.rows <= kPrepFewRows) {
+        prep_kernel<D, PREP_MX><<<grid, kPrepThreads, 0, stream>>>(A, span);
+    } else {
+        const size_t lds = sizeof(double) * (D + at_once * A.rot + key_rows(at_once, A.kv.hkv) * A.rot);
+        const long long keys = ((long long)A.rows * A.kv.hkv + at_once - 1) / at_once;
+        prep_kernel<D, PREP_MX_APART><<<(unsigned)(A.rows + keys), kPrepThreads, lds, stream>>>(A, heads);
+    }
 }
 
 hipError_t launch_prep(const PrepArgs &A, hipStream_t stream)

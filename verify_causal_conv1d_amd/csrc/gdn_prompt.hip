@@ -49,11 +49,6 @@ __device__ __forceinline__ const_args *fresh_args()
 
 __device__ __forceinline__ float uniform(float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x))); }
 
-// Entries of the block table, which nothing writes while the kernel runs, through
-// the scalar cache: their addresses are the wave's.
-typedef const __attribute__((address_space(4))) int const_int;
-__device__ __forceinline__ int table_entry(const int *table, int i) { return ((const_int *)table)[i]; }
-
 constexpr int kSub = 32;       // keys of a matrix instruction's tile
 constexpr int kAhead = 3;      // operands on their way from LDS
 
