@@ -228,7 +228,9 @@ def test_offsets_past_32_bits():
     (1, 1, 1, 64, 0, 16, False, True), (5, 4, 2, 64, 64, 16, False, True), (5, 4, 2, 64, 64, 16, True, True),
     (33, 24, 4, 256, 64, 64, False, True), (33, 24, 4, 256, 64, 64, True, False), (7, 6, 2, 128, 50, 32, False, True),
     (7, 3, 3, 128, 2, 256, True, False), (7, 9, 3, 128, 126, 128, False, True), (64, 8, 1, 256, 256, 16, False, True),
-    (64, 7, 7, 256, 256, 16, True, True), (300, 2, 1, 64, 22, 16, True, True), (700, 3, 3, 128, 128, 64, False, False)])
+    (64, 7, 7, 256, 256, 16, True, True), (300, 2, 1, 64, 22, 16, True, True), (700, 3, 3, 128, 128, 64, False, False),
+    (700, 3, 3, 64, 20, 64, False, True), (601, 4, 1, 256, 2, 16, True, True), (520, 2, 2, 128, 126, 32, False, True),
+    (513, 1, 1, 64, 0, 16, False, True), (900, 20, 5, 64, 60, 16, True, True)])
 def test_prep_writes_the_oracles_codes(R, hq, hkv, d, rot, page, inter, norm):
     """Every code and every exponent, of keys and of values."""
     announce(f"prep into 4 bits, rows {R} heads {hq}/{hkv} d {d} rot {rot} page {page} interleaved {inter} norm {norm}")

@@ -341,17 +341,20 @@ __device__ __forceinline__ void exact_key(const PrepArgs &A, uint4 raw, int lane
     __builtin_amdgcn_wave_barrier();
 }
 
-// A workgroup's keys of many rows into a 4-bit cache: (row, kv head) pairs in order,
-// as many as its lanes hold.
-// (rows that n pairs in order belong to, at most)
+// Rows that n (row, kv head) pairs in order belong to, at most, and the doubles that
+// a key takes for its lanes' exchange (a lane puts down all of its eight)
 __host__ __device__ inline int key_rows(int n, int hkv) { return (n - 1) / hkv + 2 < n ? (n - 1) / hkv + 2 : n; }
 
+__host__ __device__ inline int key_swap(int rot) { return (rot + 7) & ~7; }
+
+// A workgroup's keys of many rows into a 4-bit cache: pairs in order, as many as its
+// lanes hold
 template <int D>
 __device__ __forceinline__ void prep_keys(const PrepArgs &A, const int block, double *lds64)
 {
     constexpr int LANES = D / 8, HEADS = kPrepThreads / LANES;
     const int tid = threadIdx.x, lane = tid % LANES, grp = tid / LANES, hkv = A.kv.hkv, half = A.rot / 2;
-    double *weight = lds64, *swap = weight + D, *cs64 = swap + HEADS * A.rot, *sn64 = cs64 + key_rows(HEADS, hkv) * half;
+    double *weight = lds64, *swap = weight + D, *cs64 = swap + HEADS * key_swap(A.rot), *sn64 = cs64 + key_rows(HEADS, hkv) * half;
     const long long first = (long long)block * HEADS, pairs = (long long)A.rows * hkv, pair = first + grp;
     const int row0 = (int)(first / hkv), r = (int)(min(pair, pairs - 1) / hkv), h = (int)(pair - (long long)r * hkv);
     const bool there = pair < pairs;
@@ -363,7 +366,7 @@ __device__ __forceinline__ void prep_keys(const PrepArgs &A, const int block, do
     if (tid < D) weight[tid] = A.k_norm ? (double)A.k_norm[tid] : 1.0;
     lds_barrier();
     float x[8];
-    exact_key<D, LANES>(A, raw, lane, swap + grp * A.rot, weight, cs64 + (r - row0) * half, sn64 + (r - row0) * half, x);
+    exact_key<D, LANES>(A, raw, lane, swap + grp * key_swap(A.rot), weight, cs64 + (r - row0) * half, sn64 + (r - row0) * half, x);
     const size_t at = (((size_t)page * hkv + h) << A.kv.page_shift) + (slot & ((1 << A.kv.page_shift) - 1));
     put_block<D>(x, lane, there && slot >= 0 && page < A.kv.n_pages, A.kv.k, A.kv.k_exp, at);
 }
@@ -730,7 +733,7 @@ static void launch_prep_d(const PrepArgs &A, hipStream_t stream)
     } else if (A.rows <= kPrepFewRows) {
         prep_kernel<D, PREP_MX><<<grid, kPrepThreads, 0, stream>>>(A, span);
     } else {
-        const size_t lds = sizeof(double) * (D + at_once * A.rot + key_rows(at_once, A.kv.hkv) * A.rot);
+        const size_t lds = sizeof(double) * (D + at_once * key_swap(A.rot) + key_rows(at_once, A.kv.hkv) * A.rot);
         const long long keys = ((long long)A.rows * A.kv.hkv + at_once - 1) / at_once;
         prep_kernel<D, PREP_MX_APART><<<(unsigned)(A.rows + keys), kPrepThreads, lds, stream>>>(A, heads);
     }
