@@ -196,37 +196,42 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
     constexpr int KS = D / 16, NT = D / 32, T = TILES;
     constexpr int NK = S::HALF / 1024, PER = 2 * NK / WAVES;     // direct loads of a stage's keys; of a wave, in all
     
+    // Operands of the queries that stay in LDS: with all of them in registers the
+    // first three of e4m3 rows of 256 channels went to memory, and reading them back
+    // waited for the rows on their way.
+    constexpr int QL = FMT == FMT_E4M3 && D == 256 ? 4 : 0;
+    __shared__ __align__(16) uint4 q_lds[QL ? WAVES * QL * 64 : 1];
     // separate arrays, so that loads into one are known not to touch the other
     __shared__ __align__(1024) uint8_t st0[S::BYTES], st1[S::BYTES];
     __shared__ __align__(16) float sc0[S::SCALES], sc1[S::SCALES];
     __shared__ int wave_ok[WAVES], bad;
     __shared__ int2 pairs[S::COLS];          // packed row and query head of each column
     __shared__ PromptPiece kept;             // K, for the end
+    __shared__ uint32_t seen[WINDOW ? S::COLS : 1];      // rows of a window that each column sees
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 31, g = lane >> 5;
+    const int cw = WINDOW ? wave : wave;
     const float scale = uniform(A.scale == 0.0f ? 1.0f : fabsf(A.scale));
     PromptPiece K;
     for (int item = blockIdx.x; find_piece<S::COLS, WINDOW>(A, split_keys, item, K); item += gridDim.x) {
         if (K.k0 >= K.k1) continue;                 // a chunk past all that the tile sees
         bool ok = true;
-        const int col0 = K.rt * S::COLS + wave * 32 * T;            // the wave's first column
+        const int col0 = K.rt * S::COLS + cw * 32 * T;            // the wave's first column
         const bool busy = col0 < K.cols;                            // waves without columns only load
         const int t_lo = min(col0, K.cols - 1) / A.group, t_hi = min(col0 + 32 * T, K.cols) - 1;   // rows of the wave
         const int see_lo = K.kv + t_lo, see_hi = K.kv + t_hi / A.group;      // the last key that the first and the last one see
         int row[T];
-        uint32_t seen[T];
 #pragma unroll
         for (int c = 0; c < T; ++c) {
             const int col = min(col0 + 32 * c + n, K.cols - 1);     // past the last one: that one again, not stored
             const int t = col / A.group;
             row[c] = t;
-            pairs[wave * 32 * T + 32 * c + n] = make_int2(K.r0 + t, K.h * A.group + col - t * A.group);     // (both halves the same)
-            seen[c] = 0;
-            if constexpr (WINDOW) seen[c] = seen_rows(A, K.r0, K.m, t, ok);
+            pairs[cw * 32 * T + 32 * c + n] = make_int2(K.r0 + t, K.h * A.group + col - t * A.group);     // (both halves the same)
+            if constexpr (WINDOW) seen[cw * 32 * T + 32 * c + n] = seen_rows(A, K.r0, K.m, t, ok);
         }
         // place of a column's (row, head) in q and out
         auto pair_of = [&](int c, int hq) {
-            const int2 p = pairs[wave * 32 * T + 32 * c + (this_lane() & 31)];
+            const int2 p = pairs[cw * 32 * T + 32 * c + (this_lane() & 31)];
             return (size_t)p.x * hq + p.y;
         };
         __builtin_amdgcn_wave_barrier();
@@ -276,14 +281,13 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
         static_assert(S::UNITS % 64 == 0, "");
         struct Unit {
             bool there, is_v;
-            int first, r, p;        // the wave's first row; the lane's, and its piece there
+            int first;              // the wave's first row
         };
         auto unit = [&](int x) {
             constexpr bool SAME = S::UNITS % S::THREADS == 0, ALL = 2 * S::UNITS % S::THREADS == 0;
             const int u = (x * WAVES + wave) * 64;
             const bool is_v = SAME ? x >= S::LOADS / 2 : u >= S::UNITS;
-            const int at = is_v ? u - S::UNITS : u, in = this_lane();
-            return Unit{ALL || u < 2 * S::UNITS, is_v, at / S::PER_ROW, at / S::PER_ROW + in / S::PER_ROW, in % S::PER_ROW};
+            return Unit{ALL || u < 2 * S::UNITS, is_v, (is_v ? u - S::UNITS : u) / S::PER_ROW};
         };
         // bf16: straight to a stage; else to registers, for put
         auto load = [&](uint8_t *stage) {
@@ -304,12 +308,19 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                 for (int x = 0; x < S::LOADS; ++x) {
                     const Unit u = unit(x);
                     if (!u.there) continue;
-                    // rows of a wave's unit: one group of 16, or two
-                    int row = group_row(u.first / 16);
-                    if constexpr (S::PER_ROW < 4) row = u.r / 16 == u.first / 16 ? row : group_row(u.first / 16 + 1);
-                    const size_t at = row + (u.r & 15);
-                    raw[x] = *reinterpret_cast<const uint4 *>((u.is_v ? A.kv.v : A.kv.k) + (at * S::CODES + 16 * u.p));
-                    if constexpr (FMT == FMT_MXFP4) raw_scale[x] = (u.is_v ? A.kv.v_exp : A.kv.k_exp)[at * (D / kMxBlock) + u.p];
+                    // the wave's rows lie one after the other in a group of 16, or in two
+                    const uint32_t ln = this_lane();
+                    size_t at;
+                    uint32_t in;
+                    if constexpr (S::PER_ROW < 4) {
+                        at = ln < 32 ? group_row(u.first / 16) : group_row(u.first / 16 + 1);
+                        in = ln & 31;
+                    } else {
+                        at = group_row(u.first / 16) + (u.first & 15);
+                        in = ln;
+                    }
+                    raw[x] = *reinterpret_cast<const uint4 *>((u.is_v ? A.kv.v : A.kv.k) + at * S::CODES + 16 * in);
+                    if constexpr (FMT == FMT_MXFP4) raw_scale[x] = ((u.is_v ? A.kv.v_exp : A.kv.k_exp) + at * (D / kMxBlock))[in];
                 }
                 if constexpr (FMT == FMT_E4M3) {        // the first waves: a scale a lane, of the keys and then of the values
                     if (wave < 2) row_scale = (wave == 0 ? A.kv.k_scale : A.kv.v_scale)[(size_t)group_row(this_lane() % S::KEYS / 16) + (this_lane() & 15)];
@@ -324,14 +335,15 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                     __builtin_amdgcn_sched_barrier(0);
                     const Unit u = unit(x);
                     if (!u.there) continue;
-                    const int p = u.p;
-                    uint8_t *to = stage + u.is_v * S::HALF + u.r * S::ROW;
-                    const int sw = u.is_v ? S::v_swizzle(u.r) : S::k_swizzle(u.r);
+                    // the lane's row and its first piece there; the others change bits of their own
+                    const uint32_t ln = this_lane(), r = u.first + ln / S::PER_ROW, p = ln % S::PER_ROW * (S::ROW / 16 / S::PER_ROW);
+                    const uint32_t to = r * S::ROW + (p ^ (u.is_v ? S::v_swizzle(r) : S::k_swizzle(r))) * 16;
+                    uint8_t *half = stage + u.is_v * S::HALF;
                     const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
                     if constexpr (FMT == FMT_MXFP4) {
                         const float f = mx_scale(raw_scale[x]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(to + ((4 * p + i) ^ sw) * 16) = mx_values8(w[i], f);
+                        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(half + (to ^ i * 16)) = mx_values8(w[i], f);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
@@ -341,7 +353,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                                 y[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * i + j], 1.0f, false));
                                 y[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * i + j], 1.0f, true));
                             }
-                            *reinterpret_cast<uint4 *>(to + ((2 * p + i) ^ sw) * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4 *>(half + (to ^ i * 16)) = make_uint4(y[0], y[1], y[2], y[3]);
                         }
                     }
                 }
@@ -382,6 +394,9 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
             bf8v ring[kAhead + 1];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) ring[k] = key(k);
+            bf8v q_first[QL + 1];
+#pragma unroll
+            for (int k = 0; k < QL; ++k) q_first[k] = __builtin_bit_cast(bf8v, q_lds[(wave * QL + k) * 64 + ln]);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 if (k + kAhead < KS) ring[(k + kAhead) % (kAhead + 1)] = key(k + kAhead);
@@ -391,7 +406,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                         for (int a = 0; a < 4; ++a) ks[a] = *reinterpret_cast<const float4 *>(scale_at + 8 * a);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int c = 0; c < T; ++c) acc[c] = mfma32(ring[k % (kAhead + 1)], q[c][k], acc[c]);
+                for (int c = 0; c < T; ++c) acc[c] = mfma32(ring[k % (kAhead + 1)], k < QL ? q_first[k < QL ? k : 0] : q[c][k], acc[c]);
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
@@ -419,9 +434,16 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                     }
                 }
                 const int from = first + (this_lane() >> 5) * 4 - K.kv;          // the lane's first key's place in the pass
+                // bit i: the lane's key i of the 32 (8 a + b), in a window
+                uint32_t in_sight = ~0u;
+                if constexpr (WINDOW)
+                    if (tail) {
+                        const uint32_t rows = seen[cw * 32 * T + 32 * c + (this_lane() & 31)];
+                        in_sight = from >= kMaxWindowRows ? 0 : from >= 0 ? rows >> from : from <= -32 ? ~0u : rows << -from | ~(~0u << -from);
+                    }
                 auto sees = [&](int e) {
-                    const int at = 8 * (e / 4) + (e & 3), j = from + at;
-                    return WINDOW ? (j < 0) | ((j < kMaxWindowRows) & (seen[c] >> (j & 31))) : at <= row[c] - from;
+                    const int at = 8 * (e / 4) + (e & 3);
+                    return WINDOW ? (bool)(in_sight >> at & 1) : at <= row[c] - from;
                 };
                 if (tail)
 #pragma unroll
@@ -532,6 +554,8 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                     q[c][k] = __builtin_bit_cast(bf8v, make_uint4((x.x & keep) ^ sign, (x.y & keep) ^ sign, (x.z & keep) ^ sign, (x.w & keep) ^ sign));
                 }
         }
+#pragma unroll
+        for (int k = 0; k < QL; ++k) q_lds[(wave * QL + k) * 64 + this_lane()] = __builtin_bit_cast(uint4, q[0][k]);
         auto step = [&](int tile, uint8_t *stage, float *scales, uint8_t *next, float *next_scales) {
             wait_and_meet<0>();
             if (tile + 1 < tiles) {
@@ -581,7 +605,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                                wave_int(kept.kv), wave_int(kept.len), wave_int(kept.k0), wave_int(kept.k1), wave_int(kept.nch), wave_int(kept.cols)};
         const uint16_t *const gate_at = B->gate;
         const int64_t gate_row = B->gate_row, gate_head = B->gate_head;
-        const int first_col = E.rt * S::COLS + wave * 32 * T, hq = B->hq, chunks = B->chunks;
+        const int first_col = E.rt * S::COLS + cw * 32 * T, hq = B->hq, chunks = B->chunks;
         constexpr int FIT = S::BYTES / (WAVES / 2 * 32 * 4), CH = FIT < D ? FIT : D, PC = CH / 4, LPC = CH / 8;    // channels; pieces of a column; lanes that read it
         static_assert(CH >= 32 && D % CH == 0, "");
         uint8_t *mine = wave < WAVES / 2 ? st0 + wave * (32 * CH * 4) : st1 + (wave - WAVES / 2) * (32 * CH * 4);
@@ -594,7 +618,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
             if (bad) {
                 for (int key = bad_from; key < E.k1; ++key) {
                     const int j = key - E.kv;
-                    if (j >= 0 && !(WINDOW ? seen[c] >> j & 1 : j <= row[c])) continue;
+                    if (j >= 0 && !(WINDOW ? seen[first_col + 32 * c + en - E.rt * S::COLS] >> j & 1 : j <= row[c])) continue;
                     const int id = B->table[(size_t)E.s * B->max_blocks + (key >> B->kv.page_shift)];
                     const size_t at = (((size_t)id * B->kv.hkv + E.h) << B->kv.page_shift) + (key & ((1 << B->kv.page_shift) - 1));
 #pragma unroll
@@ -629,7 +653,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                 if (E.nch == 1 && gate_at)
 #pragma unroll
                     for (int y = 0; y < RUNS; ++y) {
-                        const int2 p = pairs[wave * 32 * T + 32 * c + y * (64 / LPC) + ln / LPC];
+                        const int2 p = pairs[cw * 32 * T + 32 * c + y * (64 / LPC) + ln / LPC];
                         const uint16_t *from = gate_at + p.x * gate_row + p.y * gate_head + (part * CH + 8 * (ln % LPC));
                         gate[y][0] = reinterpret_cast<const uint2 *>(from)[0], gate[y][1] = reinterpret_cast<const uint2 *>(from)[1];
                     }
@@ -640,7 +664,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                     const float4 v = *reinterpret_cast<const float4 *>(mine + (n * PC + ((2 * x + 1) ^ (n & (PC - 1)))) * 16);
                     __builtin_amdgcn_sched_barrier(0);
                     if (first_col + 32 * c + n >= E.cols) continue;
-                    const int2 p = pairs[wave * 32 * T + 32 * c + n];
+                    const int2 p = pairs[cw * 32 * T + 32 * c + n];
                     const size_t pair = (size_t)p.x * hq + p.y;
                     if (E.nch == 1) {
                         const uint2 a = gated4(u, gate_at != nullptr, gate[y][0]), b = gated4(v, gate_at != nullptr, gate[y][1]);
