@@ -52,17 +52,42 @@ __device__ __forceinline__ float uniform(float x) { return __uint_as_float(__bui
 constexpr int kSub = 32;       // keys of a matrix instruction's tile
 constexpr int kAhead = 3;      // operands on their way from LDS
 
-// A stage of keys and values in LDS, in bf16: KEYS rows of K, then of V.  The
-// 16-byte pieces of a row of K are exchanged by a function of the row, so that 16
-// rows of one operand lie in different banks; rows of V likewise, the 16 channels
-// of a transposing read (32 bytes) together.
+// A stage of keys and values in LDS, in bf16: KEYS rows of K, then of V, in 16-byte
+// pieces.  A lane that converts 16 bytes of e4m3 or of 4-bit codes stores 2 or 4
+// pieces; those of the same turn lie one after the other, for a row's lanes.  Pieces
+// are exchanged by a function of the row, linear in its bits, so that of 16 lanes
+// one after the other that store a piece, of 16 rows of K read at one piece, and
+// of 32 lanes that read V transposed (4 rows at 64 bytes of channels), each 256 bytes
+// of LDS hold every place as often as any other.  (Pieces in order, with the rows
+// exchanged as those of bf16: half of the LDS's busy cycles over 4 bits were
+// conflicts.)
 template <int D, int FMT, int WAVES, int TILES, int KEYS_>
 struct PromptShape {
     static constexpr int THREADS = 64 * WAVES, COLS = 32 * TILES * WAVES;
     static constexpr int KEYS = KEYS_, ROW = 2 * D, HALF = KEYS * ROW, BYTES = 2 * HALF;
     static constexpr int PIECES = ROW / 16, ROWS = 1024 / ROW;    // of a direct load
-    static __device__ __forceinline__ int k_swizzle(int key) { return ROW >= 256 ? key & 15 : key >> 1 & 7; }
-    static __device__ __forceinline__ int v_swizzle(int key) { return 2 * (ROW >= 256 ? key & 7 : key >> 1 & 3); }
+    static constexpr int TURNS = FMT == FMT_BF16 ? 1 : FMT == FMT_E4M3 ? 2 : 4, LANES = PIECES / TURNS;     // of a row
+    static __device__ __forceinline__ int k_place(int c) { return c % TURNS * LANES + c / TURNS; }
+    static __device__ __forceinline__ int v_place(int c)
+    {
+        const int i = c % TURNS, more = D < 256 ? 0 : FMT == FMT_E4M3 ? 8 * i : FMT == FMT_MXFP4 ? (i >> 1) * 4 : 0;
+        return (i * LANES + c / TURNS) ^ more;
+    }
+    static __device__ __forceinline__ int k_swizzle(int r)
+    {
+        if (FMT == FMT_BF16) return ROW >= 256 ? r & 15 : r >> 1 & 7;
+        if (D == 64) return FMT == FMT_E4M3 ? (r & 2) * 2 + (r & 4) / 2 + (r & 8) / 8 : (r & 6) + (r & 8) / 8;
+        return FMT == FMT_MXFP4 && D == 128 ? (r & 3) * 4 | (r >> 2 & 3) : (r & 1) * 8 | (r >> 1 & 7);
+    }
+    static __device__ __forceinline__ int v_swizzle(int r)
+    {
+        if (FMT == FMT_BF16) return ROW >= 256 ? (r & 3) * 4 : (r & 2) * 2;
+        if (D == 64) return FMT == FMT_E4M3 ? (r >> 1 & 1) * 6 : (r >> 1 & 1) * 3 ^ (r & 4);
+        if (D == 128) return FMT == FMT_E4M3 ? (r & 1) * 10 ^ (r & 2) * 2 : (r & 3) * 5;
+        return FMT == FMT_E4M3 ? (r & 3) * 2 : (r & 1) * 9 ^ (r & 6);
+    }
+    // `from`, a row's place in bytes, with piece c's place (known at compile time) exchanged into it
+    static __device__ __forceinline__ int with_place(int from, int place) { return (from ^ (place & 15) * 16) + (place & ~15) * 16; }
     // cached rows in their own format
     static constexpr int CODES = FMT == FMT_BF16 ? ROW : FMT == FMT_E4M3 ? D : D / 2;
     static constexpr int PER_ROW = CODES / 16;                   // 16-byte units of a row
@@ -210,13 +235,12 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
     __shared__ uint32_t seen[WINDOW ? S::COLS : 1];      // rows of a window that each column sees
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 31, g = lane >> 5;
-    const int cw = WINDOW ? wave : wave;
     const float scale = uniform(A.scale == 0.0f ? 1.0f : fabsf(A.scale));
     PromptPiece K;
     for (int item = blockIdx.x; find_piece<S::COLS, WINDOW>(A, split_keys, item, K); item += gridDim.x) {
         if (K.k0 >= K.k1) continue;                 // a chunk past all that the tile sees
         bool ok = true;
-        const int col0 = K.rt * S::COLS + cw * 32 * T;            // the wave's first column
+        const int col0 = K.rt * S::COLS + wave * 32 * T;            // the wave's first column
         const bool busy = col0 < K.cols;                            // waves without columns only load
         const int t_lo = min(col0, K.cols - 1) / A.group, t_hi = min(col0 + 32 * T, K.cols) - 1;   // rows of the wave
         const int see_lo = K.kv + t_lo, see_hi = K.kv + t_hi / A.group;      // the last key that the first and the last one see
@@ -226,12 +250,12 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
             const int col = min(col0 + 32 * c + n, K.cols - 1);     // past the last one: that one again, not stored
             const int t = col / A.group;
             row[c] = t;
-            pairs[cw * 32 * T + 32 * c + n] = make_int2(K.r0 + t, K.h * A.group + col - t * A.group);     // (both halves the same)
-            if constexpr (WINDOW) seen[cw * 32 * T + 32 * c + n] = seen_rows(A, K.r0, K.m, t, ok);
+            pairs[wave * 32 * T + 32 * c + n] = make_int2(K.r0 + t, K.h * A.group + col - t * A.group);     // (both halves the same)
+            if constexpr (WINDOW) seen[wave * 32 * T + 32 * c + n] = seen_rows(A, K.r0, K.m, t, ok);
         }
         // place of a column's (row, head) in q and out
         auto pair_of = [&](int c, int hq) {
-            const int2 p = pairs[cw * 32 * T + 32 * c + (this_lane() & 31)];
+            const int2 p = pairs[wave * 32 * T + 32 * c + (this_lane() & 31)];
             return (size_t)p.x * hq + p.y;
         };
         __builtin_amdgcn_wave_barrier();
@@ -335,15 +359,15 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                     __builtin_amdgcn_sched_barrier(0);
                     const Unit u = unit(x);
                     if (!u.there) continue;
-                    // the lane's row and its first piece there; the others change bits of their own
-                    const uint32_t ln = this_lane(), r = u.first + ln / S::PER_ROW, p = ln % S::PER_ROW * (S::ROW / 16 / S::PER_ROW);
-                    const uint32_t to = r * S::ROW + (p ^ (u.is_v ? S::v_swizzle(r) : S::k_swizzle(r))) * 16;
+                    // the lane's row and its place there
+                    const uint32_t ln = this_lane(), r = u.first + ln / S::PER_ROW, p = ln % S::PER_ROW;
+                    const int to = r * S::ROW + (p ^ (u.is_v ? S::v_swizzle(r) : S::k_swizzle(r))) * 16;
                     uint8_t *half = stage + u.is_v * S::HALF;
                     const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
                     if constexpr (FMT == FMT_MXFP4) {
                         const float f = mx_scale(raw_scale[x]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(half + (to ^ i * 16)) = mx_values8(w[i], f);
+                        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(half + S::with_place(to, u.is_v ? S::v_place(i) : S::k_place(i))) = mx_values8(w[i], f);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
@@ -353,12 +377,12 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                                 y[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * i + j], 1.0f, false));
                                 y[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * i + j], 1.0f, true));
                             }
-                            *reinterpret_cast<uint4 *>(half + (to ^ i * 16)) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4 *>(half + S::with_place(to, u.is_v ? S::v_place(i) : S::k_place(i))) = make_uint4(y[0], y[1], y[2], y[3]);
                         }
                     }
                 }
                 if constexpr (FMT == FMT_E4M3)
-                    if (wave < 2 && this_lane() < S::KEYS) scales[wave * S::KEYS + this_lane()] = row_scale;
+                    if (wave < 2 && this_lane() < S::KEYS) scales[wave * S::KEYS + this_lane()] = wave == 0 ? row_scale * scale : row_scale;
             }
         };
 
@@ -372,18 +396,18 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
 
             // Operands are read kAhead steps before the products that take them; the
             // first ones of the values before the weights are worked out.
-            // piece 2 k + g of row n: 2 k is even, so that it changes bits of its own
+            // piece 2 k + g of row n
             const int ln = this_lane(), kn = ln & 31;
             const uint8_t *kr = stage + sub * kSub * S::ROW;
-            const int k_at = kn * S::ROW + ((ln >> 5) ^ S::k_swizzle(kn)) * 16;
-            auto key = [&](int k) { return *reinterpret_cast<const bf8v *>(kr + ((k_at ^ (k & 7) * 32) + (k >> 3) * 256)); };
+            const int k_at = kn * S::ROW + (S::k_place(ln >> 5) ^ S::k_swizzle(kn)) * 16;
+            auto key = [&](int k) { return *reinterpret_cast<const bf8v *>(kr + S::with_place(k_at, S::k_place(2 * k))); };
             // the operand of channels 32 i .. and keys 16 t + 8 a + 4 g .. + 3 (a < 2),
             // transposed by the reads: this lane brings 4 channels of one of those keys
             const int l16 = ln & 15, vr = 4 * (ln >> 5) + (l16 >> 2), cb = ln >> 4 & 1;
             const uint8_t *vp = stage + S::HALF + sub * kSub * S::ROW;
-            const int v_at = vr * S::ROW + (l16 & 3) * 8 + ((2 * cb) ^ S::v_swizzle(vr)) * 16;
+            const int v_at = vr * S::ROW + (l16 & 1) * 8 + (S::v_place(2 * cb + (l16 >> 1 & 1)) ^ S::v_swizzle(vr)) * 16;
             auto value = [&](int x) {
-                const int i = x >> 1, t = x & 1, at = (v_at ^ (i & 3) * 64) + (i >> 2) * 256 + 16 * t * S::ROW;
+                const int i = x >> 1, t = x & 1, at = S::with_place(v_at, S::v_place(4 * i)) + 16 * t * S::ROW;
                 const s4v lo = read_transposed(vp + at), hi = read_transposed(vp + (at + 8 * S::ROW));
                 return __builtin_bit_cast(bf8v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
             };
@@ -420,6 +444,11 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
 #pragma unroll
             for (int c = 0; c < T; ++c) {
                 f16v &s = acc[c];
+                // Any base within reach of the maximum does: scores are taken from the one
+                // that is there, and it moves, to 2^8 above the maximum, only when that has
+                // passed it.  (e4m3: the keys' scales in LDS have the call's in them.)
+                const bool unset = mx[c] == -INFINITY;
+                const float base = unset ? 0.0f : mx[c];
                 if constexpr (FMT == FMT_E4M3) {
 #pragma unroll
                     for (int a = 0; a < 4; ++a) {
@@ -430,15 +459,19 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                             __builtin_amdgcn_sched_barrier(0);
                             f = *reinterpret_cast<const float4 *>(scale_at + 8 * a);
                         }
-                        s[4 * a] *= f.x, s[4 * a + 1] *= f.y, s[4 * a + 2] *= f.z, s[4 * a + 3] *= f.w;
+                        s[4 * a] = fmaf(s[4 * a], f.x, -base), s[4 * a + 1] = fmaf(s[4 * a + 1], f.y, -base);
+                        s[4 * a + 2] = fmaf(s[4 * a + 2], f.z, -base), s[4 * a + 3] = fmaf(s[4 * a + 3], f.w, -base);
                     }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) s[e] = fmaf(s[e], scale, -base);
                 }
                 const int from = first + (this_lane() >> 5) * 4 - K.kv;          // the lane's first key's place in the pass
                 // bit i: the lane's key i of the 32 (8 a + b), in a window
                 uint32_t in_sight = ~0u;
                 if constexpr (WINDOW)
                     if (tail) {
-                        const uint32_t rows = seen[cw * 32 * T + 32 * c + (this_lane() & 31)];
+                        const uint32_t rows = seen[wave * 32 * T + 32 * c + (this_lane() & 31)];
                         in_sight = from >= kMaxWindowRows ? 0 : from >= 0 ? rows >> from : from <= -32 ? ~0u : rows << -from | ~(~0u << -from);
                     }
                 auto sees = [&](int e) {
@@ -448,24 +481,27 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                 if (tail)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) s[e] = sees(e) ? s[e] : -INFINITY;
-                float tm = fmaxf(s[0], s[1]);
+                float top = fmaxf(s[0], s[1]);
 #pragma unroll
-                for (int e = 2; e < 16; ++e) tm = fmaxf(tm, s[e]);
-                // Any base within reach of the maximum does: it moves only when the
-                // maximum has passed it, and then to 2^8 above that
-                tm = max_halves(tm) * scale;
-                tm = tm > mx[c] ? tm + 8.0f : mx[c];
-                const float base = tm == -INFINITY ? 0.0f : tm;
-                const float back = __builtin_amdgcn_exp2f(mx[c] - base);
-                const bool moved = __ballot(tm != mx[c] && mx[c] != -INFINITY);
-                mx[c] = tm;
-                float ps = 0.0f;
+                for (int e = 2; e < 16; ++e) top = fmaxf(top, s[e]);
+                top = max_halves(top);
+                const bool passed = top > (unset ? -INFINITY : 0.0f);
+                if (__ballot(passed)) {
+                    const float by = passed ? top + 8.0f : 0.0f, back = __builtin_amdgcn_exp2f(mx[c] - (base + by));
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) s[e] -= by;
+                    if (passed) mx[c] = base + by;
+                    sum[c] *= back;
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[c][i][e] *= back;
+                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], scale, -base));
-                    ps += s[e];
+                    s[e] = __builtin_amdgcn_exp2f(s[e]);
+                    sum[c] += s[e];
                 }
-                sum[c] = fmaf(sum[c], back, ps);
                 if constexpr (FMT == FMT_E4M3) {
 #pragma unroll
                     for (int a = 0; a < 4; ++a) {
@@ -487,12 +523,6 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                     const uint4 x = {pack2(s[8 * t], s[8 * t + 1]), pack2(s[8 * t + 2], s[8 * t + 3]), pack2(s[8 * t + 4], s[8 * t + 5]),
                                      pack2(s[8 * t + 6], s[8 * t + 7])};
                     pb[c][t] = __builtin_bit_cast(bf8v, x);
-                }
-                if (moved) {
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[c][i][e] *= back;
                 }
             }
 #pragma unroll
@@ -605,7 +635,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                                wave_int(kept.kv), wave_int(kept.len), wave_int(kept.k0), wave_int(kept.k1), wave_int(kept.nch), wave_int(kept.cols)};
         const uint16_t *const gate_at = B->gate;
         const int64_t gate_row = B->gate_row, gate_head = B->gate_head;
-        const int first_col = E.rt * S::COLS + cw * 32 * T, hq = B->hq, chunks = B->chunks;
+        const int first_col = E.rt * S::COLS + wave * 32 * T, hq = B->hq, chunks = B->chunks;
         constexpr int FIT = S::BYTES / (WAVES / 2 * 32 * 4), CH = FIT < D ? FIT : D, PC = CH / 4, LPC = CH / 8;    // channels; pieces of a column; lanes that read it
         static_assert(CH >= 32 && D % CH == 0, "");
         uint8_t *mine = wave < WAVES / 2 ? st0 + wave * (32 * CH * 4) : st1 + (wave - WAVES / 2) * (32 * CH * 4);
@@ -653,7 +683,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                 if (E.nch == 1 && gate_at)
 #pragma unroll
                     for (int y = 0; y < RUNS; ++y) {
-                        const int2 p = pairs[cw * 32 * T + 32 * c + y * (64 / LPC) + ln / LPC];
+                        const int2 p = pairs[wave * 32 * T + 32 * c + y * (64 / LPC) + ln / LPC];
                         const uint16_t *from = gate_at + p.x * gate_row + p.y * gate_head + (part * CH + 8 * (ln % LPC));
                         gate[y][0] = reinterpret_cast<const uint2 *>(from)[0], gate[y][1] = reinterpret_cast<const uint2 *>(from)[1];
                     }
@@ -664,7 +694,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                     const float4 v = *reinterpret_cast<const float4 *>(mine + (n * PC + ((2 * x + 1) ^ (n & (PC - 1)))) * 16);
                     __builtin_amdgcn_sched_barrier(0);
                     if (first_col + 32 * c + n >= E.cols) continue;
-                    const int2 p = pairs[cw * 32 * T + 32 * c + n];
+                    const int2 p = pairs[wave * 32 * T + 32 * c + n];
                     const size_t pair = (size_t)p.x * hq + p.y;
                     if (E.nch == 1) {
                         const uint2 a = gated4(u, gate_at != nullptr, gate[y][0]), b = gated4(v, gate_at != nullptr, gate[y][1]);
