@@ -1120,15 +1120,16 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
     wait_vmem();      // no load may reach LDS that is no longer this workgroup's
 }
 
-// Merges a (row, head)'s chunks, one wave each, D / 64 channels a lane.  What it
-// reads does not wait for the stream to be found: the first parts, the sums and
-// the gates are asked for at once, by the row alone (a stream has at most
-// A.chunks chunks; what lies past its own is not used), and the streams' windows
-// are looked at 64 at a time.  The price: a (row, head) of a short stream asks for
-// more parts than it has.  The 16 trees above, the longest of which has 17 chunks
-// and ten of which have 4 to 6, ask for 58 MB where their chunks wrote 25, and the
-// kernel's 11 us are the time of those bytes.
+// Merges a (row, head)'s chunks, one wave each, D / 64 channels a lane.  Where all
+// parts are few bytes, what it reads does not wait for the stream to be found: the
+// first parts, the sums and the gates are asked for at once, by the row alone (a
+// stream has at most A.chunks chunks; what lies past its own is not used), and the
+// streams' windows are looked at 64 at a time.  Of many bytes, whose time it is
+// that the kernel takes, only those that are there: of the 16 trees above the longest
+// has 17 chunks and ten have 4 to 6, and asked for by the row alone they were 58 MB and
+// 12.2 us, where the 25 MB that the chunks wrote take 7.6.
 constexpr int kJoinWaves = 4, kJoinBatch = 16;      // loads in flight
+constexpr long long kJoinAtOnce = 16 << 20;        // bytes
 
 template <int D, bool PROMPT>
 __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const AttnArgs A, const int is_wide, const int split_keys)
@@ -1142,10 +1143,12 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const AttnArgs A,
     const int r = item / A.hq, head = item - r * A.hq;
     const size_t at = (size_t)item * A.chunks;
     const part_t *parts = reinterpret_cast<const part_t *>(A.part + at * D) + lane;
-    part_t b[kJoinBatch];
+    part_t b[kJoinBatch] = {};
+    const bool at_once = (long long)A.total_rows * A.hq * at_most(A.chunks, kJoinBatch) * (D * 4) <= kJoinAtOnce;
+    if (at_once)
 #pragma unroll
-    for (int i = 0; i < kJoinBatch; ++i)
-        if (i < A.chunks) b[i] = parts[(size_t)i * 64];
+        for (int i = 0; i < kJoinBatch; ++i)
+            if (i < A.chunks) b[i] = parts[(size_t)i * 64];
     static_assert(kMaxChunks == 64, "");
     float2 st = {-INFINITY, 0.0f};
     if (lane < A.chunks) st = A.stat[at + lane];
@@ -1197,7 +1200,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(const AttnArgs A,
     const float inv = 1.0f / sum_wave(st.y * f);
     part_t a = {};
     for (int c = 0; c < nch; c += kJoinBatch) {
-        if (c > 0)
+        if (c > 0 || !at_once)
 #pragma unroll
             for (int i = 0; i < kJoinBatch; ++i)
                 if (c + i < nch) b[i] = parts[(size_t)(c + i) * 64];
