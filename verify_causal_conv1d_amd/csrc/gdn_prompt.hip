@@ -497,11 +497,13 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
 #pragma unroll
                         for (int e = 0; e < 16; ++e) o[c][i][e] *= back;
                 }
+                float ps = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     s[e] = __builtin_amdgcn_exp2f(s[e]);
-                    sum[c] += s[e];
+                    ps += s[e];
                 }
+                sum[c] += ps;
                 if constexpr (FMT == FMT_E4M3) {
 #pragma unroll
                     for (int a = 0; a < 4; ++a) {
