@@ -49,7 +49,7 @@ __device__ __forceinline__ const_args *fresh_args()
 
 __device__ __forceinline__ float uniform(float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x))); }
 
-constexpr int kSub = 32;       // keys of a matrix instruction's tile
+constexpr int kKeys = 32;      // of a stage: a matrix instruction's tile
 constexpr int kAhead = 3;      // operands on their way from LDS
 
 // A stage of keys and values in LDS, in bf16: KEYS rows of K, then of V, in 16-byte
@@ -61,10 +61,10 @@ constexpr int kAhead = 3;      // operands on their way from LDS
 // of LDS hold every place as often as any other.  (Pieces in order, with the rows
 // exchanged as those of bf16: half of the LDS's busy cycles over 4 bits were
 // conflicts.)
-template <int D, int FMT, int WAVES, int TILES, int KEYS_>
+template <int D, int FMT, int WAVES>
 struct PromptShape {
-    static constexpr int THREADS = 64 * WAVES, COLS = 32 * TILES * WAVES;
-    static constexpr int KEYS = KEYS_, ROW = 2 * D, HALF = KEYS * ROW, BYTES = 2 * HALF;
+    static constexpr int THREADS = 64 * WAVES, COLS = 32 * WAVES;
+    static constexpr int KEYS = kKeys, ROW = 2 * D, HALF = KEYS * ROW, BYTES = 2 * HALF;
     static constexpr int PIECES = ROW / 16, ROWS = 1024 / ROW;    // of a direct load
     static constexpr int TURNS = FMT == FMT_BF16 ? 1 : FMT == FMT_E4M3 ? 2 : 4, LANES = PIECES / TURNS;     // of a row
     static __device__ __forceinline__ int k_place(int c) { return c % TURNS * LANES + c / TURNS; }
@@ -214,13 +214,12 @@ __device__ __forceinline__ uint2 gated4(float4 o, bool gated, uint2 g)
 __device__ __forceinline__ int wave_int(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ float not_finite(uint32_t bits) { return (bits & 0x7f800000u) == 0x7f800000u ? __uint_as_float(bits) : 0.0f; }
 
-template <int D, int FMT, int WAVES, int TILES, int KEYS, int PER_SIMD, bool WINDOW>
+template <int D, int FMT, int WAVES, int PER_SIMD, bool WINDOW>
 __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const AttnArgs A, const int split_keys)
 {
-    using S = PromptShape<D, FMT, WAVES, TILES, KEYS>;
-    constexpr int KS = D / 16, NT = D / 32, T = TILES;
-    constexpr int NK = S::HALF / 1024, PER = 2 * NK / WAVES;     // direct loads of a stage's keys; of a wave, in all
-    
+    using S = PromptShape<D, FMT, WAVES>;
+    constexpr int KS = D / 16, NT = D / 32;
+    constexpr int PER = 2 * S::HALF / 1024 / WAVES;     // direct loads of a wave
     // Operands of the queries that stay in LDS: with all of them in registers the
     // first three of e4m3 rows of 256 channels went to memory, and reading them back
     // waited for the rows on their way.
@@ -240,43 +239,30 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
     for (int item = blockIdx.x; find_piece<S::COLS, WINDOW>(A, split_keys, item, K); item += gridDim.x) {
         if (K.k0 >= K.k1) continue;                 // a chunk past all that the tile sees
         bool ok = true;
-        const int col0 = K.rt * S::COLS + wave * 32 * T;            // the wave's first column
+        const int col0 = K.rt * S::COLS + wave * 32;            // the wave's first column
         const bool busy = col0 < K.cols;                            // waves without columns only load
-        const int t_lo = min(col0, K.cols - 1) / A.group, t_hi = min(col0 + 32 * T, K.cols) - 1;   // rows of the wave
+        const int t_lo = min(col0, K.cols - 1) / A.group, t_hi = min(col0 + 32, K.cols) - 1;   // rows of the wave
         const int see_lo = K.kv + t_lo, see_hi = K.kv + t_hi / A.group;      // the last key that the first and the last one see
-        int row[T];
-#pragma unroll
-        for (int c = 0; c < T; ++c) {
-            const int col = min(col0 + 32 * c + n, K.cols - 1);     // past the last one: that one again, not stored
-            const int t = col / A.group;
-            row[c] = t;
-            pairs[wave * 32 * T + 32 * c + n] = make_int2(K.r0 + t, K.h * A.group + col - t * A.group);     // (both halves the same)
-            if constexpr (WINDOW) seen[wave * 32 * T + 32 * c + n] = seen_rows(A, K.r0, K.m, t, ok);
-        }
+        const int col = min(col0 + n, K.cols - 1);     // past the last one: that one again, not stored
+        const int row = col / A.group;
+        pairs[wave * 32 + n] = make_int2(K.r0 + row, K.h * A.group + col - row * A.group);     // (both halves the same)
+        if constexpr (WINDOW) seen[wave * 32 + n] = seen_rows(A, K.r0, K.m, row, ok);
         // place of a column's (row, head) in q and out
-        auto pair_of = [&](int c, int hq) {
-            const int2 p = pairs[wave * 32 * T + 32 * c + (this_lane() & 31)];
+        auto pair_of = [&](int hq) {
+            const int2 p = pairs[wave * 32 + (this_lane() & 31)];
             return (size_t)p.x * hq + p.y;
         };
         __builtin_amdgcn_wave_barrier();
-        bf8v q[T][KS];
+        bf8v q[KS];
+        const uint16_t *p = A.q + pair_of(A.hq) * D + 8 * (this_lane() >> 5);
 #pragma unroll
-        for (int c = 0; c < T; ++c) {
-            const uint16_t *p = A.q + pair_of(c, A.hq) * D + 8 * (this_lane() >> 5);
+        for (int k = 0; k < KS; ++k) q[k] = *reinterpret_cast<const bf8v *>(p + 16 * k);
+        f16v o[NT];
+        float mx = -INFINITY, sum = 0.0f;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) q[c][k] = *reinterpret_cast<const bf8v *>(p + 16 * k);
-        }
-        f16v o[T][NT];
-        float mx[T], sum[T];
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int c = 0; c < T; ++c) {
-            mx[c] = -INFINITY;
-            sum[c] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[c][i][e] = 0.0f;
-        }
+            for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
         // keys that every column of the workgroup sees
         const int all_see = WINDOW ? K.kv : K.kv + K.rt * S::COLS / A.group + 1;
 
@@ -386,25 +372,22 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
             }
         };
 
-        // 32 keys from `first`, rows sub * 32 .. of the stage.  tail: some column does not see all of them.
-        auto multiply = [&](bool tail, int first, int sub, const uint8_t *stage, const float *scales) {
-            f16v acc[T];
+        // The stage's keys, from `first`.  tail: some column does not see all of them.
+        auto multiply = [&](bool tail, int first, const uint8_t *stage, const float *scales) {
+            f16v s;
 #pragma unroll
-            for (int c = 0; c < T; ++c)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) acc[c][e] = 0.0f;
+            for (int e = 0; e < 16; ++e) s[e] = 0.0f;
 
             // Operands are read kAhead steps before the products that take them; the
             // first ones of the values before the weights are worked out.
             // piece 2 k + g of row n
             const int ln = this_lane(), kn = ln & 31;
-            const uint8_t *kr = stage + sub * kSub * S::ROW;
             const int k_at = kn * S::ROW + (S::k_place(ln >> 5) ^ S::k_swizzle(kn)) * 16;
-            auto key = [&](int k) { return *reinterpret_cast<const bf8v *>(kr + S::with_place(k_at, S::k_place(2 * k))); };
+            auto key = [&](int k) { return *reinterpret_cast<const bf8v *>(stage + S::with_place(k_at, S::k_place(2 * k))); };
             // the operand of channels 32 i .. and keys 16 t + 8 a + 4 g .. + 3 (a < 2),
             // transposed by the reads: this lane brings 4 channels of one of those keys
             const int l16 = ln & 15, vr = 4 * (ln >> 5) + (l16 >> 2), cb = ln >> 4 & 1;
-            const uint8_t *vp = stage + S::HALF + sub * kSub * S::ROW;
+            const uint8_t *vp = stage + S::HALF;
             const int v_at = vr * S::ROW + (l16 & 1) * 8 + (S::v_place(2 * cb + (l16 >> 1 & 1)) ^ S::v_swizzle(vr)) * 16;
             auto value = [&](int x) {
                 const int i = x >> 1, t = x & 1, at = S::with_place(v_at, S::v_place(4 * i)) + 16 * t * S::ROW;
@@ -414,7 +397,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
             // (e4m3 rows' scales: asked for ahead where registers are left)
             constexpr bool EARLY = FMT == FMT_E4M3 && D < 256;
             float4 ks[4], vs[4];
-            const float *scale_at = scales + sub * kSub + 4 * (ln >> 5);
+            const float *scale_at = scales + 4 * (ln >> 5);
             bf8v ring[kAhead + 1];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) ring[k] = key(k);
@@ -429,8 +412,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
 #pragma unroll
                         for (int a = 0; a < 4; ++a) ks[a] = *reinterpret_cast<const float4 *>(scale_at + 8 * a);
                 __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int c = 0; c < T; ++c) acc[c] = mfma32(ring[k % (kAhead + 1)], k < QL ? q_first[k < QL ? k : 0] : q[c][k], acc[c]);
+                s = mfma32(ring[k % (kAhead + 1)], k < QL ? q_first[k < QL ? k : 0] : q[k], s);
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
@@ -440,110 +422,101 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                 for (int a = 0; a < 4; ++a) vs[a] = *reinterpret_cast<const float4 *>(scale_at + S::KEYS + 8 * a);
             __builtin_amdgcn_sched_barrier(0);
             // lane (n, g) has of column n the keys 8 a + 4 g + b (a, b < 4) of the 32
-            bf8v pb[T][2];
+            bf8v pb[2];
+            // Any base within reach of the maximum does: scores are taken from the one
+            // that is there, and it moves, to 2^8 above the maximum, only when that has
+            // passed it.  (e4m3: the keys' scales in LDS have the call's in them.)
+            const bool unset = mx == -INFINITY;
+            const float base = unset ? 0.0f : mx;
+            if constexpr (FMT == FMT_E4M3) {
 #pragma unroll
-            for (int c = 0; c < T; ++c) {
-                f16v &s = acc[c];
-                // Any base within reach of the maximum does: scores are taken from the one
-                // that is there, and it moves, to 2^8 above the maximum, only when that has
-                // passed it.  (e4m3: the keys' scales in LDS have the call's in them.)
-                const bool unset = mx[c] == -INFINITY;
-                const float base = unset ? 0.0f : mx[c];
-                if constexpr (FMT == FMT_E4M3) {
-#pragma unroll
-                    for (int a = 0; a < 4; ++a) {
-                        float4 f;
-                        if constexpr (EARLY) {
-                            f = ks[a];
-                        } else {
-                            __builtin_amdgcn_sched_barrier(0);
-                            f = *reinterpret_cast<const float4 *>(scale_at + 8 * a);
-                        }
-                        s[4 * a] = fmaf(s[4 * a], f.x, -base), s[4 * a + 1] = fmaf(s[4 * a + 1], f.y, -base);
-                        s[4 * a + 2] = fmaf(s[4 * a + 2], f.z, -base), s[4 * a + 3] = fmaf(s[4 * a + 3], f.w, -base);
+                for (int a = 0; a < 4; ++a) {
+                    float4 f;
+                    if constexpr (EARLY) {
+                        f = ks[a];
+                    } else {
+                        __builtin_amdgcn_sched_barrier(0);
+                        f = *reinterpret_cast<const float4 *>(scale_at + 8 * a);
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) s[e] = fmaf(s[e], scale, -base);
+                    s[4 * a] = fmaf(s[4 * a], f.x, -base), s[4 * a + 1] = fmaf(s[4 * a + 1], f.y, -base);
+                    s[4 * a + 2] = fmaf(s[4 * a + 2], f.z, -base), s[4 * a + 3] = fmaf(s[4 * a + 3], f.w, -base);
                 }
-                const int from = first + (this_lane() >> 5) * 4 - K.kv;          // the lane's first key's place in the pass
-                // bit i: the lane's key i of the 32 (8 a + b), in a window
-                uint32_t in_sight = ~0u;
-                if constexpr (WINDOW)
-                    if (tail) {
-                        const uint32_t rows = seen[wave * 32 * T + 32 * c + (this_lane() & 31)];
-                        in_sight = from >= kMaxWindowRows ? 0 : from >= 0 ? rows >> from : from <= -32 ? ~0u : rows << -from | ~(~0u << -from);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[e] = fmaf(s[e], scale, -base);
+            }
+            const int from = first + (this_lane() >> 5) * 4 - K.kv;          // the lane's first key's place in the pass
+            // bit i: the lane's key i of the 32 (8 a + b), in a window
+            uint32_t in_sight = ~0u;
+            if constexpr (WINDOW)
+                if (tail) {
+                    const uint32_t rows = seen[wave * 32 + (this_lane() & 31)];
+                    in_sight = from >= kMaxWindowRows ? 0 : from >= 0 ? rows >> from : from <= -32 ? ~0u : rows << -from | ~(~0u << -from);
+                }
+            auto sees = [&](int e) {
+                const int at = 8 * (e / 4) + (e & 3);
+                return WINDOW ? (bool)(in_sight >> at & 1) : at <= row - from;
+            };
+            if (tail)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[e] = sees(e) ? s[e] : -INFINITY;
+            float top = fmaxf(s[0], s[1]);
+#pragma unroll
+            for (int e = 2; e < 16; ++e) top = fmaxf(top, s[e]);
+            top = max_halves(top);
+            const bool passed = top > (unset ? -INFINITY : 0.0f);
+            if (__ballot(passed)) {
+                const float by = passed ? top + 8.0f : 0.0f, back = __builtin_amdgcn_exp2f(mx - (base + by));
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[e] -= by;
+                if (passed) mx = base + by;
+                sum *= back;
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[i][e] *= back;
+            }
+            float ps = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                s[e] = __builtin_amdgcn_exp2f(s[e]);
+                ps += s[e];
+            }
+            sum += ps;
+            if constexpr (FMT == FMT_E4M3) {
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    float4 f;
+                    if constexpr (EARLY) {
+                        f = vs[a];
+                    } else {
+                        __builtin_amdgcn_sched_barrier(0);
+                        f = *reinterpret_cast<const float4 *>(scale_at + S::KEYS + 8 * a);
                     }
-                auto sees = [&](int e) {
-                    const int at = 8 * (e / 4) + (e & 3);
-                    return WINDOW ? (bool)(in_sight >> at & 1) : at <= row[c] - from;
-                };
-                if (tail)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) s[e] = sees(e) ? s[e] : -INFINITY;
-                float top = fmaxf(s[0], s[1]);
-#pragma unroll
-                for (int e = 2; e < 16; ++e) top = fmaxf(top, s[e]);
-                top = max_halves(top);
-                const bool passed = top > (unset ? -INFINITY : 0.0f);
-                if (__ballot(passed)) {
-                    const float by = passed ? top + 8.0f : 0.0f, back = __builtin_amdgcn_exp2f(mx[c] - (base + by));
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) s[e] -= by;
-                    if (passed) mx[c] = base + by;
-                    sum[c] *= back;
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[c][i][e] *= back;
+                    s[4 * a] *= f.x, s[4 * a + 1] *= f.y, s[4 * a + 2] *= f.z, s[4 * a + 3] *= f.w;
                 }
-                float ps = 0.0f;
+                if (tail)                  // a masked row's scale may be anything
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    s[e] = __builtin_amdgcn_exp2f(s[e]);
-                    ps += s[e];
-                }
-                sum[c] += ps;
-                if constexpr (FMT == FMT_E4M3) {
+                    for (int e = 0; e < 16; ++e) s[e] = sees(e) ? s[e] : 0.0f;
+            }
 #pragma unroll
-                    for (int a = 0; a < 4; ++a) {
-                        float4 f;
-                        if constexpr (EARLY) {
-                            f = vs[a];
-                        } else {
-                            __builtin_amdgcn_sched_barrier(0);
-                            f = *reinterpret_cast<const float4 *>(scale_at + S::KEYS + 8 * a);
-                        }
-                        s[4 * a] *= f.x, s[4 * a + 1] *= f.y, s[4 * a + 2] *= f.z, s[4 * a + 3] *= f.w;
-                    }
-                    if (tail)                  // a masked row's scale may be anything
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) s[e] = sees(e) ? s[e] : 0.0f;
-                }
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const uint4 x = {pack2(s[8 * t], s[8 * t + 1]), pack2(s[8 * t + 2], s[8 * t + 3]), pack2(s[8 * t + 4], s[8 * t + 5]),
-                                     pack2(s[8 * t + 6], s[8 * t + 7])};
-                    pb[c][t] = __builtin_bit_cast(bf8v, x);
-                }
+            for (int t = 0; t < 2; ++t) {
+                const uint4 x = {pack2(s[8 * t], s[8 * t + 1]), pack2(s[8 * t + 2], s[8 * t + 3]), pack2(s[8 * t + 4], s[8 * t + 5]),
+                                 pack2(s[8 * t + 6], s[8 * t + 7])};
+                pb[t] = __builtin_bit_cast(bf8v, x);
             }
 #pragma unroll
             for (int x = 0; x < 2 * NT; ++x) {
                 if (x + kAhead < 2 * NT) ring[(x + kAhead) % (kAhead + 1)] = value(x + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int c = 0; c < T; ++c) o[c][x >> 1] = mfma32(ring[x % (kAhead + 1)], pb[c][x & 1], o[c][x >> 1]);
+                o[x >> 1] = mfma32(ring[x % (kAhead + 1)], pb[x & 1], o[x >> 1]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
         auto compute = [&](int tile, const uint8_t *stage, const float *scales) {
             if (!busy) return;
-#pragma unroll 1
-            for (int sub = 0; sub < S::KEYS / kSub; ++sub) {
-                const int first = K.k0 + tile * S::KEYS + sub * kSub;
-                if (first >= K.k1 || (!WINDOW && first > see_hi)) break;
-                multiply(first + kSub > (WINDOW ? K.kv : see_lo + 1), first, sub, stage, scales);
-            }
+            const int first = K.k0 + tile * S::KEYS;
+            if (WINDOW || first <= see_hi) multiply(first + S::KEYS > (WINDOW ? K.kv : see_lo + 1), first, stage, scales);
         };
 
         // The first stage is on its way while the stream's pages are checked: entries
@@ -562,9 +535,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
         for (int w = 0; w < WAVES; ++w) ok = ok && wave_ok[w];
         if (!ok) {
             if (K.nch > 1 && g == 0)
-#pragma unroll
-                for (int c = 0; c < T; ++c)
-                    if (col0 + 32 * c + n < K.cols) A.stat[pair_of(c, A.hq) * A.chunks + K.c] = make_float2(0.0f, kSkipped);
+                if (col0 + n < K.cols) A.stat[pair_of(A.hq) * A.chunks + K.c] = make_float2(0.0f, kSkipped);
             wait_vmem();
             __syncthreads();
             continue;
@@ -579,15 +550,13 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
         if (A.scale <= 0.0f) {
             const uint32_t sign = A.scale < 0.0f ? 0x80008000u : 0u, keep = A.scale < 0.0f ? ~0u : 0u;
 #pragma unroll
-            for (int c = 0; c < T; ++c)
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    const uint4 x = __builtin_bit_cast(uint4, q[c][k]);
-                    q[c][k] = __builtin_bit_cast(bf8v, make_uint4((x.x & keep) ^ sign, (x.y & keep) ^ sign, (x.z & keep) ^ sign, (x.w & keep) ^ sign));
-                }
+            for (int k = 0; k < KS; ++k) {
+                const uint4 x = __builtin_bit_cast(uint4, q[k]);
+                q[k] = __builtin_bit_cast(bf8v, make_uint4((x.x & keep) ^ sign, (x.y & keep) ^ sign, (x.z & keep) ^ sign, (x.w & keep) ^ sign));
+            }
         }
 #pragma unroll
-        for (int k = 0; k < QL; ++k) q_lds[(wave * QL + k) * 64 + this_lane()] = __builtin_bit_cast(uint4, q[0][k]);
+        for (int k = 0; k < QL; ++k) q_lds[(wave * QL + k) * 64 + this_lane()] = __builtin_bit_cast(uint4, q[k]);
         auto step = [&](int tile, uint8_t *stage, float *scales, uint8_t *next, float *next_scales) {
             wait_and_meet<0>();
             if (tile + 1 < tiles) {
@@ -637,75 +606,72 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                                wave_int(kept.kv), wave_int(kept.len), wave_int(kept.k0), wave_int(kept.k1), wave_int(kept.nch), wave_int(kept.cols)};
         const uint16_t *const gate_at = B->gate;
         const int64_t gate_row = B->gate_row, gate_head = B->gate_head;
-        const int first_col = E.rt * S::COLS + wave * 32 * T, hq = B->hq, chunks = B->chunks;
+        const int first_col = E.rt * S::COLS + wave * 32, hq = B->hq, chunks = B->chunks;
         constexpr int FIT = S::BYTES / (WAVES / 2 * 32 * 4), CH = FIT < D ? FIT : D, PC = CH / 4, LPC = CH / 8;    // channels; pieces of a column; lanes that read it
         static_assert(CH >= 32 && D % CH == 0, "");
         uint8_t *mine = wave < WAVES / 2 ? st0 + wave * (32 * CH * 4) : st1 + (wave - WAVES / 2) * (32 * CH * 4);
         const int ln = this_lane(), en = ln & 31, eg = ln >> 5;
         const int sees = WINDOW ? E.kv : E.kv + E.rt * S::COLS / B->group + 1, bad_from = E.k0 + max(0, (sees - E.k0) / S::KEYS) * S::KEYS;       // the first stage that was looked at
+        const float l = sum_halves(sum);
+        if (E.nch > 1 && eg == 0 && first_col + en < E.cols) B->stat[pair_of(hq) * chunks + E.c] = make_float2(mx, l);
+        if (bad) {
+            for (int key = bad_from; key < E.k1; ++key) {
+                const int j = key - E.kv;
+                if (j >= 0 && !(WINDOW ? seen[first_col + en - E.rt * S::COLS] >> j & 1 : j <= row)) continue;
+                const int id = B->table[(size_t)E.s * B->max_blocks + (key >> B->kv.page_shift)];
+                const size_t at = (((size_t)id * B->kv.hkv + E.h) << B->kv.page_shift) + (key & ((1 << B->kv.page_shift) - 1));
 #pragma unroll
-        for (int c = 0; c < T; ++c) {
-            const float l = sum_halves(sum[c]);
-            if (E.nch > 1 && eg == 0 && first_col + 32 * c + en < E.cols) B->stat[pair_of(c, hq) * chunks + E.c] = make_float2(mx[c], l);
-            if (bad) {
-                for (int key = bad_from; key < E.k1; ++key) {
-                    const int j = key - E.kv;
-                    if (j >= 0 && !(WINDOW ? seen[first_col + 32 * c + en - E.rt * S::COLS] >> j & 1 : j <= row[c])) continue;
-                    const int id = B->table[(size_t)E.s * B->max_blocks + (key >> B->kv.page_shift)];
-                    const size_t at = (((size_t)id * B->kv.hkv + E.h) << B->kv.page_shift) + (key & ((1 << B->kv.page_shift) - 1));
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-#pragma unroll
-                        for (int a = 0; a < 4; ++a) {
-                            const uint2 w = cached_values4<D, FMT>(B->kv.v, B->kv.v_exp, at, 32 * i + 8 * a + 4 * eg);
-                            o[c][i][4 * a] += not_finite(w.x << 16), o[c][i][4 * a + 1] += not_finite(w.x & 0xffff0000u);
-                            o[c][i][4 * a + 2] += not_finite(w.y << 16), o[c][i][4 * a + 3] += not_finite(w.y & 0xffff0000u);
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
-                }
-            }
-            const float inv = E.nch == 1 ? 1.0f / l : 1.0f;
-#pragma unroll
-            for (int part = 0; part < D / CH; ++part) {
-                constexpr int RUNS = 32 * LPC / 64;
-                uint2 gate[RUNS][2];
-                if (c + part > 0) __builtin_amdgcn_wave_barrier();
-#pragma unroll
-                for (int i = 0; i < CH / 32; ++i)
+                for (int i = 0; i < NT; ++i)
 #pragma unroll
                     for (int a = 0; a < 4; ++a) {
-                        const f16v &x = o[c][part * (CH / 32) + i];
-                        *reinterpret_cast<float4 *>(mine + (en * PC + ((8 * i + 2 * a + eg) ^ (en & (PC - 1)))) * 16) =
-                            make_float4(x[4 * a] * inv, x[4 * a + 1] * inv, x[4 * a + 2] * inv, x[4 * a + 3] * inv);
+                        const uint2 w = cached_values4<D, FMT>(B->kv.v, B->kv.v_exp, at, 32 * i + 8 * a + 4 * eg);
+                        o[i][4 * a] += not_finite(w.x << 16), o[i][4 * a + 1] += not_finite(w.x & 0xffff0000u);
+                        o[i][4 * a + 2] += not_finite(w.y << 16), o[i][4 * a + 3] += not_finite(w.y & 0xffff0000u);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
-                __builtin_amdgcn_sched_barrier(0);
-                __builtin_amdgcn_wave_barrier();
+            }
+        }
+        const float inv = E.nch == 1 ? 1.0f / l : 1.0f;
 #pragma unroll
-                for (int y = 0; y < RUNS; ++y) gate[y][0] = gate[y][1] = make_uint2(0, 0);
-                if (E.nch == 1 && gate_at)
+        for (int part = 0; part < D / CH; ++part) {
+            constexpr int RUNS = 32 * LPC / 64;
+            uint2 gate[RUNS][2];
+            if (part > 0) __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                    for (int y = 0; y < RUNS; ++y) {
-                        const int2 p = pairs[wave * 32 * T + 32 * c + y * (64 / LPC) + ln / LPC];
-                        const uint16_t *from = gate_at + p.x * gate_row + p.y * gate_head + (part * CH + 8 * (ln % LPC));
-                        gate[y][0] = reinterpret_cast<const uint2 *>(from)[0], gate[y][1] = reinterpret_cast<const uint2 *>(from)[1];
-                    }
+            for (int i = 0; i < CH / 32; ++i)
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    const f16v &x = o[part * (CH / 32) + i];
+                    *reinterpret_cast<float4 *>(mine + (en * PC + ((8 * i + 2 * a + eg) ^ (en & (PC - 1)))) * 16) =
+                        make_float4(x[4 * a] * inv, x[4 * a + 1] * inv, x[4 * a + 2] * inv, x[4 * a + 3] * inv);
+                }
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int y = 0; y < RUNS; ++y) gate[y][0] = gate[y][1] = make_uint2(0, 0);
+            if (E.nch == 1 && gate_at)
 #pragma unroll
                 for (int y = 0; y < RUNS; ++y) {
-                    const int n = y * (64 / LPC) + ln / LPC, x = ln % LPC, d = part * CH + 8 * x;
-                    const float4 u = *reinterpret_cast<const float4 *>(mine + (n * PC + ((2 * x) ^ (n & (PC - 1)))) * 16);
-                    const float4 v = *reinterpret_cast<const float4 *>(mine + (n * PC + ((2 * x + 1) ^ (n & (PC - 1)))) * 16);
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (first_col + 32 * c + n >= E.cols) continue;
-                    const int2 p = pairs[wave * 32 * T + 32 * c + n];
-                    const size_t pair = (size_t)p.x * hq + p.y;
-                    if (E.nch == 1) {
-                        const uint2 a = gated4(u, gate_at != nullptr, gate[y][0]), b = gated4(v, gate_at != nullptr, gate[y][1]);
-                        *reinterpret_cast<uint4 *>(B->out + pair * D + d) = make_uint4(a.x, a.y, b.x, b.y);
-                    } else {
-                        float *to = B->part + (pair * chunks + E.c) * D + d;
-                        *reinterpret_cast<float4 *>(to) = u;
-                        *reinterpret_cast<float4 *>(to + 4) = v;
-                    }
+                    const int2 p = pairs[wave * 32 + y * (64 / LPC) + ln / LPC];
+                    const uint16_t *from = gate_at + p.x * gate_row + p.y * gate_head + (part * CH + 8 * (ln % LPC));
+                    gate[y][0] = reinterpret_cast<const uint2 *>(from)[0], gate[y][1] = reinterpret_cast<const uint2 *>(from)[1];
+                }
+#pragma unroll
+            for (int y = 0; y < RUNS; ++y) {
+                const int n = y * (64 / LPC) + ln / LPC, x = ln % LPC, d = part * CH + 8 * x;
+                const float4 u = *reinterpret_cast<const float4 *>(mine + (n * PC + ((2 * x) ^ (n & (PC - 1)))) * 16);
+                const float4 v = *reinterpret_cast<const float4 *>(mine + (n * PC + ((2 * x + 1) ^ (n & (PC - 1)))) * 16);
+                __builtin_amdgcn_sched_barrier(0);
+                if (first_col + n >= E.cols) continue;
+                const int2 p = pairs[wave * 32 + n];
+                const size_t pair = (size_t)p.x * hq + p.y;
+                if (E.nch == 1) {
+                    const uint2 a = gated4(u, gate_at != nullptr, gate[y][0]), b = gated4(v, gate_at != nullptr, gate[y][1]);
+                    *reinterpret_cast<uint4 *>(B->out + pair * D + d) = make_uint4(a.x, a.y, b.x, b.y);
+                } else {
+                    float *to = B->part + (pair * chunks + E.c) * D + d;
+                    *reinterpret_cast<float4 *>(to) = u;
+                    *reinterpret_cast<float4 *>(to + 4) = v;
                 }
             }
         }
@@ -713,17 +679,16 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
     }
 }
 
-template <int D, int FMT>
-struct PromptConfig {
-    static constexpr int WAVES = FMT == FMT_BF16 || D == 64 ? 4 : 8, KEYS = FMT == FMT_MXFP4 && D > 64 ? 64 : FMT == FMT_E4M3 && D == 128 ? 64 : 32;
-    static constexpr int PER_SIMD = D == 64 ? (FMT == FMT_E4M3 ? 3 : 4) : D == 128 && FMT == FMT_BF16 ? 3 : 2;
-};
+// Waves of a workgroup, that is columns that share what is loaded and converted, and
+// waves of a SIMD, that is registers of each.
+constexpr int prompt_waves(int d, int fmt) { return fmt == FMT_BF16 || d == 64 || (d == 128 && fmt == FMT_MXFP4) ? 4 : 8; }
+constexpr int prompt_per_simd(int d, int fmt) { return d == 64 ? (fmt == FMT_E4M3 ? 3 : 4) : d == 128 && fmt != FMT_E4M3 ? 3 : 2; }
 
 template <int D, int FMT>
 hipError_t launch_prompt_d(const AttnArgs &A, int split_keys, unsigned blocks, hipStream_t stream)
 {
-    using P = PromptConfig<D, FMT>;
-    prompt_kernel<D, FMT, P::WAVES, 1, P::KEYS, P::PER_SIMD, false><<<blocks, 64 * P::WAVES, 0, stream>>>(A, split_keys);
+    constexpr int WAVES = prompt_waves(D, FMT);
+    prompt_kernel<D, FMT, WAVES, prompt_per_simd(D, FMT), false><<<blocks, 64 * WAVES, 0, stream>>>(A, split_keys);
     return hipGetLastError();
 }
 
@@ -737,13 +702,11 @@ hipError_t launch_prompt_fmt(const AttnArgs &A, int split_keys, unsigned blocks,
     }
 }
 
-int prompt_waves(int d, int fmt) { return fmt == FMT_BF16 || d == 64 ? 4 : 8; }
 int prompt_cols(int d, int fmt) { return 32 * prompt_waves(d, fmt); }
 // workgroups that the chip holds at once
 int prompt_slots(int d, int fmt)
 {
-    const int per_simd = d == 64 ? (fmt == FMT_E4M3 ? 3 : 4) : d == 128 && fmt == FMT_BF16 ? 3 : 2;
-    return 256 * 4 * per_simd / prompt_waves(d, fmt);
+    return 256 * 4 * prompt_per_simd(d, fmt) / prompt_waves(d, fmt);
 }
 
 // Chunks of the longest stream: by the time that the call would take, in keys of a
@@ -798,9 +761,9 @@ hipError_t launch_wide4(const AttnArgs &A, long long pieces, hipStream_t stream)
 {
     const unsigned blocks = (unsigned)(pieces < 2048 ? pieces : 2048);
     switch (A.kv.d) {
-    case 64: prompt_kernel<64, FMT_MXFP4, 4, 1, 32, 2, true><<<blocks, 256, 0, stream>>>(A, 0); break;
-    case 128: prompt_kernel<128, FMT_MXFP4, 4, 1, 32, 2, true><<<blocks, 256, 0, stream>>>(A, 0); break;
-    default: prompt_kernel<256, FMT_MXFP4, 4, 1, 32, 2, true><<<blocks, 256, 0, stream>>>(A, 0); break;
+    case 64: prompt_kernel<64, FMT_MXFP4, 4, 2, true><<<blocks, 256, 0, stream>>>(A, 0); break;
+    case 128: prompt_kernel<128, FMT_MXFP4, 4, 2, true><<<blocks, 256, 0, stream>>>(A, 0); break;
+    default: prompt_kernel<256, FMT_MXFP4, 4, 2, true><<<blocks, 256, 0, stream>>>(A, 0); break;
     }
     return hipGetLastError();
 }
