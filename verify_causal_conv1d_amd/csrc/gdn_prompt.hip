@@ -680,8 +680,13 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
 }
 
 // Waves of a workgroup, that is columns that share what is loaded and converted, and
-// waves of a SIMD, that is registers of each.
-constexpr int prompt_waves(int d, int fmt) { return fmt == FMT_BF16 || d == 64 || (d == 128 && fmt == FMT_MXFP4) ? 4 : 8; }
+// waves of a SIMD, that is registers of each.  16,384 rows in 8 waves and in 4: 256
+// channels (24 query and 4 kv heads) in bf16 2,809 us and 2,974, over 4 bits 2,669 and
+// 2,858 (but 2,048 rows, which leave the chip part empty, 112 and 102, and 112 and 99);
+// 128 channels (32 and 8) in bf16 2,240 and 2,082, over 4 bits 2,255 and 2,176, in
+// e4m3 2,705 and 2,785, a resumed prompt 1,320 and 1,422: there what is converted
+// weighs most.
+constexpr int prompt_waves(int d, int fmt) { return d == 256 || (d == 128 && fmt == FMT_E4M3) ? 8 : 4; }
 constexpr int prompt_per_simd(int d, int fmt) { return d == 64 ? (fmt == FMT_E4M3 ? 3 : 4) : d == 128 && fmt != FMT_E4M3 ? 3 : 2; }
 
 template <int D, int FMT>
