@@ -106,8 +106,8 @@ struct PromptPiece {
 // of a head meet in as few XCDs as can be, and the tiles that see the most keys
 // come first, since workgroups begin in their order: of a stream its last rows,
 // and where a wave holds all streams and they are not cut into chunks, over all of
-// them (a prompt of 4,722 rows packed after shorter ones began too late to end
-// with them: 451 us and 373 in order).
+// them (a prompt of 4,722 rows packed after three shorter ones begins too late to end
+// with them: 391 us, and 375 in order).
 template <int COLS, bool WINDOW>
 __device__ __forceinline__ bool find_piece(const AttnArgs &A, int split_keys, int item, PromptPiece &K)
 {
@@ -717,11 +717,14 @@ int prompt_slots(int d, int fmt)
 // Chunks of the longest stream: by the time that the call would take, in keys of a
 // workgroup, if its longest stream were the only one.  A workgroup's beginning and
 // end cost as much as 160 keys, a chunk's parts 400 more, and the join 600.  What
-// limits the call is its longest piece, or all of them spread over the chip with
-// half a piece to end on where the pieces are alike, less where the last ones are
-// short; workgroups that have their CU to themselves are faster.  (24 query and 4
-// kv heads of 256: a fresh prompt of 2,048 rows takes 109 us whole and 124 in two
-// chunks, 512 rows over 32,000 cached keys 526 in 12 chunks.)
+// limits the call is its longest piece, or all of them spread over the chip and what
+// is left to end on: where the pieces are alike, since most of their keys are cached,
+// the rest of a last round (half a piece once the rounds are many), less where the
+// last ones are short.  Workgroups that have their CU to themselves are faster.  (24
+// query and 4 kv heads of 256 in bf16: a fresh prompt of 2,048 rows takes 114 us whole
+// and 143 in two chunks; 512 rows over 32,000 cached keys 1,492 us whole, 394 in 5
+// chunks, which are 240 pieces for the chip's 256 places, 463 in 8, 504 in 12 and
+// 452 in 16.)
 constexpr int kPromptRounds = 4;           // pieces of a call that is cut, in workgroups that the chip holds
 int most_chunks(int max_kv) { return at_most(kMaxChunks, max_kv / 256); }
 
@@ -732,8 +735,9 @@ int prompt_chunks(long long tiles, int slots, int total_rows, int max_kv)
     double least = 0;
     for (int c = 1; c == 1 || (c <= most_chunks(max_kv) && tiles * c <= (long long)kPromptRounds * slots); ++c) {
         const double parts = c > 1 ? 1 + (c - 1) * mean / keys : 0;       // of a mean tile
-        const double full = tiles * c < slots ? (double)(tiles * c) / slots : 1.0;
-        const double all = tiles * (mean + 160 + 400 * parts) / slots + (cached / 2 + (keys - cached) / 8) / c;
+        const double rounds = (double)(tiles * c) / slots, full = rounds < 1 ? rounds : 1.0;
+        const double left = rounds <= 1 ? 1 - rounds : rounds <= 2 ? 2 - rounds : 0.5;
+        const double all = tiles * (mean + 160 + 400 * parts) / slots + (left * cached + (keys - cached) / 8) / c;
         const double one = (keys / c + 160 + (c > 1 ? 400 : 0)) * (0.6 + 0.4 * full);
         const double cost = (all > one ? all : one) + (c > 1 ? 600 : 0);
         if (c == 1 || cost < least) best = c, least = cost;
