@@ -179,6 +179,22 @@ def test_peaked_scores_and_scales():
             close(c.run(scale=scale), *c.oracle(scale=scale))
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_scores_that_rise_and_fall(fmt):
+    """Each column's base has to move at every stage of keys, or never again after the first."""
+    for d, rising in ((64, True), (128, True), (256, True), (256, False)):
+        announce(f"scores that {'rise' if rising else 'fall'} along the keys, {fmt}, d {d}")
+        c = Case([700], [90], 4, 2, d, 64, fmt=fmt, seed=16)
+        x = 0.1 * torch.randn((c.pages, 2, 64, d), generator=c.g)
+        for j in range(-(-790 // 64)):
+            at = torch.arange(64 * j, 64 * j + 64) / 790.0
+            x[c.table[0, j]] += 8.0 * (at if rising else 1 - at)[None, :, None]
+        c.k, c.ks = made(x, fmt)
+        c.q = c.q.abs()
+        close(c.run(), *c.oracle())
+        close(c.run(scale=-0.05), *c.oracle(scale=-0.05))
+
+
 def test_values_near_the_types_largest():
     """Sums of weighted values overflow no sooner than the result does."""
     announce("prompts, values near the largest")

@@ -20,9 +20,11 @@
 // Two kernels, by the columns that a window can have (max_rows * G):
 //  - up to 16, attn_kernel: its four waves take tiles of 32 keys in turn, each
 //    straight from memory into the registers that feed the matrix
-//    instructions, and join through LDS;
+//    instructions, and join through LDS (over 4-bit rows attn4_kernel, whose tiles
+//    come by way of LDS);
 //  - more, attn_wide_kernel: each wave has a column tile of its own, and K and
-//    V pass through LDS once for all of them.
+//    V pass through LDS once for all of them (over 4-bit rows the kernel of
+//    prompts, with a window's masks).
 // (16 streams of 700 to 8,191 keys, 24 query and 4 kv heads of 256: with 24
 // columns the wide kernel takes 53 us and the other one, reading K and V once a
 // tile, 69; with 48 columns 59 and 97.  One stream of 500 keys and 18 columns:
@@ -500,7 +502,14 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
 // its own in LDS (16 bytes a lane, no registers, no barriers).  Codes
 // are converted as they are used: K in blocks of 32 channels, whose exponent is the
 // conversion's scale; of V a byte's two channels at once, then set beside the next
-// key's.  Two workgroups a CU (LDS).
+// key's.
+//
+// One stream of 262,143 keys (24 query and 4 kv heads of 256) takes 57 us, 5.0 TB/s:
+// memory.  16 streams of 1,000 to 16,384 take 32 us where their bytes are 20: 1,116
+// pieces of up to 256 keys on 512 places, each 5 us of loop and 7 of beginning and end
+// (chunks of 512: 30.6).  Loads through registers, as in attn_kernel: 70 and 37.  Three
+// workgroups a CU and a ring of one tile: 55 registers of a lane go to memory, 240 and 64.
+
 // A direct load into LDS, 16 bytes a lane, lane after lane from byte `to` on (at is
 // the wave's, off the lane's).  The compiler is not told what it is: it would wait
 // for all of a ring's loads before the first read, where the kernel waits itself
@@ -630,7 +639,6 @@ __device__ __forceinline__ void add_values4(Column<D, false> &C, const Values4<D
         C.o[2 * b + 1] = mfma(c, rest, mfma(c, pb, C.o[2 * b + 1]));
     }
 }
-
 
 constexpr int kWaves4 = 4, kThreads4 = 64 * kWaves4;
 

@@ -7,8 +7,6 @@
 #include "gdn_device.h"
 #include "gdn_internal.h"
 
-#include <type_traits>
-
 namespace gdn {
 
 constexpr int kTile = 32;                  // keys of a wave's step
