@@ -730,13 +730,13 @@ static void launch_prep_d(const PrepArgs &A, hipStream_t stream)
     const int heads = A.hq + 2 * A.kv.hkv, at_once = kPrepThreads / (D / 8);
     const int span = A.rows <= kPrepFewRows && heads > at_once ? at_once : heads;
     const dim3 grid(A.rows, (heads + span - 1) / span);
+    const long long keys = ((long long)A.rows * A.kv.hkv + at_once - 1) / at_once;
     if (!A.kv.k_exp) {
         prep_kernel<D, PREP_ROWS><<<grid, kPrepThreads, 0, stream>>>(A, span);
-    } else if (A.rows <= kPrepFewRows) {
+    } else if (A.rows <= kPrepFewRows || A.rows + keys > kMaxGroups) {
         prep_kernel<D, PREP_MX><<<grid, kPrepThreads, 0, stream>>>(A, span);
     } else {
         const size_t lds = sizeof(double) * (D + at_once * key_swap(A.rot) + key_rows(at_once, A.kv.hkv) * A.rot);
-        const long long keys = ((long long)A.rows * A.kv.hkv + at_once - 1) / at_once;
         prep_kernel<D, PREP_MX_APART><<<(unsigned)(A.rows + keys), kPrepThreads, lds, stream>>>(A, heads);
     }
 }
