@@ -799,8 +799,8 @@ __global__ __launch_bounds__(kThreads4, 2) void attn4_kernel(const AttnArgs A)
 // rows of an operand lie in different banks.
 //
 // One workgroup of 8 waves stays on each CU and goes through its pieces.  16
-// draft trees of up to 16 rows over 700 to 8,191 keys (96 columns, 212 MB): 70 us
-// with the join (11 us, what bounds it is said there).  A tile of 32 keys
+// draft trees of up to 16 rows over 700 to 8,191 keys (96 columns, 212 MB): 66 us
+// with the join (7.5 us).  A tile of 32 keys
 // takes a CU about 1.2 us when nothing else runs there (each wave reads the
 // tile's 32 KB from LDS, and two of the waves with columns share a SIMD); how
 // evenly the pieces fall on the CUs costs the rest.  Over e4m3 rows (110 MB) they
