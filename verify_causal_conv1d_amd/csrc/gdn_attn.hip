@@ -505,9 +505,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
 // key's.
 //
 // One stream of 262,143 keys (24 query and 4 kv heads of 256) takes 57 us, 5.0 TB/s:
-// memory.  16 streams of 1,000 to 16,384 take 32 us where their bytes are 20: 1,116
-// pieces of up to 256 keys on 512 places, each 5 us of loop and 7 of beginning and end
-// (chunks of 512: 30.6).  Loads through registers, as in attn_kernel: 70 and 37.  Three
+// memory.  16 streams of 1,000 to 16,384 take 29 us where their bytes are 20: 1,116
+// pieces of up to 256 keys on 512 places, each 5 us of loop and 6 of beginning and end
+// (the queries through registers: 32).  Loads through registers, as in attn_kernel: 70 and 37.  Three
 // workgroups a CU and a ring of one tile: 55 registers of a lane go to memory, 240 and 64.
 
 // A direct load into LDS, 16 bytes a lane, lane after lane from byte `to` on (at is
@@ -669,11 +669,20 @@ __global__ __launch_bounds__(kThreads4, 2) void attn4_kernel(const AttnArgs A)
         const int id = table_entry(table, key >> A.kv.page_shift);
         return ((((uint32_t)id < (uint32_t)A.kv.n_pages ? id : 0) * A.kv.hkv + K.h) << A.kv.page_shift) + (key & ((1 << A.kv.page_shift) - 1));
     };
+    const uint32_t q_at = __builtin_amdgcn_readfirstlane(lds_at(reinterpret_cast<const uint8_t *>(q_lds)));
     auto issue = [&](int tile, uint8_t *ring) {
         const int key = K.k0 + tile * kTile;
         S::load(A.kv, __builtin_amdgcn_readfirstlane(lds_at(ring)) + wave * S::BYTES, group_row(key), group_row(key + 16), lane);
     };
-    // the chunk's pages
+    // The queries, in the order of the lanes' operands (past the last column the last
+    // one's), on their way while the chunk's pages are looked at
+#pragma unroll
+    for (int s = 0; s < S::STEPS; ++s) {
+        if (s % kWaves4 != wave) continue;
+        const int col = col0 + min(n, ncol - 1);
+        const uint16_t *p = A.q + ((size_t)col_row(A, K, col) * A.hq + col_head(A, K, col)) * D + S::channel(s, g);
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(q_at + s * 1024) : "memory");
+    }
     bool ok = true;
     for (int i = (K.k0 >> A.kv.page_shift) + tid; i <= (K.k1 - 1) >> A.kv.page_shift; i += kThreads4) {
         const int id = table[i];
@@ -681,18 +690,13 @@ __global__ __launch_bounds__(kThreads4, 2) void attn4_kernel(const AttnArgs A)
     }
     ok = !__ballot(!ok);
     const uint32_t seen = seen_rows(A, K.r0, K.m, min(small_div(col0 + n, A.group), K.m - 1), ok);
-    // the queries, in the order of the lanes' operands (zero past the last column)
-    for (int i = tid; i < S::STEPS * 64; i += kThreads4) {
-        const int qc = i & 15, qg = i >> 4 & 3, s = i >> 6;
-        uint4 x = {0, 0, 0, 0};
-        if (qc < ncol)
-            x = *reinterpret_cast<const uint4 *>(A.q + ((size_t)col_row(A, K, col0 + qc) * A.hq + col_head(A, K, col0 + qc)) * D + S::channel(s, qg));
-        q_lds[i] = x;
-    }
     if (lane == 0) ok_lds[wave] = ok;
     if (tid == 0) bad_lds = 0;
     if (tid < kCols) seen_lds[tid] = seen;
-    // (the waits for what came before are over, and none of them waits for these)
+    // (the queries have come: the waits for what came before end here)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    asm volatile("" ::: "memory");
     if (wave < tiles) issue(wave, ring0);
     if (wave + kWaves4 < tiles) issue(wave + kWaves4, ring1);
     lds_barrier();
