@@ -697,37 +697,41 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
 // Waves of a workgroup, that is columns that share what is loaded and converted, and
 // waves of a SIMD, that is registers of each.  16,384 rows in 8 waves and in 4: 256
 // channels (24 query and 4 kv heads) in bf16 2,809 us and 2,974, over 4 bits 2,669 and
-// 2,858 (but 2,048 rows, which leave the chip part empty, 112 and 102, and 112 and 99);
-// 128 channels (32 and 8) in bf16 2,240 and 2,082, over 4 bits 2,255 and 2,176, in
-// e4m3 2,705 and 2,785, a resumed prompt 1,320 and 1,422: there what is converted
-// weighs most.
+// 2,858; 128 channels (32 and 8) in bf16 2,240 and 2,082, over 4 bits 2,255 and
+// 2,176, in e4m3 2,705 and 2,785, a resumed prompt 1,320 and 1,422: there what is
+// converted weighs most.  Of 256 channels both are here, for calls that leave some of
+// the chip empty (prompt_plan): 2,048 fresh rows in bf16 119 and 111 us, over 4 bits
+// 125 and 110, 1,024 rows 68 and 60, 64 rows 21 and 18; over cached rows, where pieces
+// are cut to fill the chip, 512 rows over 32,000 in 4 bits 414 and 455.
 constexpr int prompt_waves(int d, int fmt) { return d == 256 || (d == 128 && fmt == FMT_E4M3) ? 8 : 4; }
+constexpr bool prompt_has_both(int d, int fmt) { return d == 256 && fmt != FMT_E4M3; }        // (e4m3: queries in LDS)
 constexpr int prompt_per_simd(int d, int fmt) { return d == 64 ? (fmt == FMT_E4M3 ? 3 : 4) : d == 128 && fmt != FMT_E4M3 ? 3 : 2; }
 
 template <int D, int FMT>
-hipError_t launch_prompt_d(const AttnArgs &A, int split_keys, unsigned blocks, hipStream_t stream)
+hipError_t launch_prompt_d(const AttnArgs &A, int split_keys, int waves, unsigned blocks, hipStream_t stream)
 {
-    constexpr int WAVES = prompt_waves(D, FMT);
-    prompt_kernel<D, FMT, WAVES, prompt_per_simd(D, FMT), false><<<blocks, 64 * WAVES, 0, stream>>>(A, split_keys);
+    constexpr int WAVES = prompt_waves(D, FMT), PER_SIMD = prompt_per_simd(D, FMT);
+    if constexpr (prompt_has_both(D, FMT))
+        if (waves == 4) {
+            prompt_kernel<D, FMT, 4, PER_SIMD, false><<<blocks, 256, 0, stream>>>(A, split_keys);
+            return hipGetLastError();
+        }
+    prompt_kernel<D, FMT, WAVES, PER_SIMD, false><<<blocks, 64 * WAVES, 0, stream>>>(A, split_keys);
     return hipGetLastError();
 }
 
 template <int D>
-hipError_t launch_prompt_fmt(const AttnArgs &A, int split_keys, unsigned blocks, hipStream_t stream)
+hipError_t launch_prompt_fmt(const AttnArgs &A, int split_keys, int waves, unsigned blocks, hipStream_t stream)
 {
     switch (format_of(A.kv)) {
-    case FMT_BF16: return launch_prompt_d<D, FMT_BF16>(A, split_keys, blocks, stream);
-    case FMT_E4M3: return launch_prompt_d<D, FMT_E4M3>(A, split_keys, blocks, stream);
-    default: return launch_prompt_d<D, FMT_MXFP4>(A, split_keys, blocks, stream);
+    case FMT_BF16: return launch_prompt_d<D, FMT_BF16>(A, split_keys, waves, blocks, stream);
+    case FMT_E4M3: return launch_prompt_d<D, FMT_E4M3>(A, split_keys, waves, blocks, stream);
+    default: return launch_prompt_d<D, FMT_MXFP4>(A, split_keys, waves, blocks, stream);
     }
 }
 
-int prompt_cols(int d, int fmt) { return 32 * prompt_waves(d, fmt); }
 // workgroups that the chip holds at once
-int prompt_slots(int d, int fmt)
-{
-    return 256 * 4 * prompt_per_simd(d, fmt) / prompt_waves(d, fmt);
-}
+int prompt_slots(int d, int fmt, int waves) { return 256 * 4 * prompt_per_simd(d, fmt) / waves; }
 
 // Chunks of the longest stream: by the time that the call would take, in keys of a
 // workgroup, if its longest stream were the only one.  A workgroup's beginning and
@@ -736,8 +740,8 @@ int prompt_slots(int d, int fmt)
 // is left to end on: where the pieces are alike, since most of their keys are cached,
 // the rest of a last round (half a piece once the rounds are many), less where the
 // last ones are short.  Workgroups that have their CU to themselves are faster.  (24
-// query and 4 kv heads of 256 in bf16: a fresh prompt of 2,048 rows takes 114 us whole
-// and 143 in two chunks; 512 rows over 32,000 cached keys 1,492 us whole, 394 in 5
+// query and 4 kv heads of 256 in bf16, 8 waves: a fresh prompt of 2,048 rows takes 114 us
+// whole and 143 in two chunks; 512 rows over 32,000 cached keys 1,492 us whole, 394 in 5
 // chunks, which are 240 pieces for the chip's 256 places, 463 in 8, 504 in 12 and
 // 452 in 16.)
 constexpr int kPromptRounds = 4;           // pieces of a call that is cut, in workgroups that the chip holds
@@ -761,15 +765,20 @@ int prompt_chunks(long long tiles, int slots, int total_rows, int max_kv)
 }
 
 struct PromptPlan {
-    int chunks, split_keys;
+    int waves, chunks, split_keys;
     long long blocks;
 };
 long long prompt_tiles(int hq, int hkv, int cols, long long total_rows) { return (total_rows * (hq / hkv) + cols - 1) / cols * hkv; }
 PromptPlan prompt_plan(int hq, int hkv, int d, int fmt, int n_streams, int total_rows, int max_kv)
 {
-    const int cols = prompt_cols(d, fmt), rows = n_streams < total_rows ? n_streams : total_rows;
+    const int rows = n_streams < total_rows ? n_streams : total_rows;
     PromptPlan P;
-    P.chunks = prompt_chunks(prompt_tiles(hq, hkv, cols, total_rows), prompt_slots(d, fmt), total_rows, max_kv);
+    P.waves = prompt_waves(d, fmt);
+    // prompts that are mostly fresh and leave some of the chip empty: twice the workgroups
+    if (prompt_has_both(d, fmt) && max_kv / 2 <= total_rows && prompt_tiles(hq, hkv, 32 * P.waves, total_rows) <= prompt_slots(d, fmt, P.waves))
+        P.waves = 4;
+    const int cols = 32 * P.waves;
+    P.chunks = prompt_chunks(prompt_tiles(hq, hkv, cols, total_rows), prompt_slots(d, fmt, P.waves), total_rows, max_kv);
     P.split_keys = ceil_div(ceil_div(max_kv, P.chunks), 64) * 64;
     P.blocks = ((long long)total_rows * (hq / hkv) / cols + rows) * hkv * P.chunks;       // at most
     return P;
@@ -806,7 +815,7 @@ size_t prompt_workspace_most(int hq, int d, int total_rows, int max_kv)
     if (chunks <= 1) return 0;
     size_t pairs = 0;
     for (int fmt : {FMT_BF16, FMT_E4M3, FMT_MXFP4}) {
-        const size_t held = (size_t)kPromptRounds * prompt_slots(d, fmt) * prompt_cols(d, fmt);
+        const size_t held = (size_t)kPromptRounds * prompt_slots(d, fmt, 4) * 32 * 4;      // (with 8 waves the same)
         pairs = held > pairs ? held : pairs;
     }
     const size_t all = (size_t)total_rows * hq * chunks;
@@ -828,9 +837,9 @@ hipError_t launch_prompt(AttnArgs A, void *workspace, hipStream_t stream)
     A.stat = reinterpret_cast<float2 *>(A.part + (size_t)A.total_rows * A.hq * A.chunks * A.kv.d);
     hipError_t rc;
     switch (A.kv.d) {
-    case 64: rc = launch_prompt_fmt<64>(A, P.split_keys, (unsigned)P.blocks, stream); break;
-    case 128: rc = launch_prompt_fmt<128>(A, P.split_keys, (unsigned)P.blocks, stream); break;
-    default: rc = launch_prompt_fmt<256>(A, P.split_keys, (unsigned)P.blocks, stream); break;
+    case 64: rc = launch_prompt_fmt<64>(A, P.split_keys, P.waves, (unsigned)P.blocks, stream); break;
+    case 128: rc = launch_prompt_fmt<128>(A, P.split_keys, P.waves, (unsigned)P.blocks, stream); break;
+    default: rc = launch_prompt_fmt<256>(A, P.split_keys, P.waves, (unsigned)P.blocks, stream); break;
     }
     if (rc != hipSuccess || A.chunks == 1) return rc;
     return launch_join(A, true, P.split_keys, stream);
