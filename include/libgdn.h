@@ -485,10 +485,10 @@ int gdn_attn_window(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_
  * rounding).  A call of few rows over long streams is cut along the keys, by
  * total_rows, max_kv, the heads and the cache's format alone; given these, a
  * stream's results depend on neither the other streams nor its place in the call,
- * bit for bit.  A row
- * takes nothing from rows that it does not see, whatever they hold.  Streams of a
- * row or two are taken, but each has tiles of 128 or 256 (row, head) pairs to
- * itself: steps belong into gdn_attn_window.  total_rows * hq <= 2^26 - 4.
+ * bit for bit.  A row takes nothing from rows that it does not see, whatever they
+ * hold.  Streams of a row or two are taken, but each has tiles of 128 or 256 (row,
+ * head) pairs to itself: steps belong into gdn_attn_window.
+ * total_rows * hq <= 2^26 - 4.
  */
 size_t gdn_attn_prompt_workspace_bytes(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,
                                        int32_t max_kv, int32_t hq);

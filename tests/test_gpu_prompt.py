@@ -139,6 +139,9 @@ PROMPTS = [
     dict(lens=[17], rows=[70], hq=256, hkv=256, d=64, page=16, spare=1),
     dict(lens=[0, 300, 40], rows=[300, 129, 1], hq=3, hkv=3, d=128, page=16, gap=5),
     dict(lens=[1000, 0], rows=[257, 700], hq=2, hkv=2, d=256, page=64),
+    # mostly cached rows, in one chunk
+    dict(lens=[300, 17, 399, 0], rows=[100, 3, 1, 0], hq=6, hkv=1, d=256, page=32, gate=True),
+    dict(lens=[350, 200], rows=[60, 90], hq=12, hkv=2, d=256, page=128),
 ]
 
 
