@@ -17,9 +17,9 @@
 // a wave's 32 keys are 32 matrix instructions and about 110 others.  16,384 rows of
 // 24 query and 4 kv heads of 256 take 2.81 ms in bf16 (1,175 TFLOP/s), 2.67 to 2.73
 // over 4-bit rows (1,207 to 1,236) and 3.13 over e4m3 rows (1,052), whose scales
-// are two more multiplications of every weight; of 32 and 8 heads of 128 1,056, 1,087 and 811
-// TFLOP/s, of 64 876, 823 and 655, as there are half and a quarter as many products to
-// a weight.  (A product of two 8,192 x 8,192 matrices reaches 1,255 on the same card.)
+// are two more multiplications of every weight; of 32 and 8 heads of 128 1,056, 1,087 and
+// 832 TFLOP/s, of 64 876, 823 and 665, as there are half and a quarter as many products
+// to a weight.  (A product of two 8,192 x 8,192 matrices reaches 1,254 on the same card.)
 #include "gdn_attn_core.h"
 #include "gdn_mxfp4.h"
 
@@ -573,8 +573,15 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
 #pragma unroll
         for (int k = 0; k < QL; ++k) q_lds[(wave * QL + k) * 64 + this_lane()] = __builtin_bit_cast(uint4, q[k]);
         auto step = [&](int tile, uint8_t *stage, float *scales, uint8_t *next, float *next_scales) {
-            wait_and_meet<0>();
-            if (tile + 1 < tiles) {
+            // Over e4m3 rows of up to 128 channels half of the waves convert the next stage
+            // before they multiply this one, the other half afterwards: while one of two
+            // waves of a SIMD keeps the vector unit busy, the other has the matrix unit (a
+            // resumed prompt of 32 and 8 heads of 128 1,320 and 1,288 us; the other rows,
+            // which are converted in fewer steps, gain nothing, or lose 2 %).
+            constexpr bool HALVES = FMT == FMT_E4M3 && D < 256;
+            const bool late = HALVES && wave >= WAVES / 2;
+            auto bring = [&] {
+                if (tile + 1 >= tiles) return;
                 if constexpr (FMT == FMT_BF16) {
                     load(next);
                     look(tile + 2);
@@ -583,7 +590,10 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                     load(nullptr);
                     look(tile + 3);
                 }
-            }
+            };
+            if constexpr (HALVES) lds_barrier();
+            else wait_and_meet<0>();
+            if (!late) bring();
             // 0 * inf is NaN: a stage with keys that some column does not see (or past
             // the stream's end) has its values that are not finite left out, to be added
             // at the end to the columns that see them (a carry into bits 15 and 31 marks
@@ -607,6 +617,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                 lds_barrier();
             }
             compute(tile, stage, scales);
+            if (late) bring();
         };
         for (int tile = 0; tile < tiles; tile += 2) {
             step(tile, st0, sc0, st1, sc1);
