@@ -193,6 +193,14 @@ def test_many_streams():
         close(c.run(), *c.oracle())
 
 
+def test_parts_of_many_bytes():
+    """More than 16 MB of parts, which the join asks for once it knows each stream's chunks: one to seven of them."""
+    announce("24 trees over 4 bits, 19 MB of parts")
+    lens = [3 + 137 * s for s in range(24)]
+    c = Windows(lens, [16 - s % 3 for s in range(24)], 16, 1, 128, 64, tree=True, gate=True, seed=27)
+    close(c.run(), *c.oracle())
+
+
 def test_offsets_past_32_bits():
     announce("windows and a commit over 4 bits, 5 GiB pools")
     pages = (5 << 30) // (2 * 64 * 128)

@@ -173,6 +173,14 @@ def test_calls_cut_along_the_keys(lens, rows, hq, hkv, d, page, fmt):
     close(c.run(), *c.oracle())
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_parts_of_many_bytes(fmt):
+    """As above, with parts of more than 16 MB, which the join asks for once it knows the stream."""
+    announce(f"prompts with many parts, {fmt}")
+    c = Case([12000, 30, 2500, 0], [250, 20, 130, 9], 16, 1, 128, 64, fmt=fmt, seed=8, gate=True)
+    close(c.run(), *c.oracle())
+
+
 def test_peaked_scores_and_scales():
     for d, fmt in ((64, "bf16"), (256, "mxfp4"), (128, "e4m3")):
         announce(f"prompts, peaked rows, given scales, d {d} {fmt}")
