@@ -332,6 +332,24 @@ def test_broken_streams_are_skipped(lens, rows):
         assert torch.isnan(got[a]).all() if s == longest else torch.isfinite(got[a]).all()
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows", [[300, 50, 150], [300, 0, 150]])
+def test_finished_streams_of_any_length(rows, fmt):
+    """A kv_len below 0 marks a finished stream, with rows or without, down to the type's
+    lowest value: the streams beside it keep their bits.  (Not cut along the keys, so that
+    tiles go by length over all streams.)"""
+    announce(f"finished prompts {rows} {fmt}")
+    c = Case([0, 30, 20], rows, 6, 2, 64, 16, fmt=fmt, seed=40)
+    good = c.run()
+    a, b = int(c.row_start[1]), int(c.row_start[2])
+    for value in (-1, -1000, -2 ** 30, -2 ** 31 + 470, -2 ** 31 + 5, -2 ** 31):
+        kv = c.kv_len.clone()
+        kv[1] = value
+        got = c.run(kv_len=kv)
+        assert torch.equal(got[:a], good[:a]) and torch.equal(got[b:], good[b:]), value
+        assert torch.isnan(got[a:b]).all(), value
+
+
 def test_many_streams():
     """More streams than a wave looks at together, among them some without rows."""
     g = torch.Generator().manual_seed(25)

@@ -134,6 +134,8 @@ __device__ __forceinline__ bool find_piece(const AttnArgs &A, int split_keys, in
             size = WINDOW ? chunk_keys(kv + m, true) : split_keys;
             tiles = ceil_div(m * A.group, COLS);
             count = tiles * ceil_div(kv + m, size) * A.kv.hkv;
+        } else {
+            kv = 0;         // a skipped stream's may be anything, down to where a level less it overflows
         }
         const int incl = wave_running_sum(count), all = __builtin_amdgcn_readlane(incl, 63);
         if (item >= all) {
