@@ -334,6 +334,37 @@ def test_every_code_under_every_exponent():
             assert np.array_equal(f64(out)[2:], want[2:], equal_nan=True)
 
 
+def test_the_least_exponent_reads_exactly():
+    """Under e = 1 the code of 0.5 is 2^-127, below the least normal number and a bf16 number all the same."""
+    announce("4-bit codes under the least exponent")
+    e = torch.ones((1, 1, 16, 2), dtype=U8, device="cuda")
+    k = torch.arange(256, dtype=U8).view(1, 1, 8, 32)
+    kc, vc = (torch.cat([x, x], 2).cuda() for x in (k, k.flip(3)))
+    ko, vo = (torch.zeros((16, 1, 64), dtype=BF16, device="cuda") for _ in "kv")
+    gdn.kv_read(i32([0, 16]), i32([0]), i32([[0]]), kc, vc, ko, vo, k_scale=e, v_scale=e)
+    torch.cuda.synchronize()
+    for pool, out in ((kc, ko), (vc, vo)):
+        assert np.array_equal(f64(out)[:, 0], ref.mx_values(pool.cpu().numpy(), e.cpu().numpy())[0, 0])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_keys_under_the_least_exponent(d):
+    """Keys of 0 and +-2^-127 only, and queries large enough that they decide the weights."""
+    for kind, rows, hq in ((Windows, [1, 2], 4), (Windows, [9, 16], 12), (Case, [40, 3], 6)):
+        announce(f"keys of 2^-127, d {d}, rows {rows}")
+        c = kind([70, 333], rows, hq, 2, d, 16, fmt="mxfp4", seed=41)
+        code = torch.tensor([0x0, 0x1, 0x9])[torch.randint(0, 3, (*c.k.shape[:3], d), generator=c.g)]
+        c.k = (code[..., 0::2] | code[..., 1::2] << 4).to(U8)
+        c.ks = torch.where(c.ks == 255, 255, 1).to(U8)
+        c.q = (torch.randn(c.q.shape, generator=c.g).clamp(-3.5, 3.5) * 2.0 ** 125).to(BF16)
+        scale = 8.0 * d ** -0.5
+        want, bound = c.oracle(scale=scale)
+        close(c.run(scale=scale), want, bound)
+        c.q = torch.zeros_like(c.q)           # and not within the bound of what they are without them
+        flat, _ = c.oracle(scale=scale)
+        assert (np.abs(want - flat) > 2 * bound).mean() > 0.5
+
+
 # ---- commits -----------------------------------------------------------------------
 
 def test_commit_moves_rows_and_exponents():
