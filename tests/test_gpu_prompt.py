@@ -350,6 +350,29 @@ def test_finished_streams_of_any_length(rows, fmt):
         assert torch.isnan(got[a:b]).all(), value
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("scale", [0.0, 0.1, -0.1])
+def test_queries_that_are_not_finite(fmt, scale):
+    """They make their row and head NaN under any scale, 0 too (0 * infinity), and no other."""
+    announce(f"queries that are not finite, {fmt}, scale {scale}")
+    for d in (64, 128, 256):
+        c = Case([70, 1300], [5, 9], 6, 2, d, 16, fmt=fmt, seed=42)
+        clean = c.run(scale=scale)
+        close(clean, *c.oracle(scale=scale))
+        for value in (float("nan"), float("inf"), float("-inf")):
+            keep = c.q.clone()
+            c.q[1, 3, 5] = c.q[7, 0, d - 1] = value
+            got = c.run(scale=scale)
+            c.q = keep
+            hit = torch.zeros((c.total, 6), dtype=torch.bool)
+            hit[1, 3] = hit[7, 0] = True
+            assert torch.equal(got[~hit], clean[~hit]), (d, value)
+            if scale == 0.0 or value != value:
+                assert torch.isnan(got[hit]).all(), (d, value)
+            else:
+                assert not torch.isfinite(got[hit]).any(), (d, value)
+
+
 def test_many_streams():
     """More streams than a wave looks at together, among them some without rows."""
     g = torch.Generator().manual_seed(25)

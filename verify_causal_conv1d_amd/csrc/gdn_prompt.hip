@@ -251,7 +251,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
     __shared__ uint32_t seen[WINDOW ? S::COLS : 1];      // rows of a window that each column sees
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 31, g = lane >> 5;
-    const float scale = uniform(A.scale == 0.0f ? 1.0f : fabsf(A.scale));
+    const float scale = uniform(A.scale);
     PromptPiece K;
     for (int item = blockIdx.x; find_piece<S::COLS, WINDOW>(A, split_keys, item, K); item += gridDim.x) {
         if (K.k0 >= K.k1) continue;                 // a chunk past all that the tile sees
@@ -561,16 +561,6 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
             put(st0, sc0);
             load(nullptr);
             look(2);
-        }
-        // Scores are multiplied by a positive scale: a negative one changes the
-        // queries' signs, 0 makes them 0.
-        if (A.scale <= 0.0f) {
-            const uint32_t sign = A.scale < 0.0f ? 0x80008000u : 0u, keep = A.scale < 0.0f ? ~0u : 0u;
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const uint4 x = __builtin_bit_cast(uint4, q[k]);
-                q[k] = __builtin_bit_cast(bf8v, make_uint4((x.x & keep) ^ sign, (x.y & keep) ^ sign, (x.z & keep) ^ sign, (x.w & keep) ^ sign));
-            }
         }
 #pragma unroll
         for (int k = 0; k < QL; ++k) q_lds[(wave * QL + k) * 64 + this_lane()] = __builtin_bit_cast(uint4, q[k]);
