@@ -510,18 +510,30 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
 // (the queries through registers: 32).  Loads through registers, as in attn_kernel: 70 and 37.  Three
 // workgroups a CU and a ring of one tile: 55 registers of a lane go to memory, 240 and 64.
 
-// A direct load into LDS, 16 bytes a lane, lane after lane from byte `to` on (at is
-// the wave's, off the lane's).  The compiler is not told what it is: it would wait
-// for all of a ring's loads before the first read, where the kernel waits itself
-// (the counter that its own waits go by counts these loads, too, so that they come
-// no earlier).
+// Direct loads into LDS, 16 bytes a lane, lane after lane from byte `to` on: of an
+// address that is the wave's and an offset, or of the lane's own address.  The
+// compiler is not told what they are: it would wait for all of a ring's loads before
+// the first read, where the kernel waits itself (the counter that its own waits go
+// by counts these loads, too, so that they come no earlier).  It is told that M0
+// changes, and warns that M0 is not its to give away.
 __device__ __forceinline__ uint32_t lds_at(const uint8_t *p) { return (uint32_t)(uintptr_t)(lds_void *)p; }
-__device__ __forceinline__ void load_to_lds(const uint8_t *at, uint32_t off, uint32_t to)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void load_to_lds_once(const uint8_t *at, uint32_t off, uint32_t to)
 {
     const uint64_t a = reinterpret_cast<uint64_t>(at);
     const uint64_t sa = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a);
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0 nt" ::"s"(sa), "v"(off), "s"(to) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0 nt" ::"s"(sa), "v"(off), "s"(to) : "memory", "m0");
 }
+__device__ __forceinline__ void load_to_lds_once(const uint8_t *at, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(at), "s"(to) : "memory", "m0");
+}
+__device__ __forceinline__ void load_to_lds(const void *at, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(at), "s"(to) : "memory", "m0");
+}
+#pragma clang diagnostic pop
 
 template <int D>
 struct Tile4 {
@@ -542,18 +554,16 @@ struct Tile4 {
                 const int b = i * 1024 + lane * 16, r = b / ROW, piece = b % ROW / 16 ^ swizzle(r), off = (r & 15) * ROW + piece * 16;
                 if constexpr (CODES == 1024) {              // both groups in one load: the second from the first one's address
                     const int64_t apart = (int64_t)(row1 - row0) * ROW;
-                    const uint8_t *p = pool + row0 * ROW + (r < 16 ? 0 : apart) + off;
-                    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(p), "s"(to + x * CODES) : "memory");
+                    load_to_lds_once(pool + row0 * ROW + (r < 16 ? 0 : apart) + off, to + x * CODES);
                 } else {
-                    load_to_lds(pool + (i * 1024 / ROW < 16 ? row0 : row1) * ROW, off, to + x * CODES + i * 1024);
+                    load_to_lds_once(pool + (i * 1024 / ROW < 16 ? row0 : row1) * ROW, off, to + x * CODES + i * 1024);
                 }
             }
         }
         constexpr int LE = 2 * EXPS;                        // lanes that bring a pool's exponents
         if (lane < 2 * LE) {
             const int b = lane % LE * 16;
-            const uint8_t *p = (lane < LE ? kv.k_exp : kv.v_exp) + (b < 16 * EXPS ? row0 * EXPS + b : row1 * EXPS + (b - 16 * EXPS));
-            asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(to + 2 * CODES) : "memory");
+            load_to_lds((lane < LE ? kv.k_exp : kv.v_exp) + (b < 16 * EXPS ? row0 * EXPS + b : row1 * EXPS + (b - 16 * EXPS)), to + 2 * CODES);
         }
     }
     // steps of the product S^T = K Q^T: step s has 8 channels from channel(s, g) on
@@ -680,8 +690,7 @@ __global__ __launch_bounds__(kThreads4, 2) void attn4_kernel(const AttnArgs A)
     for (int s = 0; s < S::STEPS; ++s) {
         if (s % kWaves4 != wave) continue;
         const int col = col0 + min(n, ncol - 1);
-        const uint16_t *p = A.q + ((size_t)col_row(A, K, col) * A.hq + col_head(A, K, col)) * D + S::channel(s, g);
-        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(q_at + s * 1024) : "memory");
+        load_to_lds(A.q + ((size_t)col_row(A, K, col) * A.hq + col_head(A, K, col)) * D + S::channel(s, g), q_at + s * 1024);
     }
     bool ok = true;
     for (int i = (K.k0 >> A.kv.page_shift) + tid; i <= (K.k1 - 1) >> A.kv.page_shift; i += kThreads4) {
