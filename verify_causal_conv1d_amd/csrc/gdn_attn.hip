@@ -515,7 +515,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(const AttnArgs A)
 // compiler is not told what they are: it would wait for all of a ring's loads before
 // the first read, where the kernel waits itself (the counter that its own waits go
 // by counts these loads, too, so that they come no earlier).  It is told that M0
-// changes, and warns that M0 is not its to give away.
+// changes, and warns that M0 is not its to give away.  The wave's address may be
+// what a v_readfirstlane has just written: five wait states before a memory
+// instruction may read it, which the compiler does not count in front of an asm
+// block, are s_mov_b32's and s_nop 3's (M0 needs one of them).
 __device__ __forceinline__ uint32_t lds_at(const uint8_t *p) { return (uint32_t)(uintptr_t)(lds_void *)p; }
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
@@ -523,7 +526,7 @@ __device__ __forceinline__ void load_to_lds_once(const uint8_t *at, uint32_t off
 {
     const uint64_t a = reinterpret_cast<uint64_t>(at);
     const uint64_t sa = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a);
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0 nt" ::"s"(sa), "v"(off), "s"(to) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %0 nt" ::"s"(sa), "v"(off), "s"(to) : "memory", "m0");
 }
 __device__ __forceinline__ void load_to_lds_once(const uint8_t *at, uint32_t to)
 {
