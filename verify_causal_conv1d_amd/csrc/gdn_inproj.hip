@@ -60,18 +60,18 @@ __device__ __forceinline__ f4v mfma16x16x32(uint4 a, uint4 b, f4v c)
 __device__ __forceinline__ uint4 dequant8(uint32_t w, float s, float b)
 {
     // even codes in the bytes of lo, odd codes in the bytes of hi: each code
-    // then converts with one byte-to-float instruction (written out: the
-    // compiler would extract each byte first)
-    const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+    // then converts with one byte-to-float instruction (that the upper halves of
+    // the bytes are 0 is hidden from the compiler, which would extract each byte
+    // first; the instructions are its own, so that it waits where a matrix
+    // instruction may still read the registers that they write)
+    uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+    asm("" : "+v"(lo), "+v"(hi));
     float q[8], v[8];
-    asm("v_cvt_f32_ubyte0 %0, %1" : "=v"(q[0]) : "v"(lo));
-    asm("v_cvt_f32_ubyte1 %0, %1" : "=v"(q[2]) : "v"(lo));
-    asm("v_cvt_f32_ubyte2 %0, %1" : "=v"(q[4]) : "v"(lo));
-    asm("v_cvt_f32_ubyte3 %0, %1" : "=v"(q[6]) : "v"(lo));
-    asm("v_cvt_f32_ubyte0 %0, %1" : "=v"(q[1]) : "v"(hi));
-    asm("v_cvt_f32_ubyte1 %0, %1" : "=v"(q[3]) : "v"(hi));
-    asm("v_cvt_f32_ubyte2 %0, %1" : "=v"(q[5]) : "v"(hi));
-    asm("v_cvt_f32_ubyte3 %0, %1" : "=v"(q[7]) : "v"(hi));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        q[2 * j] = (float)(lo >> 8 * j & 255u);
+        q[2 * j + 1] = (float)(hi >> 8 * j & 255u);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = fmaf(s, q[j], b);
     return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
