@@ -42,13 +42,15 @@ __device__ __forceinline__ float sum_halves(float x)
     return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
-// The lane's number, worked out anew where it is needed: no register holds it
-// through the loop.
-__device__ __forceinline__ int this_lane()
+// The lane's number, worked out anew from a mask that the compiler cannot trace: no
+// register holds it through the loop.  (The instructions are the compiler's own, so
+// that it waits where a matrix instruction may still use the register that they
+// write.)
+__device__ __forceinline__ int lane_number()
 {
-    int x;
-    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(x));
-    return x;
+    uint32_t all = ~0u;
+    asm volatile("" : "+s"(all));
+    return __builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0));
 }
 
 // The kernel's arguments, loaded anew: none of them holds scalar registers through
@@ -252,6 +254,12 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 31, g = lane >> 5;
     const float scale = uniform(A.scale);
+    // Of up to 128 channels a register is left for it (e4m3 rows of 128, a resumed
+    // prompt: 1,256 us, worked out anew 1,309).
+    auto this_lane = [&] {
+        if constexpr (D < 256) return fresh(lane);
+        else return lane_number();
+    };
     PromptPiece K;
     for (int item = blockIdx.x; find_piece<S::COLS, WINDOW>(A, split_keys, item, K); item += gridDim.x) {
         if (K.k0 >= K.k1) continue;                 // a chunk past all that the tile sees
