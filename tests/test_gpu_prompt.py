@@ -395,6 +395,20 @@ def test_longest_bound():
     close(c.run()[:50], *(x[:50] for x in _some(c, 50)))
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_loose_bounds(fmt):
+    """Under bounds far above all lengths every stream has one chunk: every row within the oracle's bound, and the same bits under another such bound."""
+    for d, lens, rows, hq, hkv in ((64, [60, 7], [1400, 200], 8, 2), (256, [600, 70, 0], [30, 40, 500], 8, 2), (128, [900], [300], 6, 1),
+                                   (256, [3000], [65], 6, 1)):
+        announce(f"prompts under loose bounds, {fmt}, d {d}, {lens} {rows}")
+        c = Case(lens, rows, hq, hkv, d, 64, fmt=fmt, seed=43, gate=d == 128)
+        want, bound = c.oracle()
+        loose = c.run(max_kv=1 << 21)
+        close(loose, want, bound)
+        assert torch.equal(loose, c.run(max_kv=1 << 20))
+        close(c.run(), want, bound)
+
+
 def _some(c, rows):
     """The oracle of a case's first rows."""
     one = Case.__new__(Case)
