@@ -475,8 +475,10 @@ int gdn_attn_window(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_
  *   workspace: gdn_attn_prompt_workspace_bytes() of device memory, 16-byte
  *     aligned (NULL where that is 0); its contents need not be kept between
  *     calls, and calls that may overlap need their own.  A size serves every call
- *     with the same hq, hkv and d whose total_rows and max_kv are no larger; 0
- *     also for what is refused
+ *     with the same hq, hkv and d whose total_rows and max_kv are no larger, so it
+ *     is what the most chunks of such calls take (up to 271 MB for d 256), also
+ *     where the call itself is not cut and uses none of it; 0 also for what is
+ *     refused
  * A stream without rows has nothing to do; one that breaks a rule (its window,
  * lengths over max_kv or max_blocks, a page outside the cache) is skipped: its
  * rows of out are left as they were, and so are rows of no stream.  Scores,
@@ -485,10 +487,13 @@ int gdn_attn_window(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_
  * rounding).  A call of few rows over long streams is cut along the keys, by
  * total_rows, max_kv, the heads and the cache's format alone; given these, a
  * stream's results depend on neither the other streams nor its place in the call,
- * bit for bit.  A row takes nothing from rows that it does not see, whatever they
- * hold.  Streams of a row or two are taken, but each has tiles of 128 or 256 (row,
- * head) pairs to itself: steps belong into gdn_attn_window.
- * total_rows * hq <= 2^26 - 4.
+ * bit for bit.  So bounds far above what the streams have, as a captured pass may
+ * need them, leave long streams in few pieces or one: 512 rows over 32,000 keys (24
+ * and 4 heads of 256) take 0.38 ms under their own bounds and 1.45 under a max_kv of
+ * 262,144, with room for 8,306 rows, or beside as many fresh rows.  A row takes
+ * nothing from rows that it does not see, whatever they hold.  Streams of a row or
+ * two are taken, but each has tiles of 128 or 256 (row, head) pairs to itself: steps
+ * belong into gdn_attn_window.  total_rows * hq <= 2^26 - 4.
  */
 size_t gdn_attn_prompt_workspace_bytes(const gdn_kv_cache *cache, int32_t n_streams, int32_t total_rows,
                                        int32_t max_kv, int32_t hq);

@@ -1151,7 +1151,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(const AttnAr
 // streams' windows are looked at 64 at a time.  Of many bytes, whose time it is
 // that the kernel takes, only those that are there: of the 16 trees above the longest
 // has 17 chunks and ten have 4 to 6, and asked for by the row alone they were 58 MB and
-// 12.2 us, where the 25 MB that the chunks wrote take 7.6.
+// 12.2 us, where the 25 MB that the chunks wrote take 7.6.  Where every stream has as
+// many as are asked for, waiting saves nothing: 64 steps of 16,384 and of 8,192 keys
+// 10.9 and 11.2 us (10.2 and 9.9 at once), of calls of 740 and 440; 16 trees of 8,191
+// 17.9 and 17.0.
 constexpr int kJoinWaves = 4, kJoinBatch = 16;      // loads in flight
 constexpr long long kJoinAtOnce = 16 << 20;        // bytes
 

@@ -264,7 +264,9 @@ __device__ __forceinline__ void cos_sin_f64(double turns, double &c, double &s)
 }
 
 // cos and sin of a position's ith angle, times the rotation's scale.  The angle is
-// exact in fp64, and so, up to 2^-52 of a turn, is what whole turns leave of it.
+// exact in fp64 for positions below 2^29 (times the 24 bits of a frequency; beyond, it
+// is the product rounded to fp64), and so, up to 2^-52 of a turn, is what whole turns
+// leave of it.
 __device__ __forceinline__ void turn_f64(const PrepArgs &A, int pos, int i, double &c, double &s)
 {
     const double angle = (double)pos * (double)A.inv_freq[i], n = rint(angle * 0.15915494309189533577);
@@ -630,8 +632,9 @@ __global__ __launch_bounds__(256) void attn_commit_kernel(const AttnCommitArgs A
 // ---- cached rows read back ---------------------------------------------------
 //
 // Bounded by memory: 16 packed rows a workgroup, all their kv heads, 16 bytes of
-// bf16 a lane and step, so that every wave writes runs of 1 KB (98,000 4-bit rows of 4
-// heads of 256 in 104 us, 4.5 TB/s; 100 rows of 2 heads of 64 in 3.3).
+// bf16 a lane and step, so that every wave writes runs of 1 KB (91,000 rows of 4 heads
+// of 256: of 4 bits 474 MB in 104 us, 4.5 TB/s, of e4m3 565 MB in 110, of bf16 749 MB
+// in 128; 100 rows of 2 heads of 64 in 3.1 to 3.3).
 constexpr int kReadRows = 16, kReadThreads = 256;
 
 template <int FMT>
@@ -726,7 +729,11 @@ static void launch_prep_d(const PrepArgs &A, hipStream_t stream)
     // its lanes hold at once (on the GPU, 32 heads of 256: one row 3.7 us instead of
     // 6.8, 249 rows of 48 heads of 128 4.5 instead of 5.3; from about 500 rows on the
     // angles that every workgroup works out again cost more: 1,024 rows 12.5 us
-    // instead of 11.0, 8,306 rows 86 instead of 62)
+    // instead of 11.0, 8,306 rows 86 instead of 62).  Into a 4-bit cache the border is
+    // the same: 24 query and 4 kv heads of 256 so and with the keys in workgroups of
+    // their own 256 rows 7.1 and 9.7 us, 400 rows 9.8 and 10.6, 512 rows 11.0 and
+    // 10.9, 640 rows 12.0 and 11.3, 1,000 rows 17.3 and 14.0, 2,000 rows 30.7 and 21.7;
+    // 32 and 8 heads of 128 400 rows 8.2 and 8.9, 640 rows 11.6 and 10.7.
     const int heads = A.hq + 2 * A.kv.hkv, at_once = kPrepThreads / (D / 8);
     const int span = A.rows <= kPrepFewRows && heads > at_once ? at_once : heads;
     const dim3 grid(A.rows, (heads + span - 1) / span);

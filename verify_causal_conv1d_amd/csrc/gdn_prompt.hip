@@ -15,11 +15,13 @@
 //
 // What bounds it is the matrix unit and the vector unit beside it: of 256 channels
 // a wave's 32 keys are 32 matrix instructions and about 110 others.  16,384 rows of
-// 24 query and 4 kv heads of 256 take 2.81 ms in bf16 (1,175 TFLOP/s), 2.67 to 2.73
-// over 4-bit rows (1,207 to 1,236) and 3.13 over e4m3 rows (1,052), whose scales
-// are two more multiplications of every weight; of 32 and 8 heads of 128 1,056, 1,087 and
-// 832 TFLOP/s, of 64 876, 823 and 665, as there are half and a quarter as many products
-// to a weight.  (A product of two 8,192 x 8,192 matrices reaches 1,254 on the same card.)
+// 24 query and 4 kv heads of 256 take 2.71 ms in bf16 (1,215 TFLOP/s), 2.66 over 4-bit
+// rows (1,240) and 3.12 to 3.18 over e4m3 rows (1,037 to 1,058).  There the scales of
+// the keys take the place of the call's in the one fmaf of a score, those of the
+// values are one more multiplication of every weight, and both are read from LDS.  Of
+// 32 and 8 heads of 128 it is 1,080, 1,101 and 862 TFLOP/s, of 64 885, 839 and 693,
+// as there are half and a quarter as many products to a weight.  (A product of two
+// 8,192 x 8,192 matrices reaches 1,254 on the same card.)
 #include "gdn_attn_core.h"
 #include "gdn_mxfp4.h"
 
@@ -447,6 +449,12 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
                 for (int a = 0; a < 4; ++a) vs[a] = *reinterpret_cast<const float4 *>(scale_at + S::KEYS + 8 * a);
             __builtin_amdgcn_sched_barrier(0);
             // lane (n, g) has of column n the keys 8 a + 4 g + b (a, b < 4) of the 32
+            // (The weights go into the second product in bf16, rounded to nearest, up to
+            // 2^-8 of each term, as the bf16 result's own rounding; the sums keep the fp32
+            // values.  A second product for what that leaves, as steps have it, whose
+            // bound is memory: 2,730 rows over 16,000 keys of 256 channels in bf16 1,386
+            // us instead of 1,013, 2,048 of 128 815 instead of 623, of 64 513 instead of
+            // 392; the other formats alike.)
             bf8v pb[2];
             // Any base within reach of the maximum does: scores are taken from the one
             // that is there, and it moves, to 2^8 above the maximum, only when that has
@@ -576,7 +584,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
             // Over e4m3 rows of up to 128 channels half of the waves convert the next stage
             // before they multiply this one, the other half afterwards: while one of two
             // waves of a SIMD keeps the vector unit busy, the other has the matrix unit (a
-            // resumed prompt of 32 and 8 heads of 128 1,320 and 1,288 us; the other rows,
+            // resumed prompt of 32 and 8 heads of 128 1,284 and 1,255 us; the other rows,
             // which are converted in fewer steps, gain nothing, or lose 2 %).
             constexpr bool HALVES = FMT == FMT_E4M3 && D < 256;
             const bool late = HALVES && wave >= WAVES / 2;
@@ -707,13 +715,13 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
 
 // Waves of a workgroup, that is columns that share what is loaded and converted, and
 // waves of a SIMD, that is registers of each.  16,384 rows in 8 waves and in 4: 256
-// channels (24 query and 4 kv heads) in bf16 2,809 us and 2,974, over 4 bits 2,669 and
-// 2,858; 128 channels (32 and 8) in bf16 2,240 and 2,082, over 4 bits 2,255 and
-// 2,176, in e4m3 2,705 and 2,785, a resumed prompt 1,320 and 1,422: there what is
+// channels (24 query and 4 kv heads) in bf16 2,715 us and 2,905, over 4 bits 2,660 and
+// 2,886; 128 channels (32 and 8) in bf16 2,203 and 2,037, over 4 bits 2,119 and
+// 1,998, in e4m3 2,550 and 2,600, a resumed prompt 1,255 and 1,351: there what is
 // converted weighs most.  Of 256 channels both are here, for calls that leave some of
-// the chip empty (prompt_plan): 2,048 fresh rows in bf16 119 and 111 us, over 4 bits
-// 125 and 110, 1,024 rows 68 and 60, 64 rows 21 and 18; over cached rows, where pieces
-// are cut to fill the chip, 512 rows over 32,000 in 4 bits 414 and 455.
+// the chip empty (prompt_plan): 2,048 fresh rows in bf16 105 and 97 us, over 4 bits
+// 114 and 110, 1,024 rows 63 and 57, 64 rows 16 and 14; over cached rows, where pieces
+// are cut to fill the chip, 512 rows over 32,000 in 4 bits 386 and 442.
 constexpr int prompt_waves(int d, int fmt) { return d == 256 || (d == 128 && fmt == FMT_E4M3) ? 8 : 4; }
 constexpr bool prompt_has_both(int d, int fmt) { return d == 256 && fmt != FMT_E4M3; }        // (e4m3: queries in LDS)
 constexpr int prompt_per_simd(int d, int fmt) { return d == 64 ? (fmt == FMT_E4M3 ? 3 : 4) : d == 128 && fmt != FMT_E4M3 ? 3 : 2; }
@@ -751,10 +759,16 @@ int prompt_slots(int d, int fmt, int waves) { return 256 * 4 * prompt_per_simd(d
 // is left to end on: where the pieces are alike, since most of their keys are cached,
 // the rest of a last round (half a piece once the rounds are many), less where the
 // last ones are short.  Workgroups that have their CU to themselves are faster.  (24
-// query and 4 kv heads of 256 in bf16, 8 waves: a fresh prompt of 2,048 rows takes 114 us
-// whole and 143 in two chunks; 512 rows over 32,000 cached keys 1,492 us whole, 394 in 5
-// chunks, which are 240 pieces for the chip's 256 places, 463 in 8, 504 in 12 and
-// 452 in 16.)
+// query and 4 kv heads of 256 in bf16: a fresh prompt of 2,048 rows takes 97 us whole
+// and 130 in two chunks; 512 rows over 32,000 cached keys 1,448 us whole, 373 in 5
+// chunks, which are 240 pieces for the chip's 256 places, 570 in 6, 446 in 8, 485 in
+// 12 and 419 in 16.)
+//
+// What is known here is the call's bounds alone, so loose ones cost: those 512 rows
+// take 610 us under a max_kv of 65,536 (3 chunks), 1,177 under 131,072 (2), 1,448 under
+// 262,144 or with room for 8,306 rows (uncut), and beside 8,306 fresh rows, which take
+// 352 by themselves, 1,462; 65 rows over 131,000 4-bit keys 256 us under their own
+// bounds, 413 under 262,144, 6,155 with room for 8,306 rows.
 constexpr int kPromptRounds = 4;           // pieces of a call that is cut, in workgroups that the chip holds
 int most_chunks(int max_kv) { return at_most(kMaxChunks, max_kv / 256); }
 
