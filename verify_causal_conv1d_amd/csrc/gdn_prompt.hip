@@ -15,13 +15,14 @@
 //
 // What bounds it is the matrix unit and the vector unit beside it: of 256 channels
 // a wave's 32 keys are 32 matrix instructions and about 110 others.  16,384 rows of
-// 24 query and 4 kv heads of 256 take 2.71 ms in bf16 (1,215 TFLOP/s), 2.66 over 4-bit
-// rows (1,240) and 3.12 to 3.18 over e4m3 rows (1,037 to 1,058).  There the scales of
-// the keys take the place of the call's in the one fmaf of a score, those of the
-// values are one more multiplication of every weight, and both are read from LDS.  Of
-// 32 and 8 heads of 128 it is 1,080, 1,101 and 862 TFLOP/s, of 64 885, 839 and 693,
-// as there are half and a quarter as many products to a weight.  (A product of two
-// 8,192 x 8,192 matrices reaches 1,254 on the same card.)
+// 24 query and 4 kv heads of 256 take 2.71 to 2.84 ms in bf16, from card to card
+// (1,160 to 1,215 TFLOP/s), 2.66 to 2.77 over 4-bit rows (1,189 to 1,240) and 3.12 to
+// 3.22 over e4m3 rows (1,024 to 1,058).  There the scales of the keys take the place of
+// the call's in the one fmaf of a score, those of the values are one more
+// multiplication of every weight, and both are read from LDS.  Of 32 and 8 heads of
+// 128 it is 1,025 to 1,080, 1,058 to 1,101 and 856 to 862 TFLOP/s, of 64 848 to 885,
+// 807 to 839 and 669 to 693, as there are half and a quarter as many products to a
+// weight.  (A product of two 8,192 x 8,192 matrices reaches 1,254.)
 #include "gdn_attn_core.h"
 #include "gdn_mxfp4.h"
 
@@ -243,8 +244,9 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
     constexpr int PER = 2 * S::HALF / 1024 / WAVES;     // direct loads of a wave
     // Operands of the queries that stay in LDS: with all of them in registers the
     // first three of e4m3 rows of 256 channels went to memory, and reading them back
-    // waited for the rows on their way.
-    constexpr int QL = FMT == FMT_E4M3 && D == 256 ? 4 : 0;
+    // waited for the rows on their way; so did the first of 4-bit rows in workgroups
+    // of 4 waves (2,048 rows 114 us, with it in LDS 105).
+    constexpr int QL = D < 256 || WINDOW ? 0 : FMT == FMT_E4M3 ? 4 : FMT == FMT_MXFP4 && WAVES == 4 ? 1 : 0;
     __shared__ __align__(16) uint4 q_lds[QL ? WAVES * QL * 64 : 1];
     // separate arrays, so that loads into one are known not to touch the other
     __shared__ __align__(1024) uint8_t st0[S::BYTES], st1[S::BYTES];
@@ -720,7 +722,7 @@ __global__ __launch_bounds__(64 * WAVES, PER_SIMD) void prompt_kernel(const Attn
 // 1,998, in e4m3 2,550 and 2,600, a resumed prompt 1,255 and 1,351: there what is
 // converted weighs most.  Of 256 channels both are here, for calls that leave some of
 // the chip empty (prompt_plan): 2,048 fresh rows in bf16 105 and 97 us, over 4 bits
-// 114 and 110, 1,024 rows 63 and 57, 64 rows 16 and 14; over cached rows, where pieces
+// 114 and 105, 1,024 rows 63 and 54, 64 rows 16 and 14; over cached rows, where pieces
 // are cut to fill the chip, 512 rows over 32,000 in 4 bits 386 and 442.
 constexpr int prompt_waves(int d, int fmt) { return d == 256 || (d == 128 && fmt == FMT_E4M3) ? 8 : 4; }
 constexpr bool prompt_has_both(int d, int fmt) { return d == 256 && fmt != FMT_E4M3; }        // (e4m3: queries in LDS)
