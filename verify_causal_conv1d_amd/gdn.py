@@ -530,6 +530,8 @@ def attn_prompt(row_start, kv_len, block_table, q, k_cache, v_cache, out, worksp
                 v_scale=None, scale=None):
     """Causal attention of packed prompts of any lengths over the cache, which holds
     this pass's rows already: row t of stream s sees cache rows up to kv_len[s] + t.
+    ``max_kv`` bounds every stream's cached rows and rows; long streams are cut by it
+    and by the number of packed rows, so that bounds far above them cost time.
     ``scale`` of the scores d ** -0.5 unless given, ``gate`` (bf16 [R][hq][d], may
     be a view) applied as sigmoid(gate)."""
     dev = _on(q, "q")
